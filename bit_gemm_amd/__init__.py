@@ -11,6 +11,9 @@ Entry points mirror the C ABI in ``include/nvfp4.h``:
 * ``quantize_fos(w, amax=None)`` -> :class:`NVFP4Weight`
 * ``dequant(q, dtype=torch.float32)``
 * ``w4a16_gemm(x, q, out_dtype=torch.bfloat16)``
+* ``quantize_mx(x, fmt=MXFP4)`` -> :class:`MXTensor`, ``dequant_mx(q)``
+* ``mx_gemm(a, w)``, ``mx_gemm_dx(dy, w)``
+* ``add_rmsnorm_mx(x, weight, residual=None)``, ``add_rmsnorm_backward(...)``
 * ``selftest_cvt()``
 """
 
@@ -37,6 +40,7 @@ STATUS_NAMES = {
     6: "NVFP4_ERR_UNSUPPORTED_DEVICE",
 }
 BF16, F32 = 0, 1
+MXFP4, MXFP8 = 0, 1
 PATH_AUTO, PATH_SKINNY, PATH_TILED = 0, 1, 2
 IMPL_DEFAULT, IMPL_PORTABLE, IMPL_HWCVT = 0, 1, 2
 
@@ -70,6 +74,18 @@ SIGNATURES = {
     "nvfp4_quantize_act": (_c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
     "nvfp4_w4a4_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
     "nvfp4_w4a4_gemm": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_size, _c_p]),
+    "nvfp4_mx_quantize": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
+    "nvfp4_mx_dequant": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_int, _c_int, _c_p]),
+    "nvfp4_mx_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "nvfp4_mx_gemm": (_c_int, [_c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_size,
+                               _c_p]),
+    "nvfp4_mx_gemm_dx_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "nvfp4_mx_gemm_dx": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_size, _c_p]),
+    "nvfp4_add_rmsnorm_mx": (_c_int, [_c_p, _c_p, _c_p, _c_int, ctypes.c_float, _c_i64, _c_i64, _c_int, _c_p, _c_p,
+                                      _c_p, _c_p, _c_p]),
+    "nvfp4_add_rmsnorm_backward_workspace_size": (_c_size, [_c_i64, _c_i64]),
+    "nvfp4_add_rmsnorm_backward": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p,
+                                            _c_size, _c_p]),
     "nvfp4_selftest_cvt": (_c_int, [_c_p, _c_p]),
     "nvfp4_stream_read": (_c_int, [_c_p, _c_size, _c_int, _c_int, _c_int, _c_p, _c_p]),
     "nvfp4_w4a16_gemm_noalloc": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p]),
@@ -562,6 +578,248 @@ def w4a4_gemm(x: torch.Tensor, q: NVFP4Weight, out_dtype: torch.dtype = torch.bf
     _check(lib().nvfp4_w4a4_gemm(_ptr(x), _ptr(q.codes), _ptr(q.scales), _ptr(q.tensor_scale), _ptr(out), m, n, k,
                                  code, _ptr(workspace), workspace.numel(), _stream(dev)))
     return out
+
+
+_OUT_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _need_all(dev, parts):
+    """_need over (tensor, name, dtype, shape) parts, None tensors skipped:
+    every type and shape first, then GPU residence on device dev."""
+    for t, name, dtype, shape in parts:
+        if t is not None:
+            _need(t, name, dtype, shape, gpu=False)
+    for t, name, _, _ in parts:
+        if t is not None:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor")
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, the other arguments on {dev}")
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev as the current
+    device (the library launches on the current one)."""
+    if torch.cuda.current_device() == dev.index:
+        return _check(fn(*args, _stream(dev)))
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(dev)))
+
+
+def _out_code(dtype, name="out_dtype"):
+    code = _OUT_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return code
+
+
+def _mx_workspace(workspace, need, dev):
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, None, dev)  # its size: checked by the library
+    elif need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, 0 if workspace is None else workspace.numel()
+
+
+@dataclass
+class MXTensor:
+    """Microscaled [m, k] matrix (see include/nvfp4.h): one power-of-two scale
+    per 32 elements of a row."""
+
+    codes: torch.Tensor  # uint8 [m, k/2] (MXFP4) or [m, k] (MXFP8)
+    scales: torch.Tensor  # uint8 [m, k/32]
+    fmt: int  # MXFP4 or MXFP8
+
+    @property
+    def shape(self):
+        return (self.codes.shape[0], self.codes.shape[1] * (2 if self.fmt == MXFP4 else 1))
+
+    def parts(self, name: str = ""):
+        """The (tensor, name, dtype, shape) pieces of a consistent matrix;
+        raises ValueError if its sizes are not those of one."""
+        if self.fmt != MXFP4 and self.fmt != MXFP8:
+            raise ValueError(f"{name}fmt must be MXFP4 or MXFP8, got {self.fmt}")
+        if not isinstance(self.codes, torch.Tensor) or self.codes.dim() != 2:
+            raise ValueError(f"{name}codes must be a 2-D uint8 tensor")
+        m, k = self.shape
+        if k % 32 != 0:
+            raise ValueError(f"{name}codes imply k={k}, not a multiple of 32")
+        return [(self.codes, name + "codes", torch.uint8, None), (self.scales, name + "scales", torch.uint8, (m, k // 32))]
+
+    @staticmethod
+    def empty(m: int, k: int, fmt: int, device) -> "MXTensor":
+        """An uninitialised [m, k] matrix (k a multiple of 32)."""
+        if fmt != MXFP4 and fmt != MXFP8:
+            raise ValueError(f"fmt must be MXFP4 or MXFP8, got {fmt}")
+        if k % 32 != 0:
+            raise ValueError(f"k={k} is not a multiple of 32")
+        return MXTensor(torch.empty((m, k // 2 if fmt == MXFP4 else k), dtype=torch.uint8, device=device),
+                        torch.empty((m, k // 32), dtype=torch.uint8, device=device), fmt)
+
+
+def _mx_out(out, m, k, fmt, dev):
+    """(out or a new MXTensor, its parts), for an operator that writes an [m, k] matrix in format fmt."""
+    if out is None:
+        return MXTensor.empty(m, k, fmt, dev), []
+    if not isinstance(out, MXTensor):
+        raise ValueError("out must be an MXTensor")
+    parts = out.parts("out.")
+    if out.fmt != fmt or out.shape != (m, k):
+        raise ValueError(f"out holds a {out.shape} matrix in format {out.fmt}, the result is {(m, k)} in format {fmt}")
+    return out, parts
+
+
+def quantize_mx(x: torch.Tensor, fmt: int = MXFP4, out: Optional[MXTensor] = None) -> MXTensor:
+    """Microscaled quantization of a bfloat16 or float32 [m, k] GPU matrix."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    code = _out_code(x.dtype, "x's dtype")
+    m, k = x.shape
+    dev = x.device
+    if out is None:  # checked before anything is allocated
+        _need_all(dev, [(x, "x", x.dtype, None)])
+    out, parts = _mx_out(out, m, k, fmt, dev)
+    if parts:
+        _need_all(dev, [(x, "x", x.dtype, None)] + parts)
+    _call(dev, lib().nvfp4_mx_quantize, x.data_ptr(), code, m, k, fmt, out.codes.data_ptr(), out.scales.data_ptr())
+    return out
+
+
+def dequant_mx(q: MXTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of an MX matrix, as float32 or bfloat16."""
+    parts = q.parts()
+    m, k = q.shape
+    code = _out_code(dtype, "dtype")
+    dev = q.codes.device
+    _need_all(dev, parts + [(out, "out", dtype, (m, k))])
+    if out is None:
+        out = torch.empty((m, k), dtype=dtype, device=dev)
+    _call(dev, lib().nvfp4_mx_dequant, q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), m, k, q.fmt, code)
+    return out
+
+
+def mx_gemm_workspace_size(m: int, n: int, k: int, a_fmt: int) -> int:
+    return int(lib().nvfp4_mx_gemm_workspace_size(m, n, k, a_fmt))
+
+
+def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+            workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[m, n] = a[m, k] @ w[n, k]^T for MXFP4 or MXFP8 a and MXFP4 w."""
+    parts = a.parts("a.") + w.parts("w.")
+    m, k = a.shape
+    n, kw = w.shape
+    if w.fmt != MXFP4:
+        raise ValueError("w must be in MXFP4")
+    if kw != k:
+        raise ValueError(f"a has k={k}, w k={kw}")
+    code = _out_code(out_dtype)
+    dev = w.codes.device
+    parts.append((out, "out", out_dtype, (m, n)))
+    _need_all(dev, parts)
+    L = lib()
+    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_mx_gemm_workspace_size(m, n, k, a.fmt), dev)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    _call(dev, L.nvfp4_mx_gemm, a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, w.codes.data_ptr(),
+          w.scales.data_ptr(), out.data_ptr(), m, n, k, code, _ptr(workspace), ws_bytes)
+    return out
+
+
+def mx_gemm_dx_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().nvfp4_mx_gemm_dx_workspace_size(m, n, k))
+
+
+def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx = dy @ w for bf16 [m, n] dy and MXFP4 w [n, k]: mx_gemm's gradient
+    with respect to its activations, straight through their quantization."""
+    parts = w.parts("w.")
+    n, k = w.shape
+    if w.fmt != MXFP4:
+        raise ValueError("w must be in MXFP4")
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2 or dy.shape[1] != n:
+        raise ValueError(f"dy must be [m, {n}], got {tuple(getattr(dy, 'shape', ()))}")
+    m = dy.shape[0]
+    code = _out_code(out_dtype)
+    dev = w.codes.device
+    _need_all(dev, [(dy, "dy", torch.bfloat16, None)] + parts + [(out, "out", out_dtype, (m, k))])
+    L = lib()
+    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_mx_gemm_dx_workspace_size(m, n, k), dev)
+    if out is None:
+        out = torch.empty((m, k), dtype=out_dtype, device=dev)
+    _call(dev, L.nvfp4_mx_gemm_dx, dy.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), m, n, k,
+          code, _ptr(workspace), ws_bytes)
+    return out
+
+
+def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                   fmt: int = MXFP8, out: Optional[MXTensor] = None, residual_out: Optional[torch.Tensor] = None,
+                   rstd: Optional[torch.Tensor] = None):
+    """Residual addition, root mean square norm and microscaled quantization
+    of bf16 [m, k] x, with a bf16 or float32 [k] weight.
+
+    Returns (h, s, rstd): the quantized norm as an MXTensor, the new residual
+    stream s = bf16(x + residual) (x itself without a residual) and the
+    float32 [m] factors that add_rmsnorm_backward takes.  residual_out may be
+    residual or x."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError("x must be a 2-D tensor")
+    m, k = x.shape
+    dev = x.device
+    if not isinstance(weight, torch.Tensor):
+        raise ValueError("weight must be a torch.Tensor")
+    wcode = _out_code(weight.dtype, "weight's dtype")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without a residual: the residual stream is x itself")
+    parts = [(x, "x", torch.bfloat16, None), (weight, "weight", weight.dtype, (k,)),
+             (residual, "residual", torch.bfloat16, (m, k)), (residual_out, "residual_out", torch.bfloat16, (m, k)),
+             (rstd, "rstd", torch.float32, (m,))]
+    if out is not None:
+        parts += _mx_out(out, m, k, fmt, dev)[1]
+    _need_all(dev, parts)
+    if out is None:
+        out = MXTensor.empty(m, k, fmt, dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if rstd is None:
+        rstd = torch.empty(m, dtype=torch.float32, device=dev)
+    _call(dev, lib().nvfp4_add_rmsnorm_mx, x.data_ptr(), _ptr(residual), weight.data_ptr(), wcode, eps, m, k, fmt,
+          _ptr(residual_out), rstd.data_ptr(), out.codes.data_ptr(), out.scales.data_ptr())
+    return out, x if residual is None else residual_out, rstd
+
+
+def add_rmsnorm_backward_workspace_size(m: int, k: int) -> int:
+    return int(lib().nvfp4_add_rmsnorm_backward_workspace_size(m, k))
+
+
+def add_rmsnorm_backward(dh: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                         ds: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                         dweight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Gradient of add_rmsnorm_mx, straight through its quantization: from dh
+    (bf16 [m, k], the gradient of the norm's output), the forward's s and
+    rstd, and ds (the gradient that reaches s by the residual branch, or
+    None), returns (dx, dweight): bf16 [m, k], the gradient of x and of the
+    residual, and float32 [k].  dx may be ds."""
+    if not isinstance(s, torch.Tensor) or s.dim() != 2:
+        raise ValueError("s must be a 2-D tensor")
+    m, k = s.shape
+    dev = s.device
+    if not isinstance(weight, torch.Tensor):
+        raise ValueError("weight must be a torch.Tensor")
+    wcode = _out_code(weight.dtype, "weight's dtype")
+    _need_all(dev, [(dh, "dh", torch.bfloat16, (m, k)), (s, "s", torch.bfloat16, None),
+                    (weight, "weight", weight.dtype, (k,)), (rstd, "rstd", torch.float32, (m,)),
+                    (ds, "ds", torch.bfloat16, (m, k)), (dx, "dx", torch.bfloat16, (m, k)),
+                    (dweight, "dweight", torch.float32, (k,))])
+    L = lib()
+    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_add_rmsnorm_backward_workspace_size(m, k), dev)
+    if dx is None:
+        dx = torch.empty_like(s)
+    if dweight is None:
+        dweight = torch.empty(k, dtype=torch.float32, device=dev)
+    _call(dev, L.nvfp4_add_rmsnorm_backward, dh.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, rstd.data_ptr(),
+          _ptr(ds), dx.data_ptr(), dweight.data_ptr(), m, k, _ptr(workspace), ws_bytes)
+    return dx, dweight
 
 
 def selftest_cvt(device=None) -> list:

@@ -160,6 +160,39 @@ size_t hessian_workspace_bytes(int64_t s, int64_t k);
 hipError_t launch_hessian(const uint16_t* x, int64_t s, int64_t k, float damp, float* h, void* workspace,
                           hipStream_t stream);
 
+// Microscaled formats (mx_device.h; fmt: 0 = MXFP4, 1 = MXFP8).
+hipError_t launch_mx_quantize(const void* x, int x_f32, int64_t m, int64_t k, int fmt, uint8_t* codes,
+                              uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, void* out, int64_t m, int64_t k, int fmt,
+                             int out_f32, hipStream_t stream);
+
+// y[m, n] = a[m, k] . w[n, k]^T, a in MXFP4 or MXFP8, w in MXFP4.
+struct MxPlan {
+  size_t ws_bytes;
+};
+MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt);
+hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a_fmt, const uint8_t* w_codes,
+                          const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
+                          const MxPlan& plan, void* workspace, hipStream_t stream);
+
+// dx[m, k] = dy[m, n] . w[n, k], w in MXFP4 (the plan of launch_gemm_dx).
+hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
+                             int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace, hipStream_t stream);
+
+// y = the sum of `splits` fp32 planes [splits, mn] in plane order, rounded
+// to the output type.
+hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits, int out_f32, hipStream_t stream);
+
+// Residual addition + RMS norm with MX output, and its gradient (workspace:
+// rmsnorm_backward_planes(m) fp32 rows of k).
+hipError_t launch_add_rmsnorm_mx(const void* x, const void* residual, const void* weight, int w_f32, double eps,
+                                 int64_t m, int64_t k, int fmt, void* residual_out, float* rstd, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream);
+int rmsnorm_backward_planes(int64_t m);
+hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd,
+                                   const void* ds, void* dx, float* dweight, int64_t m, int64_t k, void* workspace,
+                                   hipStream_t stream);
+
 // Thread-local error text and status codes of the C ABI (api.cpp), for
 // entry points defined in other sources.
 void clear_error();

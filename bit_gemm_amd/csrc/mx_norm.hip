@@ -1,0 +1,310 @@
+// Residual addition + root mean square norm with microscaled output, and the
+// norm's gradient, for gfx950.
+//
+// Forward, per row of k elements:
+//   s = bf16(x + residual)              (the new residual stream; s = x without one)
+//   rstd = fl32(1 / sqrt(mean(s^2) + eps))
+//   h_i = fl32(fl32(s_i rstd) weight_i)
+//   MX codes and scales of h            (mx_device.h; blocks of 32 along the row)
+// The mean is summed and the root taken in fp64: its error (about 2^-50) is
+// below fp32's last bit but for one row in millions, so rstd, and with it
+// every code, does not depend on how a row is cut over lanes.  The fp64 adds
+// run beside the memory traffic that bounds the kernel.
+//
+// Backward, with xhat_i = s_i rstd and g_i = dh_i weight_i (the gradient
+// passes straight through the MX rounding, and through bf16's):
+//   dx_i = rstd (g_i - xhat_i mean(g xhat)) + ds_i
+//   dweight_i = sum over rows of dh_i xhat_i
+// in fp32; dx is the gradient of x and of the residual alike.
+#include "launchers.h"
+#include "mx_device.h"
+
+#pragma clang fp contract(off)
+
+namespace nvfp4 {
+namespace {
+
+// 1 / sqrt(v) in fp64: the hardware estimate and two Newton steps
+// (relative error about 1.5 e^2 each: 2^-26 -> 2^-51, then rounding only);
+// 0, infinity and NaN as the estimate has them.
+__device__ __forceinline__ double rsqrt64(double v) {
+  const double e = __builtin_amdgcn_rsq(v);
+  double y = e;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = y * __builtin_fma(-0.5 * v * y, y, 1.5);
+  return v > 0.0 && v < __builtin_inf() ? y : e;
+}
+
+// Sum over the T threads of a row (T a multiple of 64), the same value in
+// every thread; part: T / 64 entries of LDS that no one else uses before the
+// next barrier but one.
+template <int T, typename F>
+__device__ __forceinline__ F row_sum(F v, F* part) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  if constexpr (T > 64) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) v += part[i];
+  }
+  return v;
+}
+
+template <bool WF32>
+__device__ __forceinline__ void load_weight8(const void* weight, int p, float (&w)[8]) {
+  if constexpr (WF32) {
+    const f32x4_t* q = static_cast<const f32x4_t*>(weight) + 2 * p;
+    const f32x4_t a = q[0], b = q[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = a[i], w[4 + i] = b[i];
+  } else {
+    const u32x4_t q = static_cast<const u32x4_t*>(weight)[p];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[2 * i] = bf16_lo(q[i]), w[2 * i + 1] = bf16_hi(q[i]);
+  }
+}
+
+// T threads per row, up to P pieces of 8 elements per thread, piece
+// t + T i; a block of 32 is a quad of lanes.
+template <int T, int P, int FMT, bool WF32>
+__global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_rmsnorm_mx(
+    const u32x4_t* x, const u32x4_t* residual, const void* __restrict__ weight, double eps, int64_t m, int k,
+    u32x4_t* residual_out, float* __restrict__ rstd_out, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  __shared__ double part[T / 64];
+  constexpr int R = T < 256 ? 256 / T : 1;  // rows per workgroup (one wave each, no LDS)
+  const int t = threadIdx.x % T;
+  const int64_t row = (int64_t)blockIdx.x * R + threadIdx.x / T;
+  if (R > 1 && row >= m) return;
+  const int np = k / 8;
+  const int64_t r0 = row * np;
+  u32x4_t s[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = t + T * i;
+    s[i] = u32x4_t{0, 0, 0, 0};
+    if (p < np) {
+      s[i] = x[r0 + p];
+      if (residual) {
+        const u32x4_t r = residual[r0 + p];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[i][j] = pack_bf16(bf16_lo(s[i][j]) + bf16_lo(r[j]), bf16_hi(s[i][j]) + bf16_hi(r[j]));
+      }
+    }
+  }
+  if (residual) {
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (t + T * i < np) residual_out[r0 + t + T * i] = s[i];
+  }
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const double a = bf16_lo(s[i][j]), b = bf16_hi(s[i][j]);
+      sum = __builtin_fma(a, a, sum);
+      sum = __builtin_fma(b, b, sum);
+    }
+  }
+  sum = row_sum<T>(sum, part);
+  const float rstd = (float)rsqrt64(sum / (double)k + eps);
+  if (t == 0 && rstd_out) rstd_out[row] = rstd;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = t + T * i;
+    float h[8];
+    uint32_t a = 0;
+    if (p < np) {
+      float w[8];
+      load_weight8<WF32>(weight, p, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[2 * j] = (bf16_lo(s[i][j]) * rstd) * w[2 * j];
+        h[2 * j + 1] = (bf16_hi(s[i][j]) * rstd) * w[2 * j + 1];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(h[j]) & 0x7FFFFFFFu);
+    }
+    a = quad_max(a);  // np is a multiple of 4: quads are whole
+    if (p < np) {
+      const uint32_t byte = mx_scale_byte<FMT>(a);
+      const float inv = mx_inv_scale(byte);
+      const uint32_t keep = byte == 255u ? 0u : 0xFFFFFFFFu;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] *= inv;
+      if constexpr (FMT == kMxFp8)
+        reinterpret_cast<u32x2_t*>(codes)[r0 + p] =
+            u32x2_t{e4m3_pack4(h[0], h[1], h[2], h[3]) & keep, e4m3_pack4(h[4], h[5], h[6], h[7]) & keep};
+      else
+        reinterpret_cast<uint32_t*>(codes)[r0 + p] =
+            e2m1_pack8_hw(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7]) & keep;
+      if ((t & 3) == 0) scales[(r0 + p) / 4] = (uint8_t)byte;
+    }
+  }
+}
+
+// A workgroup of T threads walks rows blockIdx.x, + gridDim.x, ..., keeping
+// its share of dweight in registers; plane blockIdx.x of `planes` receives it.
+template <int T, int P, bool WF32>
+__global__ __launch_bounds__(T) void k_rmsnorm_backward(const u32x4_t* __restrict__ dh, const u32x4_t* __restrict__ s,
+                                                        const void* __restrict__ weight,
+                                                        const float* __restrict__ rstd, const u32x4_t* ds,
+                                                        u32x4_t* dx, float* __restrict__ planes, int64_t m, int k) {
+  __shared__ float part[2][T / 64];
+  const int t = threadIdx.x;
+  const int np = k / 8;
+  float w[P][8], dw[P][8];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
+    if (t + T * i < np) load_weight8<WF32>(weight, t + T * i, w[i]);
+  }
+  int parity = 0;
+  for (int64_t row = blockIdx.x; row < m; row += gridDim.x, parity ^= 1) {
+    const int64_t r0 = row * np;
+    const float rs = rstd[row];
+    u32x4_t a[P], b[P], d[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = t + T * i;
+      a[i] = b[i] = d[i] = u32x4_t{0, 0, 0, 0};
+      if (p < np) {
+        a[i] = dh[r0 + p];
+        b[i] = s[r0 + p];
+        if (ds) d[i] = ds[r0 + p];
+      }
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float gh = j & 1 ? bf16_hi(a[i][j / 2]) : bf16_lo(a[i][j / 2]);
+        const float xh = (j & 1 ? bf16_hi(b[i][j / 2]) : bf16_lo(b[i][j / 2])) * rs;
+        dot = __builtin_fmaf(gh * w[i][j], xh, dot);
+        dw[i][j] = __builtin_fmaf(gh, xh, dw[i][j]);
+      }
+    }
+    const float c = row_sum<T>(dot, part[parity]) / (float)k;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = t + T * i;
+      if (p >= np) continue;
+      u32x4_t o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float gh = e ? bf16_hi(a[i][j]) : bf16_lo(a[i][j]);
+          const float xh = (e ? bf16_hi(b[i][j]) : bf16_lo(b[i][j])) * rs;
+          v[e] = rs * __builtin_fmaf(-xh, c, gh * w[i][2 * j + e]);
+          if (ds) v[e] += e ? bf16_hi(d[i][j]) : bf16_lo(d[i][j]);
+        }
+        o[j] = pack_bf16(v[0], v[1]);
+      }
+      dx[r0 + p] = o;
+    }
+  }
+  float* plane = planes + (int64_t)blockIdx.x * k;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = t + T * i;
+    if (p >= np) continue;
+    f32x4_t* q = reinterpret_cast<f32x4_t*>(plane) + 2 * p;
+    q[0] = f32x4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+    q[1] = f32x4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// dweight = sum of the planes [count, k]: 32 columns per workgroup (8 lanes
+// of 4), the planes cut over 32 slices, summed in a fixed order.
+__global__ __launch_bounds__(256) void k_dweight_sum(const float* __restrict__ planes, float* __restrict__ dweight,
+                                                     int count, int k) {
+  __shared__ f32x4_t part[32][8];
+  const int c = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const f32x4_t* p = reinterpret_cast<const f32x4_t*>(planes) + (int64_t)blockIdx.x * 8 + c;
+  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int g = slice; g < count; g += 32) v += p[(int64_t)g * (k / 4)];
+  part[slice][c] = v;
+  __syncthreads();
+  if (slice == 0) {
+    for (int i = 1; i < 32; ++i) v += part[i][c];
+    reinterpret_cast<f32x4_t*>(dweight)[blockIdx.x * 8 + c] = v;
+  }
+}
+
+constexpr int kMaxPlanes = 512;  // two workgroups per CU
+
+template <int T, int P>
+void norm_rows(const void* x, const void* residual, const void* weight, int w_f32, double eps, int64_t m, int k,
+               int fmt, void* residual_out, float* rstd, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
+  constexpr int R = T < 256 ? 256 / T : 1;
+  const dim3 grid((unsigned)((m + R - 1) / R)), block(T < 256 ? 256 : T);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, block, 0, stream, static_cast<const u32x4_t*>(x),
+                       static_cast<const u32x4_t*>(residual), weight, eps, m, k, static_cast<u32x4_t*>(residual_out),
+                       rstd, codes, scales);
+  };
+  if (fmt == kMxFp4)
+    w_f32 ? go(k_add_rmsnorm_mx<T, P, kMxFp4, true>) : go(k_add_rmsnorm_mx<T, P, kMxFp4, false>);
+  else
+    w_f32 ? go(k_add_rmsnorm_mx<T, P, kMxFp8, true>) : go(k_add_rmsnorm_mx<T, P, kMxFp8, false>);
+}
+
+template <int T, int P>
+void backward_rows(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd, const void* ds,
+                   void* dx, float* planes, int count, int64_t m, int k, hipStream_t stream) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(T), 0, stream, static_cast<const u32x4_t*>(dh),
+                       static_cast<const u32x4_t*>(s), weight, rstd, static_cast<const u32x4_t*>(ds),
+                       static_cast<u32x4_t*>(dx), planes, m, k);
+  };
+  w_f32 ? go(k_rmsnorm_backward<T, P, true>) : go(k_rmsnorm_backward<T, P, false>);
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm_mx(const void* x, const void* residual, const void* weight, int w_f32, double eps,
+                                 int64_t m, int64_t k, int fmt, void* residual_out, float* rstd, uint8_t* codes,
+                                 uint8_t* scales, hipStream_t stream) {
+  const int kk = (int)k;
+  auto call = [&](auto f) { f(x, residual, weight, w_f32, eps, m, kk, fmt, residual_out, rstd, codes, scales, stream); };
+  if (k <= 512) call(norm_rows<64, 1>);
+  else if (k <= 2048) call(norm_rows<256, 1>);
+  else if (k <= 4096) call(norm_rows<256, 2>);
+  else if (k <= 8192) call(norm_rows<256, 4>);
+  else if (k <= 16384) call(norm_rows<512, 4>);
+  else if (k <= 32768) call(norm_rows<1024, 4>);
+  else call(norm_rows<1024, 8>);
+  return hipGetLastError();
+}
+
+int rmsnorm_backward_planes(int64_t m) { return (int)(m < kMaxPlanes ? m : kMaxPlanes); }
+
+hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd,
+                                   const void* ds, void* dx, float* dweight, int64_t m, int64_t k, void* workspace,
+                                   hipStream_t stream) {
+  const int kk = (int)k, count = rmsnorm_backward_planes(m);
+  float* planes = static_cast<float*>(workspace);
+  auto call = [&](auto f) { f(dh, s, weight, w_f32, rstd, ds, dx, planes, count, m, kk, stream); };
+  if (count > 0) {
+    if (k <= 512) call(backward_rows<64, 1>);
+    else if (k <= 2048) call(backward_rows<256, 1>);
+    else if (k <= 4096) call(backward_rows<256, 2>);
+    else if (k <= 8192) call(backward_rows<256, 4>);
+    else if (k <= 16384) call(backward_rows<512, 4>);
+    else if (k <= 32768) call(backward_rows<1024, 4>);
+    else call(backward_rows<1024, 8>);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(k_dweight_sum, dim3((unsigned)(k / 32)), dim3(256), 0, stream, planes, dweight, count, kk);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

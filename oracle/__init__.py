@@ -37,6 +37,8 @@ w4a4    Activation quantization to NVFP4 (standard M=6 block scale) and the
 qat     Quantization-aware training of a linear layer: forward on the FP4
         weights, input gradient through the same weights, STE weight
         gradient.
+mx      Microscaled formats (power-of-two scale per 32), and the residual +
+        RMS norm with its gradient that feeds the product on them.
 
 Parity status: every function here is pinned by ``-m "not gpu"`` tests against
 something other than itself (the pages' printed value set, torch's
@@ -58,3 +60,4 @@ from .gemm import dequant, dequant_f64, gemm_ref  # noqa: F401
 from .gptq import gptq_fos, gptq_fos_obs, hessian, hessian_factor  # noqa: F401
 from .w4a4 import ActResult, act_blockscaled, quantize_act, w4a4_gemm_ref  # noqa: F401
 from .qat import qat_forward, qat_input_grad, qat_weight_grad  # noqa: F401
+from . import mx  # noqa: F401

@@ -1,0 +1,140 @@
+"""Refusals of the microscaled operators: by the library on the host, before
+any HIP call, and by the Python binding before the library is reached."""
+
+import os
+
+import pytest
+import torch
+
+import bit_gemm_amd as nv
+
+FAKE, ODD = 0x10000, 0x10008  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(nv.LIB_PATH):
+        from bit_gemm_amd import build
+        build.build()
+    return nv.lib()
+
+
+def test_quantize_and_dequant(L):
+    q = L.nvfp4_mx_quantize
+    assert q(FAKE, 0, 4, 48, 0, FAKE, FAKE, None) == 2  # k % 32
+    assert "multiple of 32" in L.nvfp4_last_error().decode()
+    assert q(FAKE, 0, -1, 64, 0, FAKE, FAKE, None) == 1
+    assert q(FAKE, 2, 4, 64, 0, FAKE, FAKE, None) == 1  # x type
+    assert q(FAKE, 0, 4, 64, 2, FAKE, FAKE, None) == 1  # format
+    assert q(None, 0, 4, 64, 0, FAKE, FAKE, None) == 1
+    assert q(FAKE, 0, 4, 64, 0, ODD, FAKE, None) == 3
+    assert q(FAKE, 0, 1 << 32, 64, 0, FAKE, FAKE, None) == 2  # more than one launch's work-items
+    assert q(None, 0, 0, 64, 0, None, None, None) == 0 and q(None, 1, 5, 0, 1, None, None, None) == 0
+    d = L.nvfp4_mx_dequant
+    assert d(FAKE, FAKE, FAKE, 4, 40, 0, 0, None) == 2
+    assert d(FAKE, FAKE, FAKE, 4, 64, -1, 0, None) == 1
+    assert d(FAKE, FAKE, FAKE, 4, 64, 0, 5, None) == 1
+    assert d(FAKE, None, FAKE, 4, 64, 0, 0, None) == 1
+    assert d(FAKE, ODD, FAKE, 4, 64, 0, 0, None) == 3
+    assert d(None, None, None, 0, 64, 0, 0, None) == 0
+
+
+def test_gemm(L):
+    def g(a=FAKE, s=FAKE, f=0, w=FAKE, ws=FAKE, y=FAKE, m=4, n=8, k=64, o=0, wsp=None, wsb=0):
+        return L.nvfp4_mx_gemm(a, s, f, w, ws, y, m, n, k, o, wsp, wsb, None)
+
+    assert g(k=48) == 2 and g(m=-1) == 1 and g(n=-2) == 1 and g(f=3) == 1 and g(o=2) == 1
+    assert g(y=None) == 1 and g(a=None) == 1 and g(ws=None) == 1
+    assert g(y=ODD) == 3 and g(w=ODD) == 3 and g(s=ODD) == 3
+    assert g(m=(1 << 22) + 1) == 2 and g(n=1 << 27) == 2 and g(k=1 << 31) == 2
+    assert g(m=0, a=None, y=None) == 0 and g(n=0, w=None, y=None) == 0
+    size = L.nvfp4_mx_gemm_workspace_size
+    assert size(0, 8, 64, 0) == 0 and size(4, 8, 48, 0) == 0 and size(4, 8, 64, 7) == 0 and size(4, -8, 64, 0) == 0
+
+
+def test_gemm_dx(L):
+    def g(dy=FAKE, w=FAKE, s=FAKE, dx=FAKE, m=4, n=8, k=64, o=0, wsp=None, wsb=0):
+        return L.nvfp4_mx_gemm_dx(dy, w, s, dx, m, n, k, o, wsp, wsb, None)
+
+    assert g(k=48) == 2 and g(m=-1) == 1 and g(o=2) == 1 and g(dx=None) == 1 and g(dy=None) == 1
+    assert g(dy=ODD) == 3 and g(dx=ODD) == 3 and g(m=0, dy=None, dx=None) == 0
+    need = L.nvfp4_mx_gemm_dx_workspace_size(64, 4096, 4096)
+    assert need > 0 and need % (64 * 4096 * 4) == 0
+    big = dict(m=64, n=4096, k=4096)
+    assert g(**big, wsp=FAKE, wsb=need - 1) == 4 and g(**big, wsp=None, wsb=need) == 1 and g(**big, wsp=ODD, wsb=need) == 3
+    assert L.nvfp4_mx_gemm_dx_workspace_size(64, 4096, 4080) == 0
+
+
+def test_norm(L):
+    def f(x=FAKE, r=None, w=FAKE, wt=0, eps=1e-6, m=4, k=64, fmt=1, ro=None, rs=FAKE, c=FAKE, s=FAKE):
+        return L.nvfp4_add_rmsnorm_mx(x, r, w, wt, eps, m, k, fmt, ro, rs, c, s, None)
+
+    assert f(k=48) == 2 and f(k=0) == 2 and f(k=65568) == 2 and f(m=-1) == 1 and f(m=(1 << 22) + 1) == 2
+    assert f(wt=4) == 1 and f(fmt=9) == 1 and f(eps=-1.0) == 1 and f(eps=float("nan")) == 1 and f(eps=float("inf")) == 1
+    assert f(r=FAKE) == 1 and f(ro=FAKE) == 1 and f(x=None) == 1 and f(c=None) == 1 and f(w=None) == 1
+    assert f(x=ODD) == 3 and f(w=ODD) == 3 and f(rs=FAKE + 2) == 3 and f(r=FAKE, ro=ODD) == 3
+    assert f(m=0, x=None, w=None, c=None, s=None, rs=None) == 0
+
+    def b(dh=FAKE, s=FAKE, w=FAKE, wt=0, rs=FAKE, ds=None, dx=FAKE, dw=FAKE, m=4, k=64, wsp=FAKE, wsb=1 << 30):
+        return L.nvfp4_add_rmsnorm_backward(dh, s, w, wt, rs, ds, dx, dw, m, k, wsp, wsb, None)
+
+    assert b(k=48) == 2 and b(k=0) == 2 and b(m=-1) == 1 and b(wt=2) == 1 and b(dw=None) == 1 and b(dx=None) == 1
+    assert b(rs=None) == 1 and b(dh=ODD) == 3 and b(ds=ODD) == 3 and b(dw=ODD) == 3
+    need = L.nvfp4_add_rmsnorm_backward_workspace_size(4, 64)
+    assert need >= 64 * 4 and b(wsb=need - 1) == 4 and b(wsp=None, wsb=need) == 1 and b(wsp=ODD, wsb=need) == 3
+    assert L.nvfp4_add_rmsnorm_backward_workspace_size(0, 64) == 0
+
+
+def _mx(m, k, fmt):
+    return nv.MXTensor.empty(m, k, fmt, "cpu")
+
+
+def test_binding_refuses():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU"):
+        nv.quantize_mx(x)
+    with pytest.raises(ValueError, match="2-D"):
+        nv.quantize_mx(x[0])
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        nv.quantize_mx(x.half())
+    with pytest.raises(ValueError, match="contiguous"):
+        nv.quantize_mx(x.t())
+    with pytest.raises(ValueError, match="format"):
+        nv.quantize_mx(x, nv.MXFP8, out=_mx(4, 64, nv.MXFP4))
+    with pytest.raises(ValueError, match="multiple of 32"):
+        nv.MXTensor.empty(4, 48, nv.MXFP4, "cpu")
+    with pytest.raises(ValueError, match="MXFP4 or MXFP8"):
+        nv.MXTensor.empty(4, 64, 2, "cpu")
+    with pytest.raises(ValueError, match="GPU"):
+        nv.dequant_mx(_mx(4, 64, nv.MXFP8))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        nv.dequant_mx(_mx(4, 64, nv.MXFP8), torch.float16)
+    bad = _mx(4, 64, nv.MXFP4)
+    bad.scales = bad.scales[:3]
+    with pytest.raises(ValueError, match="w.scales must have shape"):
+        nv.mx_gemm(_mx(2, 64, nv.MXFP8), bad)
+    with pytest.raises(ValueError, match="w must be in MXFP4"):
+        nv.mx_gemm(_mx(2, 64, nv.MXFP8), _mx(4, 64, nv.MXFP8))
+    with pytest.raises(ValueError, match="k=96"):
+        nv.mx_gemm(_mx(2, 96, nv.MXFP8), _mx(4, 64, nv.MXFP4))
+    with pytest.raises(ValueError, match="out must have shape"):
+        nv.mx_gemm(_mx(2, 64, nv.MXFP8), _mx(4, 64, nv.MXFP4), out=torch.zeros(2, 5, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="GPU"):
+        nv.mx_gemm(_mx(2, 64, nv.MXFP8), _mx(4, 64, nv.MXFP4))
+    with pytest.raises(ValueError, match="dy must be"):
+        nv.mx_gemm_dx(x, _mx(5, 64, nv.MXFP4))
+    with pytest.raises(ValueError, match="GPU"):
+        nv.mx_gemm_dx(x, _mx(64, 64, nv.MXFP4))
+    w = torch.ones(64)
+    with pytest.raises(ValueError, match="residual_out without"):
+        nv.add_rmsnorm_mx(x, w, residual_out=x)
+    with pytest.raises(ValueError, match="weight must have shape"):
+        nv.add_rmsnorm_mx(x, w[:32])
+    with pytest.raises(ValueError, match="residual must be torch.bfloat16"):
+        nv.add_rmsnorm_mx(x, w, residual=x.float())
+    with pytest.raises(ValueError, match="GPU"):
+        nv.add_rmsnorm_mx(x, w, residual=x)
+    with pytest.raises(ValueError, match="rstd must have shape"):
+        nv.add_rmsnorm_backward(x, x, w, torch.ones(3))
+    with pytest.raises(ValueError, match="GPU"):
+        nv.add_rmsnorm_backward(x, x, w, torch.ones(4))
