@@ -166,8 +166,14 @@ hipError_t launch_mx_quantize(const void* x, int x_f32, int64_t m, int64_t k, in
 hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, void* out, int64_t m, int64_t k, int fmt,
                              int out_f32, hipStream_t stream);
 
-// y[m, n] = a[m, k] . w[n, k]^T, a in MXFP4 or MXFP8, w in MXFP4.
+// y[m, n] = a[m, k] . w[n, k]^T, a in MXFP4 or MXFP8, w in MXFP4.  tile: 0 =
+// the kernel for few rows of a, else tile x tile outputs per workgroup with K
+// split over `splits` of them, `stages_per` LDS stages each (fp32 planes
+// [splits, m, n] in the workspace, then launch_plane_sum).
 struct MxPlan {
+  int tile;
+  int splits;
+  int stages_per;
   size_t ws_bytes;
 };
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt);
