@@ -142,42 +142,78 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_mx_rows(const uint8_t* __res
 }
 
 // ---------------------------------------------------------------------------
-// k_mx_tile: 64 NT weight rows x 64 MT rows of a per workgroup of 4 waves
-// (2 x 2, each NT x MT products of 32 x 32), both operands staged in LDS by
-// DMA, two stages: while stage s is multiplied stage s + 1 arrives, one barrier per
-// stage.  A stage is 128 bytes of every row of a (256 k of MXFP4, 128 k of
-// MXFP8) and the same k of the weights (128 or 64 bytes).
+// k_mx_tile: 4 waves, WN x WM of them, each NT x MT products of 32 x 32: a tile
+// of 32 NT WN weight rows x 32 MT WM rows of a per workgroup.  K passes in
+// stages of S steps of 64, staged in LDS by DMA (operands and scales), B
+// stages deep.
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4 reached 8.45 PFLOP/s on E2M1 operands here
 // (4.77 with one E4M3 operand) from registers alone, the 16x16x128 form 4.8 to
 // 6.1.  Lane l holds row l % 32; with h = l / 32, its 32 E2M1 codes are k =
 // 32 h .. +32 of the step's 64, its E4M3 codes k = 16 h .. +16 and 32 + 16 h ..
 // +16, its scale that of block h.  The k order of a stage is free as long as
-// both operands share it, so block h of step j is the stage's block S h + j
-// (S steps per stage): a lane's scales of all steps are then adjacent bytes,
-// one LDS read, and each step's product picks its byte with the instruction's
-// byte selector.
+// both operands share it, so block h of step j is the stage's block S h + j: a
+// lane's scales of all steps are then adjacent bytes, one LDS read, and each
+// step's product picks its byte with the instruction's byte selector.
 //
-// LDS rows are stored as 16-byte pieces, piece p of row r at slot
-// p ^ (r / 2 % 8) (rows of 128 bytes; p ^ (r / 4 % 4) for 64): the 16 rows that a
-// quarter of a read instruction takes then lie in 16 different bank groups.  The
-// DMA writes LDS in lane order, so the permutation is in its source
-// addresses.  Pieces past K come from a block of zeros (scale 1).
+// LDS rows are stored as 16-byte pieces, P per row, piece p of row r at slot
+// p ^ (r P / 16 % P): the 16 rows that a quarter of a read instruction takes
+// then lie in 16 different bank groups.  The DMA writes LDS in lane order, so
+// the permutation is in its source addresses.  Pieces past K come from a block
+// of zeros, their scales from one of ones.
+//
+// The operands of step j + 1 are read while step j is multiplied.  Before
+// the last step of a stage, whose operands are in registers by then, the waves
+// meet: the stage's buffer is free and the next stage has landed, so that the
+// copies of a later stage and the next stage's first operands are under way
+// during that step.
+//
+// SDMA = false (scale rows that are not whole 4-byte words: K % 128 != 0): the
+// scales pass through registers instead.
 __device__ __align__(16) const uint8_t kZeros[16] = {};
+__device__ __align__(16) const uint32_t kOnes[1] = {0x7F7F7F7Fu};
 
-template <int FMT, bool EXACT, int NT, int MT>
-__global__ __launch_bounds__(256, NT * MT > 8 ? 1 : 2) void k_mx_tile(
+// A barrier behind this wave's LDS accesses that leaves its copies under way
+// (__syncthreads would wait for all of them).
+__device__ __forceinline__ void meet() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#endif
+}
+
+template <int P>
+__device__ __forceinline__ int swizzle(int r) {
+  return (r / (16 / P)) & (P - 1);
+}
+__device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint8_t* dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 4, 0, 0);
+#endif
+}
+
+template <int FMT, int NT_, int MT_, int WN_, int S_, int B_>
+struct Tile {
+  static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_;
+  static constexpr int TN = 32 * NT * WN, TM = 32 * MT * WM;
+  static constexpr int WP = 2 * S, AP = FMT == kMxFp4 ? 2 * S : 4 * S;  // 16-byte pieces of a row per stage
+  static constexpr int kA = TM * 16 * AP, kW = TN * 16 * WP, kScales = (TM + TN) * 2 * S;
+  static constexpr int kStage = kA + kW + kScales;
+  static constexpr int NA = kA / 4096, NW = kW / 4096, NS = kScales / 1024;  // DMA instructions per wave and stage
+  static constexpr int kEpilogue = 4 * 32 * (32 * NT * 4 + 16);              // a padded 32-row fp32 slab per wave
+  static constexpr int kLds = B * kStage > kEpilogue ? B * kStage : kEpilogue;
+  static_assert(kA % 4096 == 0 && kW % 4096 == 0 && kScales % 1024 == 0, "whole instructions");
+  static_assert(B >= 2 && (S == 2 || S == 4), "stages");
+};
+
+template <int FMT, bool EXACT, bool SDMA, typename T>
+__global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, const uint8_t* __restrict__ w_codes,
     const uint8_t* __restrict__ w_scales, void* __restrict__ y, float* __restrict__ planes, int M, int N, int K,
     int tiles_m, int tiles_n, int stages_per, int out_f32) {
-  constexpr int TN = 64 * NT, TM = 64 * MT;
-  constexpr int S = FMT == kMxFp4 ? 4 : 2;         // 64-k steps per stage
-  constexpr int WP = 2 * S;                        // 16-byte pieces of a weight row per stage
-  constexpr int kABytes = TM * 128, kWBytes = TN * 16 * WP;
-  constexpr int kStage = kABytes + kWBytes + (TM + TN) * 2 * S;
-  constexpr int NA = TM / 32, NW = TN * WP / 256;  // DMA instructions per wave and stage
+  constexpr int TN = T::TN, TM = T::TM, NT = T::NT, MT = T::MT, S = T::S, B = T::B, WP = T::WP, AP = T::AP;
+  static_assert(SDMA || B == 2, "scales through registers: one stage ahead");
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = K / 32;
   const int stages = (nb + 2 * S - 1) / (2 * S), whole = nb / (2 * S);
 
@@ -185,79 +221,92 @@ __global__ __launch_bounds__(256, NT * MT > 8 ? 1 : 2) void k_mx_tile(
   // ordered in panels of 4 rows of tiles, so that the tiles it works on at one
   // time share few rows of a and w in its L2.
   const int tiles = tiles_m * tiles_n;
-  const int per = tiles / 8, rest = tiles % 8, x = blockIdx.x % 8;
-  const int t = x * per + min(x, rest) + blockIdx.x / 8;
-  const int panel = t / (4 * tiles_n), in = t % (4 * tiles_n), high = min(4, tiles_m - 4 * panel);
+  const int per = tiles / 8, rest = tiles % 8, xcd = blockIdx.x % 8;
+  const int tile = xcd * per + min(xcd, rest) + blockIdx.x / 8;
+  const int panel = tile / (4 * tiles_n), in = tile % (4 * tiles_n), high = min(4, tiles_m - 4 * panel);
   const int m0 = (4 * panel + in % high) * TM, n0 = in / high * TN;
-  const int s0 = blockIdx.z * stages_per, s1 = min(stages, s0 + stages_per);
+  const int s0 = blockIdx.y * stages_per, ns = min(stages - s0, stages_per);  // >= 1
 
-  const uint8_t* abase = a_codes + (int64_t)m0 * nb * (FMT == kMxFp4 ? 16 : 32);
-  const uint8_t* wbase = w_codes + (int64_t)n0 * nb * 16;
   const uint32_t apitch = nb * (FMT == kMxFp4 ? 16 : 32), wpitch = nb * 16;
+  const uint8_t* abase = a_codes + (int64_t)m0 * apitch;
+  const uint8_t* wbase = w_codes + (int64_t)n0 * wpitch;
+  const uint8_t* asbase = a_scales + (int64_t)m0 * nb;
+  const uint8_t* wsbase = w_scales + (int64_t)n0 * nb;
   const int arows = min(TM, M - m0) - 1, wrows = min(TN, N - n0) - 1;  // rows past the end read the last one
-  uint32_t aoff[NA], woff[NW];
-  uint32_t apiece[NA], wpiece[NW];
+  uint32_t aoff[T::NA], woff[T::NW], soff[T::NS];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) {
-    const int r = 8 * (wave + 4 * i) + (lane >> 3);
-    apiece[i] = (lane & 7) ^ ((r >> 1) & 7);
-    aoff[i] = min(r, arows) * apitch + 16 * apiece[i];
+  for (int i = 0; i < T::NA; ++i) {
+    const int r = (64 / AP) * (wave + 4 * i) + lane / AP;
+    aoff[i] = min(r, arows) * apitch + 16 * ((lane % AP) ^ swizzle<AP>(r)) + 16u * AP * s0;
   }
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const int r = WP == 8 ? 8 * (wave + 4 * i) + (lane >> 3) : 16 * (wave + 4 * i) + (lane >> 2);
-    wpiece[i] = WP == 8 ? (lane & 7) ^ ((r >> 1) & 7) : (lane & 3) ^ ((r >> 2) & 3);
-    woff[i] = min(r, wrows) * wpitch + 16 * wpiece[i];
+  for (int i = 0; i < T::NW; ++i) {
+    const int r = (64 / WP) * (wave + 4 * i) + lane / WP;
+    woff[i] = min(r, wrows) * wpitch + 16 * ((lane % WP) ^ swizzle<WP>(r)) + 16u * WP * s0;
   }
-  auto copy = [&](int s, int st) {
-    uint8_t* al = lds + st * kStage;
-    uint8_t* wl = al + kABytes;
+  // scale words: rows of a, then of w, S / 2 words each
+  constexpr int SW = S / 2;
+  static_assert((TM * SW) % 64 == 0, "an instruction's rows belong to one matrix");
+  auto scale_row = [&](int i) { return (64 / SW) * (wave + 4 * i) + lane / SW; };
 #pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const uint8_t* p = abase + (uint32_t)(aoff[i] + 128u * s);
-      if (s >= whole && 8 * s + apiece[i] >= apitch / 16) p = kZeros;
-      copy16_to_lds(reinterpret_cast<const uint16_t*>(p), al + 1024 * (wave + 4 * i));
-    }
+  for (int i = 0; i < T::NS; ++i) {
+    const int r = scale_row(i);
+    soff[i] = (r < TM ? min(r, arows) : min(r - TM, wrows)) * nb + 4 * (lane % SW) + 2 * S * s0;
+  }
+  // Part q of S of the copies of stage s (counted from s0) into the buffer at
+  // byte `buf`.  Whole stages: the stage's offset is scalar, a lane's own
+  // constant.
+  constexpr int NC = T::NA + T::NW + (SDMA ? T::NS : 0);
+  auto copy = [&](int s, int buf, int q, auto wholec) {
+    uint8_t* al = lds + buf;
+    uint8_t* wl = al + T::kA;
+    uint8_t* sl = wl + T::kW;
+    const uint8_t* ap = abase + 16 * AP * (int64_t)s;
+    const uint8_t* wp = wbase + 16 * WP * (int64_t)s;
+    const bool tail = !decltype(wholec)::value && s0 + s >= whole;
 #pragma unroll
-    for (int i = 0; i < NW; ++i) {
-      const uint8_t* p = wbase + (uint32_t)(woff[i] + 16u * WP * s);
-      if (s >= whole && WP * s + wpiece[i] >= wpitch / 16) p = kZeros;
-      copy16_to_lds(reinterpret_cast<const uint16_t*>(p), wl + 1024 * (wave + 4 * i));
-    }
-  };
-  // scales: thread -> rows tid, + 256, ... of [a | w], 2 S bytes each
-  constexpr int NS = (TM + TN + 255) / 256;
-  uint32_t sc[NS][S / 2];
-  auto load_scales = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int r = tid + 256 * i;
-      if (r >= TM + TN) break;
-      const uint8_t* p = r < TM ? a_scales + (int64_t)(m0 + min(r, arows)) * nb
-                                : w_scales + (int64_t)(n0 + min(r - TM, wrows)) * nb;
-      p += 2 * S * s;
-      if (s < whole) {
-        __builtin_memcpy(sc[i], p, 2 * S);
+    for (int c = 0; c < NC; ++c) {
+      if (c * S / NC != q) continue;
+      if (c < T::NA) {
+        const int i = c, r = (64 / AP) * (wave + 4 * i) + lane / AP;
+        const uint8_t* p = ap + aoff[i];
+        if (tail && AP * (s0 + s) + ((lane % AP) ^ swizzle<AP>(r)) >= (int)(apitch / 16)) p = kZeros;
+        copy16_to_lds(reinterpret_cast<const uint16_t*>(p), al + 1024 * (wave + 4 * i));
+      } else if (c < T::NA + T::NW) {
+        const int i = c - T::NA, r = (64 / WP) * (wave + 4 * i) + lane / WP;
+        const uint8_t* p = wp + woff[i];
+        if (tail && WP * (s0 + s) + ((lane % WP) ^ swizzle<WP>(r)) >= nb) p = kZeros;
+        copy16_to_lds(reinterpret_cast<const uint16_t*>(p), wl + 1024 * (wave + 4 * i));
       } else {
-#pragma unroll
-        for (int d = 0; d < S / 2; ++d) {
-          sc[i][d] = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            sc[i][d] |= (uint32_t)(2 * S * s + 4 * d + b < nb ? p[4 * d + b] : 127) << (8 * b);
-        }
+        const int i = c - T::NA - T::NW;
+        const bool is_a = (64 / SW) * (wave + 4 * i) < TM;  // the whole wave's
+        const uint8_t* p = (is_a ? asbase : wsbase) + 2 * S * (int64_t)s + soff[i];
+        if (tail && 2 * S * (s0 + s) + 4 * (lane % SW) >= nb) p = reinterpret_cast<const uint8_t*>(kOnes);
+        copy4_to_lds(p, sl + 256 * (wave + 4 * i));
       }
     }
   };
-  auto store_scales = [&](int st) {
-    uint32_t* sl = reinterpret_cast<uint32_t*>(lds + st * kStage + kABytes + kWBytes);
+  // scales through registers: word i of this thread as the DMA would place it
+  uint32_t sreg[T::NS];
+  auto load_scales = [&](int s) {
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      const int r = tid + 256 * i;
-      if (r >= TM + TN) break;
+    for (int i = 0; i < T::NS; ++i) {
+      const bool is_a = (64 / SW) * (wave + 4 * i) < TM;
+      const uint8_t* p = (is_a ? asbase : wsbase) + (soff[i] + 2u * S * s);
+      if (s0 + s < whole) {
+        __builtin_memcpy(&sreg[i], p, 4);
+      } else {
+        sreg[i] = 0;
 #pragma unroll
-      for (int d = 0; d < S / 2; ++d) sl[r * (S / 2) + d] = sc[i][d];
+        for (int b = 0; b < 4; ++b)
+          sreg[i] |= (uint32_t)(2 * S * (s0 + s) + 4 * (lane % SW) + b < nb ? p[b] : 127) << (8 * b);
+      }
     }
+  };
+  auto store_scales = [&](int buf) {
+    uint32_t* sl = reinterpret_cast<uint32_t*>(lds + buf + T::kA + T::kW);
+#pragma unroll
+    for (int i = 0; i < T::NS; ++i) sl[64 * (wave + 4 * i) + lane] = sreg[i];
   };
 
   f32x16_t acc[NT][MT];
@@ -268,125 +317,225 @@ __global__ __launch_bounds__(256, NT * MT > 8 ? 1 : 2) void k_mx_tile(
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
 
-  const int wn = (wave >> 1) * 32 * NT, wm = (wave & 1) * 32 * MT;
+  const int wn = wave / T::WM * 32 * NT, wm = wave % T::WM * 32 * MT;
   const int r = lane & 31, h = lane >> 5;
-  if (s0 < s1) {
-    copy(s0, 0);
-    load_scales(s0);
-  }
-  for (int s = s0; s < s1; ++s) {
-    const int st = (s - s0) & 1;
-    store_scales(st);
-    wait_vm_all();  // this wave's copies of stage s have landed
-    __syncthreads();  // everyone's have, and everyone is done with the other stage
-    if (s + 1 < s1) {
-      copy(s + 1, st ^ 1);
-      load_scales(s + 1);
-    }
-    const uint8_t* al = lds + st * kStage;
-    const uint8_t* wl = al + kABytes;
-    const uint8_t* sl = wl + kWBytes;
-    uint32_t as[MT], ws[NT];
+  struct Operands {
+    u32x4_t w[NT], a[MT], a1[FMT == kMxFp8 ? MT : 1];
+  };
+  auto read = [&](Operands& o, int buf, int j) {
+    const uint8_t* al = lds + buf;
+    const uint8_t* wl = al + T::kA + (wn + r) * (16 * WP) + 16 * ((S * h + j) ^ swizzle<WP>(r));
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const uint8_t* p = sl + 2 * S * (wm + 32 * j + r) + S * h;
-      as[j] = S == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-    }
+    for (int i = 0; i < NT; ++i) o.w[i] = load16(wl + 32 * 16 * WP * i);
+    al += (wm + r) * (16 * AP);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const uint8_t* p = sl + 2 * S * (TM + wn + 32 * i + r) + S * h;
-      ws[i] = S == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-    }
-    auto step = [&](auto jc) {
-      constexpr int j = decltype(jc)::value;
-      i32x8_t wf[NT], af[MT], ah[EXACT ? MT : 1];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const int slot = WP == 8 ? (S * h + j) ^ ((r >> 1) & 7) : (S * h + j) ^ ((r >> 2) & 3);
-        wf[i] = operand(load16(wl + (wn + 32 * i + r) * (16 * WP) + 16 * slot));
+    for (int i = 0; i < MT; ++i) {
+      if constexpr (FMT == kMxFp4) {
+        o.a[i] = load16(al + 32 * 16 * AP * i + 16 * ((S * h + j) ^ swizzle<AP>(r)));
+      } else {
+        o.a[i] = load16(al + 32 * 16 * AP * i + 16 * ((2 * j + h) ^ swizzle<AP>(r)));
+        o.a1[i] = load16(al + 32 * 16 * AP * i + 16 * ((2 * (S + j) + h) ^ swizzle<AP>(r)));
       }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const uint8_t* row = al + (wm + 32 * i + r) * 128;
-        const int x = (r >> 1) & 7;
-        if constexpr (FMT == kMxFp4) {
-          af[i] = operand(load16(row + 16 * ((S * h + j) ^ x)));
-        } else {
-          u32x4_t lo = load16(row + 16 * ((2 * j + h) ^ x)), hi = load16(row + 16 * ((4 + 2 * j + h) ^ x));
-          if constexpr (EXACT) {
-            const u32x4_t l2 = large_codes(lo), h2 = large_codes(hi);
-            ah[i] = operand(l2, h2);
-            lo ^= l2, hi ^= h2;
-          }
-          af[i] = operand(lo, hi);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], af[m], acc[i][m], 4, kCbsz<FMT>, j,
-                                                                      (int)ws[i], j, (int)as[m]);
-          if constexpr (EXACT)
-            acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], ah[m], acc[i][m], 4, kCbsz<FMT>, j,
-                                                                        (int)ws[i], j, (int)as[m]);
-        }
+    }
+  };
+  struct Scales {
+    uint32_t w[NT], a[MT];
+  };
+  auto read_scales = [&](Scales& o, int buf) {
+    const uint8_t* sl = lds + buf + T::kA + T::kW + S * h;
+    auto get = [](const uint8_t* p) -> uint32_t {
+      if constexpr (S == 4) return *reinterpret_cast<const uint32_t*>(p);
+      else return *reinterpret_cast<const uint16_t*>(p);
     };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    if constexpr (S == 4) {
-      step(std::integral_constant<int, 2>{});
-      step(std::integral_constant<int, 3>{});
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o.a[i] = get(sl + 2 * S * (wm + 32 * i + r));
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o.w[i] = get(sl + 2 * S * (TM + wn + 32 * i + r));
+  };
+  auto multiply = [&](const Operands& o, const Scales& c, auto jc) {
+    constexpr int j = decltype(jc)::value;
+    i32x8_t af[MT], ah[EXACT ? MT : 1];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      if constexpr (FMT == kMxFp4) {
+        af[i] = operand(o.a[i]);
+      } else if constexpr (EXACT) {
+        const u32x4_t lo = large_codes(o.a[i]), hi = large_codes(o.a1[i]);
+        ah[i] = operand(lo, hi);
+        af[i] = operand(o.a[i] ^ lo, o.a1[i] ^ hi);
+      } else {
+        af[i] = operand(o.a[i], o.a1[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(o.w[i]), af[m], acc[i][m], 4, kCbsz<FMT>, j,
+                                                                    (int)c.w[i], j, (int)c.a[m]);
+        if constexpr (EXACT)
+          acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(o.w[i]), ah[m], acc[i][m], 4, kCbsz<FMT>,
+                                                                      j, (int)c.w[i], j, (int)c.a[m]);
+      }
+  };
+  // Order of a step: products of this one between the operand reads and the
+  // copies of later ones (reads first: a copy may not pass a read of LDS).
+  constexpr int kReads = NT + (FMT == kMxFp8 ? 2 : 1) * MT, kProducts = NT * MT * (EXACT ? 2 : 1);
+  constexpr int kCopies = (NC + S - 1) / S;
+  auto interleave = [&](auto readsc) {
+    constexpr int reads = decltype(readsc)::value, slots = reads + kCopies;
+#pragma unroll
+    for (int i = 0; i < slots; ++i) {
+      const int products = (i + 1) * kProducts / slots - i * kProducts / slots;
+      if (i == 0 || products > 0) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i > 0 && products > 1) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i > 0 && products > 2) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
+      else __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);             // a copy
+    }
+  };
+
+  // End of a step: the compiler sees products as plain arithmetic and would
+  // gather those of a whole stage behind its reads and barrier.  (Sums of more
+  // than 128 registers live in the accumulation half of the register file.)
+  auto pin = [&] {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        if constexpr (NT * MT > 8) asm volatile("" : "+a"(acc[i][m]) : : "memory");
+        else asm volatile("" : "+v"(acc[i][m]) : : "memory");
+      }
+#endif
+  };
+
+  // The copies of stage s + B go into the buffer of stage s: the first part
+  // during the last step of stage s, the others during the next stage's steps.
+  constexpr std::true_type kWhole;
+  constexpr std::false_type kAny;
+#pragma unroll
+  for (int s = 0; s < B; ++s) {
+    if (s >= ns) continue;
+#pragma unroll
+    for (int q = 0; q < S; ++q)
+      if (q == 0 || s < B - 1) copy(s, s * T::kStage, q, kAny);
+    if constexpr (!SDMA) {
+      load_scales(s);
+      store_scales(s * T::kStage);
     }
   }
+  wait_vm_all();
+  __syncthreads();
+  Operands o[2];
+  Scales sc, next;
+  read_scales(sc, 0);
+  read(o[0], 0, 0);
+  int prev = (B - 1) * T::kStage, buf = 0;  // the buffers of stages s - 1 and s
+  auto stage = [&](int s, auto wholec) {
+    constexpr bool kAll = decltype(wholec)::value;  // stage s + B exists and is whole
+    const int following = buf == (B - 1) * T::kStage ? 0 : buf + T::kStage;
+    if constexpr (!SDMA) {
+      if (s + B < ns) load_scales(s + B);
+    }
+    auto inner = [&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      read(o[(j + 1) & 1], buf, j + 1);
+      if (kAll || s + B - 1 < ns) copy(s + B - 1, prev, j + 1, wholec);
+      multiply(o[j & 1], sc, jc);
+      interleave(std::integral_constant<int, kReads>{});
+      pin();
+    };
+    inner(std::integral_constant<int, 0>{});
+    if constexpr (S == 4) {
+      inner(std::integral_constant<int, 1>{});
+      inner(std::integral_constant<int, 2>{});
+    }
+    // this wave's copies of stage s + 1 have landed (those of later stages
+    // may be under way), and its reads of stage s
+    if (SDMA && (kAll || s + B - 1 < ns)) wait_vm_count<(B - 2) * NC>();
+    else wait_vm_all();
+    meet();
+    if constexpr (!SDMA) {
+      if (s + B < ns) store_scales(buf);
+    }
+    read_scales(next, following);  // past the last stage: stale values, not used
+    read(o[0], following, 0);
+    if (kAll || s + B < ns) copy(s + B, buf, 0, wholec);
+    multiply(o[(S - 1) & 1], sc, std::integral_constant<int, S - 1>{});
+    interleave(std::integral_constant<int, kReads + NT + MT>{});
+    pin();
+    sc = next;
+    prev = buf;
+    buf = following;
+  };
+  int s = 0;
+  for (const int all = min(ns, whole - s0) - B; s < all; ++s) stage(s, kWhole);
+  for (; s < ns; ++s) stage(s, kAny);
+  __syncthreads();  // the stages' LDS becomes the output's
 
   // D of a 32 x 32 product: lane l, value v -> weight row 8 (v / 4) + 4 h +
-  // v % 4, row l % 32 of a
-  const bool partial = gridDim.z > 1;
-  float* plane = planes + (int64_t)blockIdx.z * M * N;
+  // v % 4, row l % 32 of a.  Each wave turns its rows of a, 32 at a time, in
+  // LDS, and stores whole runs of 32 NT outputs.
+  const bool partial = gridDim.y > 1, f32 = partial || out_f32;
+  uint8_t* out = f32 ? reinterpret_cast<uint8_t*>(partial ? planes + (int64_t)blockIdx.y * M * N : static_cast<float*>(y))
+                     : static_cast<uint8_t*>(y);
+  const int lg = f32 ? 2 : 1;
+  uint8_t* slab = lds + wave * (T::kEpilogue / 4);
+  const int pitch = (32 * NT << lg) + 16;
+  const bool vec = (N & ((16 >> lg) - 1)) == 0;
 #pragma unroll
   for (int j = 0; j < MT; ++j) {
-    const int m = m0 + wm + 32 * j + r;
-    if (m >= M) continue;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int n = n0 + wn + 32 * i + 8 * g + 4 * h;
         const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-        const int64_t idx = (int64_t)m * N + n;
-        if (N % 4 == 0) {
-          if (n >= N) continue;
-          if (partial) *reinterpret_cast<f32x4_t*>(plane + idx) = v;
-          else if (out_f32) *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + idx) = v;
-          else *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(y) + idx) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (n + e >= N) break;
-            if (partial) plane[idx + e] = v[e];
-            else if (out_f32) static_cast<float*>(y)[idx + e] = v[e];
-            else static_cast<uint16_t*>(y)[idx + e] = (uint16_t)pack_bf16(v[e], 0.0f);
-          }
+        uint8_t* p = slab + r * pitch + ((32 * i + 8 * g + 4 * h) << lg);
+        if (f32) *reinterpret_cast<f32x4_t*>(p) = v;
+        else *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      }
+    const int runs = 2 * NT << lg;  // 16-byte pieces of a slab row
+    for (int e = lane; e < 32 * runs; e += 64) {
+      const int row = e / runs, piece = e % runs;
+      const int m = m0 + wm + 32 * j + row, n = n0 + wn + piece * (16 >> lg);
+      if (m >= M || n >= N) continue;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(slab + row * pitch + 16 * piece);
+      uint8_t* q = out + (((int64_t)m * N + n) << lg);
+      if (vec) {
+        *reinterpret_cast<u32x4_t*>(q) = v;
+      } else {
+        const int count = min(16 >> lg, N - n);
+        for (int c = 0; c < count; ++c) {
+          if (f32) reinterpret_cast<uint32_t*>(q)[c] = v[c];
+          else reinterpret_cast<uint16_t*>(q)[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
         }
       }
     }
   }
 }
 
-template <int FMT, bool EXACT, int NT, int MT>
+template <int FMT, bool EXACT, typename T>
 hipError_t launch_tile(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        const MxPlan& plan, void* workspace, hipStream_t stream) {
-  constexpr int S = FMT == kMxFp4 ? 4 : 2;
-  constexpr size_t lds = 2 * (64 * MT * 128 + 64 * NT * 32 * S + 64 * (MT + NT) * 2 * S);
-  const int tiles_m = (int)((m + 64 * MT - 1) / (64 * MT)), tiles_n = (int)((n + 64 * NT - 1) / (64 * NT));
-  hipError_t e = set_lds_limit<k_mx_tile<FMT, EXACT, NT, MT>>(lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mx_tile<FMT, EXACT, NT, MT>), dim3((unsigned)(tiles_m * tiles_n), 1, (unsigned)plan.splits),
-                     dim3(256), lds, stream, a_codes, a_scales, w_codes, w_scales, y, static_cast<float*>(workspace),
-                     (int)m, (int)n, (int)k, tiles_m, tiles_n, plan.stages_per, out_f32);
-  e = hipGetLastError();
+  using R = Tile<FMT, T::NT, T::MT, T::WN, T::S, 2>;  // scales through registers: two stages
+  const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_n = (int)((n + T::TN - 1) / T::TN);
+  const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits);
+  hipError_t e;
+  auto go = [&](auto kernel, int lds) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), lds, stream, a_codes, a_scales, w_codes, w_scales, y,
+                       static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_n, plan.stages_per,
+                       out_f32);
+    return hipGetLastError();
+  };
+  if (k % 128 == 0) {
+    e = set_lds_limit<k_mx_tile<FMT, EXACT, true, T>>(T::kLds);
+    if (e == hipSuccess) e = go(k_mx_tile<FMT, EXACT, true, T>, T::kLds);
+  } else {
+    e = set_lds_limit<k_mx_tile<FMT, EXACT, false, R>>(R::kLds);
+    if (e == hipSuccess) e = go(k_mx_tile<FMT, EXACT, false, R>, R::kLds);
+  }
   if (e != hipSuccess || plan.splits == 1) return e;
   return launch_plane_sum(static_cast<const float*>(workspace), y, m * n, plan.splits, out_f32, stream);
 }
@@ -460,10 +609,10 @@ template <int FMT, bool EXACT>
 hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
-  if (plan.tile == 256)
-    return launch_tile<FMT, EXACT, 4, 4>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream);
-  if (plan.tile == 128)
-    return launch_tile<FMT, EXACT, 2, 2>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream);
+  constexpr int S = FMT == kMxFp4 ? 4 : 2;
+  auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
+  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, 2, FMT == kMxFp4 ? 4 : 3>>);
+  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile<FMT, 2, 2, 2, S, 2>>);
   return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
 }
 }  // namespace
