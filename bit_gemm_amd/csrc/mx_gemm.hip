@@ -196,12 +196,13 @@ struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_;
   static constexpr int TN = 32 * NT * WN, TM = 32 * MT * WM;
   static constexpr int WP = 2 * S, AP = FMT == kMxFp4 ? 2 * S : 4 * S;  // 16-byte pieces of a row per stage
-  static constexpr int kA = TM * 16 * AP, kW = TN * 16 * WP, kScales = (TM + TN) * 2 * S;
-  static constexpr int kStage = kA + kW + kScales;
-  static constexpr int NA = kA / 4096, NW = kW / 4096, NS = kScales / 1024;  // DMA instructions per wave and stage
+  static constexpr int kA = TM * 16 * AP, kW = TN * 16 * WP;
+  // DMA instructions per wave and stage (of scales: the last may repeat the last row)
+  static constexpr int NA = kA / 4096, NW = kW / 4096, NS = ((TM + TN) * 2 * S + 1023) / 1024;
+  static constexpr int kStage = kA + kW + NS * 1024;
   static constexpr int kEpilogue = 4 * 32 * (32 * NT * 4 + 16);              // a padded 32-row fp32 slab per wave
   static constexpr int kLds = B * kStage > kEpilogue ? B * kStage : kEpilogue;
-  static_assert(kA % 4096 == 0 && kW % 4096 == 0 && kScales % 1024 == 0, "whole instructions");
+  static_assert(kA % 4096 == 0 && kW % 4096 == 0, "whole instructions");
   static_assert(B >= 2 && (S == 2 || S == 4), "stages");
 };
 
@@ -611,7 +612,7 @@ hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
   constexpr int S = FMT == kMxFp4 ? 4 : 2;
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
-  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, 2, FMT == kMxFp4 ? 4 : 3>>);
+  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, S, FMT == kMxFp4 ? 2 : 3>>);
   if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile<FMT, 2, 2, 2, S, 2>>);
   return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
 }

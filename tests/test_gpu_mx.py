@@ -108,6 +108,23 @@ def test_gemm(fmt, m, n, k):
 
 
 @FMTS
+@pytest.mark.parametrize("m,n,k", [(3500, 3700, 544), (2300, 5000, 1024), (4096, 4224, 2080)])
+def test_gemm_many_tiles(fmt, m, n, k):
+    # enough outputs for every workgroup tile the library has; sampled rows against the oracle
+    print("mx gemm", fmt, m, n, k, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    a = nv.quantize_mx(torch.randn(m, k, generator=g, device="cuda"), fmt)
+    w = nv.quantize_mx(torch.randn(n, k, generator=g, device="cuda"))
+    pick = np.unique(np.concatenate([[0, 31, 32, 63, 64, 127, 128, 255, 256, m - 1], np.random.default_rng(m).integers(0, m, 30)]))
+    av = mx.dequant_mx(a.codes.cpu().numpy()[pick], a.scales.cpu().numpy()[pick], fmt)
+    wv = mx.dequant_mx(w.codes.cpu().numpy(), w.scales.cpu().numpy(), mx.FP4)
+    for dt in (torch.bfloat16, torch.float32):
+        ref, bound = product_bound(av, wv, fmt, dt)
+        y = _np(nv.mx_gemm(a, w, out_dtype=dt)[torch.from_numpy(pick).cuda()])
+        assert np.all(np.abs(y - ref) <= bound), (dt, float((np.abs(y - ref) / bound).max()))
+
+
+@FMTS
 @pytest.mark.parametrize("m,n", [(7, 19), (70, 140), (300, 520)])
 def test_gemm_exact_sums(fmt, m, n):
     # small codes and scales: every partial sum is an integer multiple of one
