@@ -144,8 +144,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_mx_rows(const uint8_t* __res
 // ---------------------------------------------------------------------------
 // k_mx_tile: 4 waves, WN x WM of them, each NT x MT products of 32 x 32: a tile
 // of 32 NT WN weight rows x 32 MT WM rows of a per workgroup.  K passes in
-// stages of S steps of 64, staged in LDS by DMA (operands and scales), B
-// stages deep.
+// stages of S steps of 64, staged in LDS by DMA, B stages deep.
 //
 // v_mfma_scale_f32_32x32x64_f8f6f4 reached 8.45 PFLOP/s on E2M1 operands here
 // (4.77 with one E4M3 operand) from registers alone, the 16x16x128 form 4.8 to
@@ -160,7 +159,7 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_mx_rows(const uint8_t* __res
 // p ^ (r P / 16 % P): the 16 rows that a quarter of a read instruction takes
 // then lie in 16 different bank groups.  The DMA writes LDS in lane order, so
 // the permutation is in its source addresses.  Pieces past K come from a block
-// of zeros, their scales from one of ones.
+// of zeros, their scales are ones.
 //
 // The operands of step j + 1 are read while step j is multiplied.  Before
 // the last step of a stage, whose operands are in registers by then, the waves
@@ -168,10 +167,11 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_mx_rows(const uint8_t* __res
 // copies of a later stage and the next stage's first operands are under way
 // during that step.
 //
-// SDMA = false (scale rows that are not whole 4-byte words: K % 128 != 0): the
-// scales pass through registers instead.
+// Scales: fetched for G stages at a time, through registers.  Their rows are
+// K / 32 bytes apart, so every row is a memory access of its own: fetching a
+// stage's 8 bytes per row cost as much time as the stage's codes (a 256 x 256
+// tile's 512 rows: 0.5 us against 0.65 us for 64 KiB of codes in whole lines).
 __device__ __align__(16) const uint8_t kZeros[16] = {};
-__device__ __align__(16) const uint32_t kOnes[1] = {0x7F7F7F7Fu};
 
 // A barrier behind this wave's LDS accesses that leaves its copies under way
 // (__syncthreads would wait for all of them).
@@ -185,34 +185,30 @@ template <int P>
 __device__ __forceinline__ int swizzle(int r) {
   return (r / (16 / P)) & (P - 1);
 }
-__device__ __forceinline__ void copy4_to_lds(const uint8_t* src, uint8_t* dst) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)dst, 4, 0, 0);
-#endif
-}
 
-template <int FMT, int NT_, int MT_, int WN_, int S_, int B_>
+template <int FMT, int NT_, int MT_, int WN_, int S_, int B_, int G_>
 struct Tile {
-  static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_;
+  static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
   static constexpr int TN = 32 * NT * WN, TM = 32 * MT * WM;
   static constexpr int WP = 2 * S, AP = FMT == kMxFp4 ? 2 * S : 4 * S;  // 16-byte pieces of a row per stage
   static constexpr int kA = TM * 16 * AP, kW = TN * 16 * WP;
-  // DMA instructions per wave and stage (of scales: the last may repeat the last row)
-  static constexpr int NA = kA / 4096, NW = kW / 4096, NS = ((TM + TN) * 2 * S + 1023) / 1024;
-  static constexpr int kStage = kA + kW + NS * 1024;
+  static constexpr int NA = kA / 4096, NW = kW / 4096;  // DMA instructions per wave and stage
+  static constexpr int kStage = kA + kW;
+  static constexpr int SR = 2 * S * G;                                // scale bytes of a row per G stages
+  static constexpr int NS = ((TM + TN) * SR / 16 + 255) / 256;        // 16-byte loads per thread for them
+  static constexpr int kScales = (TM + TN) * SR, kAll = B * kStage + 2 * kScales;
   static constexpr int kEpilogue = 4 * 32 * (32 * NT * 4 + 16);              // a padded 32-row fp32 slab per wave
-  static constexpr int kLds = B * kStage > kEpilogue ? B * kStage : kEpilogue;
+  static constexpr int kLds = kAll > kEpilogue ? kAll : kEpilogue;
   static_assert(kA % 4096 == 0 && kW % 4096 == 0, "whole instructions");
-  static_assert(B >= 2 && (S == 2 || S == 4), "stages");
+  static_assert(B >= 2 && (S == 2 || S == 4) && G >= 2 && SR % 16 == 0 && kLds <= 160 * 1024, "stages");
 };
 
-template <int FMT, bool EXACT, bool SDMA, typename T>
+template <int FMT, bool EXACT, typename T>
 __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, const uint8_t* __restrict__ w_codes,
     const uint8_t* __restrict__ w_scales, void* __restrict__ y, float* __restrict__ planes, int M, int N, int K,
     int tiles_m, int tiles_n, int stages_per, int out_f32) {
-  constexpr int TN = T::TN, TM = T::TM, NT = T::NT, MT = T::MT, S = T::S, B = T::B, WP = T::WP, AP = T::AP;
-  static_assert(SDMA || B == 2, "scales through registers: one stage ahead");
+  constexpr int TN = T::TN, TM = T::TM, NT = T::NT, MT = T::MT, S = T::S, B = T::B, G = T::G, WP = T::WP, AP = T::AP;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nb = K / 32;
@@ -234,7 +230,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   const uint8_t* asbase = a_scales + (int64_t)m0 * nb;
   const uint8_t* wsbase = w_scales + (int64_t)n0 * nb;
   const int arows = min(TM, M - m0) - 1, wrows = min(TN, N - n0) - 1;  // rows past the end read the last one
-  uint32_t aoff[T::NA], woff[T::NW], soff[T::NS];
+  uint32_t aoff[T::NA], woff[T::NW];
 #pragma unroll
   for (int i = 0; i < T::NA; ++i) {
     const int r = (64 / AP) * (wave + 4 * i) + lane / AP;
@@ -245,69 +241,68 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     const int r = (64 / WP) * (wave + 4 * i) + lane / WP;
     woff[i] = min(r, wrows) * wpitch + 16 * ((lane % WP) ^ swizzle<WP>(r)) + 16u * WP * s0;
   }
-  // scale words: rows of a, then of w, S / 2 words each
-  constexpr int SW = S / 2;
-  static_assert((TM * SW) % 64 == 0, "an instruction's rows belong to one matrix");
-  auto scale_row = [&](int i) { return (64 / SW) * (wave + 4 * i) + lane / SW; };
-#pragma unroll
-  for (int i = 0; i < T::NS; ++i) {
-    const int r = scale_row(i);
-    soff[i] = (r < TM ? min(r, arows) : min(r - TM, wrows)) * nb + 4 * (lane % SW) + 2 * S * s0;
-  }
-  // Part q of S of the copies of stage s (counted from s0) into the buffer at
-  // byte `buf`.  Whole stages: the stage's offset is scalar, a lane's own
-  // constant.
-  constexpr int NC = T::NA + T::NW + (SDMA ? T::NS : 0);
+  // Half q of the copies of stage s (counted from s0) into the buffer at byte
+  // `buf`.  Whole stages: the stage's offset is scalar, a lane's own constant.
+  constexpr int NC = T::NA + T::NW, kFirst = (NC + 1) / 2;
   auto copy = [&](int s, int buf, int q, auto wholec) {
     uint8_t* al = lds + buf;
     uint8_t* wl = al + T::kA;
-    uint8_t* sl = wl + T::kW;
     const uint8_t* ap = abase + 16 * AP * (int64_t)s;
     const uint8_t* wp = wbase + 16 * WP * (int64_t)s;
     const bool tail = !decltype(wholec)::value && s0 + s >= whole;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (c * S / NC != q) continue;
+      if ((c >= kFirst) != (q == 1)) continue;
       if (c < T::NA) {
         const int i = c, r = (64 / AP) * (wave + 4 * i) + lane / AP;
         const uint8_t* p = ap + aoff[i];
         if (tail && AP * (s0 + s) + ((lane % AP) ^ swizzle<AP>(r)) >= (int)(apitch / 16)) p = kZeros;
         copy16_to_lds(reinterpret_cast<const uint16_t*>(p), al + 1024 * (wave + 4 * i));
-      } else if (c < T::NA + T::NW) {
+      } else {
         const int i = c - T::NA, r = (64 / WP) * (wave + 4 * i) + lane / WP;
         const uint8_t* p = wp + woff[i];
         if (tail && WP * (s0 + s) + ((lane % WP) ^ swizzle<WP>(r)) >= nb) p = kZeros;
         copy16_to_lds(reinterpret_cast<const uint16_t*>(p), wl + 1024 * (wave + 4 * i));
-      } else {
-        const int i = c - T::NA - T::NW;
-        const bool is_a = (64 / SW) * (wave + 4 * i) < TM;  // the whole wave's
-        const uint8_t* p = (is_a ? asbase : wsbase) + 2 * S * (int64_t)s + soff[i];
-        if (tail && 2 * S * (s0 + s) + 4 * (lane % SW) >= nb) p = reinterpret_cast<const uint8_t*>(kOnes);
-        copy4_to_lds(p, sl + 256 * (wave + 4 * i));
       }
     }
   };
-  // scales through registers: word i of this thread as the DMA would place it
-  uint32_t sreg[T::NS];
-  auto load_scales = [&](int s) {
+  // The scales of stages G u .. + G (counted from s0): rows of a, then of w, SR
+  // bytes each; a thread takes 16-byte pieces tid, + 256, ... of them.  In LDS
+  // word d of every row lies in an array of its own, odd arrays with rows 32
+  // apart exchanged: a wave's read of two words of 32 rows meets 64 banks.
+  constexpr int SR = T::SR, kRows = TN + TM;
+  auto scale_at = [](int row, int d) { return 4 * (d * kRows + (row ^ (d & 1) * 32)); };
+  u32x4_t sreg[T::NS];
+  auto load_scales = [&](int u) {
 #pragma unroll
     for (int i = 0; i < T::NS; ++i) {
-      const bool is_a = (64 / SW) * (wave + 4 * i) < TM;
-      const uint8_t* p = (is_a ? asbase : wsbase) + (soff[i] + 2u * S * s);
-      if (s0 + s < whole) {
-        __builtin_memcpy(&sreg[i], p, 4);
-      } else {
-        sreg[i] = 0;
+      const int e = (int)threadIdx.x + 256 * i, r = e / (SR / 16);
+      const int at = 2 * S * s0 + SR * u + 16 * (e % (SR / 16));  // byte of the row
+      const uint8_t* p = r < TM ? a_scales + (int64_t)(m0 + min(r, arows)) * nb
+                                : w_scales + (int64_t)(n0 + min(r - TM, wrows)) * nb;
+      if (2 * S * s0 + SR * (u + 1) <= nb) {
+        __builtin_memcpy(&sreg[i], p + at, 16);
+      } else {  // the end of the rows: byte by byte, ones behind it
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          sreg[i] |= (uint32_t)(2 * S * (s0 + s) + 4 * (lane % SW) + b < nb ? p[b] : 127) << (8 * b);
+        for (int d = 0; d < 4; ++d) {
+          uint32_t v = 0;
+#pragma unroll 1
+          for (int b = at + 4 * d; b < at + 4 * d + 4; ++b) v = (v >> 8) | (uint32_t)(b < nb ? p[b] : 127) << 24;
+          sreg[i][d] = v;
+        }
       }
     }
   };
-  auto store_scales = [&](int buf) {
-    uint32_t* sl = reinterpret_cast<uint32_t*>(lds + buf + T::kA + T::kW);
+  auto store_scales = [&](int u) {
+    uint8_t* sl = lds + B * T::kStage + (u & 1) * T::kScales;
 #pragma unroll
-    for (int i = 0; i < T::NS; ++i) sl[64 * (wave + 4 * i) + lane] = sreg[i];
+    for (int i = 0; i < T::NS; ++i) {
+      const int e = (int)threadIdx.x + 256 * i;
+      if (kRows * SR / 16 % 256 != 0 && e >= kRows * SR / 16) break;
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        *reinterpret_cast<uint32_t*>(sl + scale_at(e / (SR / 16), e % (SR / 16) * 4 + d)) = sreg[i][d];
+    }
   };
 
   f32x16_t acc[NT][MT];
@@ -342,16 +337,17 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   struct Scales {
     uint32_t w[NT], a[MT];
   };
-  auto read_scales = [&](Scales& o, int buf) {
-    const uint8_t* sl = lds + buf + T::kA + T::kW + S * h;
-    auto get = [](const uint8_t* p) -> uint32_t {
-      if constexpr (S == 4) return *reinterpret_cast<const uint32_t*>(p);
-      else return *reinterpret_cast<const uint16_t*>(p);
+  auto read_scales = [&](Scales& o, int s) {
+    const uint8_t* sl = lds + B * T::kStage + (s / G & 1) * T::kScales;
+    const int u = s % G;
+    auto get = [&](int row) -> uint32_t {
+      if constexpr (S == 4) return *reinterpret_cast<const uint32_t*>(sl + scale_at(row, 2 * u + h));
+      else return *reinterpret_cast<const uint16_t*>(sl + scale_at(row, u) + 2 * h);
     };
 #pragma unroll
-    for (int i = 0; i < MT; ++i) o.a[i] = get(sl + 2 * S * (wm + 32 * i + r));
+    for (int i = 0; i < MT; ++i) o.a[i] = get(wm + 32 * i + r);
 #pragma unroll
-    for (int i = 0; i < NT; ++i) o.w[i] = get(sl + 2 * S * (TM + wn + 32 * i + r));
+    for (int i = 0; i < NT; ++i) o.w[i] = get(TM + wn + 32 * i + r);
   };
   auto multiply = [&](const Operands& o, const Scales& c, auto jc) {
     constexpr int j = decltype(jc)::value;
@@ -382,9 +378,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   // Order of a step: products of this one between the operand reads and the
   // copies of later ones (reads first: a copy may not pass a read of LDS).
   constexpr int kReads = NT + (FMT == kMxFp8 ? 2 : 1) * MT, kProducts = NT * MT * (EXACT ? 2 : 1);
-  constexpr int kCopies = (NC + S - 1) / S;
-  auto interleave = [&](auto readsc) {
-    constexpr int reads = decltype(readsc)::value, slots = reads + kCopies;
+  auto interleave = [&](auto readsc, auto copiesc) {
+    constexpr int reads = decltype(readsc)::value, slots = reads + decltype(copiesc)::value;
 #pragma unroll
     for (int i = 0; i < slots; ++i) {
       const int products = (i + 1) * kProducts / slots - i * kProducts / slots;
@@ -396,36 +391,35 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     }
   };
 
-  // End of a step: the compiler sees products as plain arithmetic and would
-  // gather those of a whole stage behind its reads and barrier.  (Sums of more
-  // than 128 registers live in the accumulation half of the register file.)
-  auto pin = [&] {
+  // Holds the sums where they are at this point.  At the end of a step: the
+  // compiler sees products as plain arithmetic and would gather those of a
+  // whole stage behind its reads and barrier.  (Sums of more than 128 registers
+  // live in the accumulation half of the register file.)
+  auto hold = [&](f32x16_t& v) {
 #if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (NT * MT > 8) asm volatile("" : "+a"(v) : : "memory");
+    else asm volatile("" : "+v"(v) : : "memory");
+#endif
+  };
+  auto pin = [&] {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if constexpr (NT * MT > 8) asm volatile("" : "+a"(acc[i][m]) : : "memory");
-        else asm volatile("" : "+v"(acc[i][m]) : : "memory");
-      }
-#endif
+      for (int m = 0; m < MT; ++m) hold(acc[i][m]);
   };
 
-  // The copies of stage s + B go into the buffer of stage s: the first part
-  // during the last step of stage s, the others during the next stage's steps.
+  // The copies of stage s + B go into the buffer of stage s: one half during
+  // the last step of stage s, the other during the first of the next stage.
   constexpr std::true_type kWhole;
   constexpr std::false_type kAny;
 #pragma unroll
   for (int s = 0; s < B; ++s) {
     if (s >= ns) continue;
-#pragma unroll
-    for (int q = 0; q < S; ++q)
-      if (q == 0 || s < B - 1) copy(s, s * T::kStage, q, kAny);
-    if constexpr (!SDMA) {
-      load_scales(s);
-      store_scales(s * T::kStage);
-    }
+    copy(s, s * T::kStage, 0, kAny);
+    if (s < B - 1) copy(s, s * T::kStage, 1, kAny);
   }
+  load_scales(0);
+  store_scales(0);
   wait_vm_all();
   __syncthreads();
   Operands o[2];
@@ -436,15 +430,14 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   auto stage = [&](int s, auto wholec) {
     constexpr bool kAll = decltype(wholec)::value;  // stage s + B exists and is whole
     const int following = buf == (B - 1) * T::kStage ? 0 : buf + T::kStage;
-    if constexpr (!SDMA) {
-      if (s + B < ns) load_scales(s + B);
-    }
+    const bool more = (s / G + 1) * G < ns;  // scales of later stages
+    if (s % G == 0 && more) load_scales(s / G + 1);
     auto inner = [&](auto jc) {
       constexpr int j = decltype(jc)::value;
       read(o[(j + 1) & 1], buf, j + 1);
-      if (kAll || s + B - 1 < ns) copy(s + B - 1, prev, j + 1, wholec);
+      if (j == 0 && (kAll || s + B - 1 < ns)) copy(s + B - 1, prev, 1, wholec);
       multiply(o[j & 1], sc, jc);
-      interleave(std::integral_constant<int, kReads>{});
+      interleave(std::integral_constant<int, kReads>{}, std::integral_constant<int, j == 0 ? NC - kFirst : 0>{});
       pin();
     };
     inner(std::integral_constant<int, 0>{});
@@ -454,17 +447,17 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     }
     // this wave's copies of stage s + 1 have landed (those of later stages
     // may be under way), and its reads of stage s
-    if (SDMA && (kAll || s + B - 1 < ns)) wait_vm_count<(B - 2) * NC>();
+    if (kAll || s + B - 1 < ns) wait_vm_count<(B - 2) * NC>();
     else wait_vm_all();
     meet();
-    if constexpr (!SDMA) {
-      if (s + B < ns) store_scales(buf);
-    }
-    read_scales(next, following);  // past the last stage: stale values, not used
+    // written one meeting before the first of them is read, G - 1 stages after
+    // the last read of what was there
+    if (s % G == G - 2 && more) store_scales(s / G + 1);
+    read_scales(next, s + 1);  // past the last stage: stale values, not used
     read(o[0], following, 0);
     if (kAll || s + B < ns) copy(s + B, buf, 0, wholec);
     multiply(o[(S - 1) & 1], sc, std::integral_constant<int, S - 1>{});
-    interleave(std::integral_constant<int, kReads + NT + MT>{});
+    interleave(std::integral_constant<int, kReads + NT + MT>{}, std::integral_constant<int, kFirst>{});
     pin();
     sc = next;
     prev = buf;
@@ -478,65 +471,77 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   // D of a 32 x 32 product: lane l, value v -> weight row 8 (v / 4) + 4 h +
   // v % 4, row l % 32 of a.  Each wave turns its rows of a, 32 at a time, in
   // LDS, and stores whole runs of 32 NT outputs.
-  const bool partial = gridDim.y > 1, f32 = partial || out_f32;
-  uint8_t* out = f32 ? reinterpret_cast<uint8_t*>(partial ? planes + (int64_t)blockIdx.y * M * N : static_cast<float*>(y))
-                     : static_cast<uint8_t*>(y);
-  const int lg = f32 ? 2 : 1;
   uint8_t* slab = lds + wave * (T::kEpilogue / 4);
-  const int pitch = (32 * NT << lg) + 16;
-  const bool vec = (N & ((16 >> lg) - 1)) == 0;
+  auto store = [&](auto* out) {
+    using E = std::remove_reference_t<decltype(*out)>;
+    constexpr int kPer = 16 / sizeof(E), kRuns = 32 * NT / kPer;  // outputs of a 16-byte piece, pieces of a slab row
+    constexpr int kPitch = 32 * NT * sizeof(E) + 16;
+    const bool vec = N % kPer == 0;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
+    for (int j = 0; j < MT; ++j) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < NT; ++i) hold(acc[i][j]);  // no earlier copy of them in other registers
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-        uint8_t* p = slab + r * pitch + ((32 * i + 8 * g + 4 * h) << lg);
-        if (f32) *reinterpret_cast<f32x4_t*>(p) = v;
-        else *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+          uint8_t* p = slab + r * kPitch + (32 * i + 8 * g + 4 * h) * sizeof(E);
+          if constexpr (sizeof(E) == 4) *reinterpret_cast<f32x4_t*>(p) = v;
+          else *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        }
+      u32x4_t v[kRuns / 2];
+#pragma unroll
+      for (int e = 0; e < kRuns / 2; ++e) {
+        const int at = lane + 64 * e;
+        v[e] = *reinterpret_cast<const u32x4_t*>(slab + at / kRuns * kPitch + at % kRuns * 16);
       }
-    const int runs = 2 * NT << lg;  // 16-byte pieces of a slab row
-    for (int e = lane; e < 32 * runs; e += 64) {
-      const int row = e / runs, piece = e % runs;
-      const int m = m0 + wm + 32 * j + row, n = n0 + wn + piece * (16 >> lg);
-      if (m >= M || n >= N) continue;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(slab + row * pitch + 16 * piece);
-      uint8_t* q = out + (((int64_t)m * N + n) << lg);
-      if (vec) {
-        *reinterpret_cast<u32x4_t*>(q) = v;
-      } else {
-        const int count = min(16 >> lg, N - n);
-        for (int c = 0; c < count; ++c) {
-          if (f32) reinterpret_cast<uint32_t*>(q)[c] = v[c];
-          else reinterpret_cast<uint16_t*>(q)[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+#pragma unroll
+      for (int e = 0; e < kRuns / 2; ++e) {
+        const int at = lane + 64 * e, m = m0 + wm + 32 * j + at / kRuns, n = n0 + wn + at % kRuns * kPer;
+        if (m >= M || n >= N) continue;
+        E* q = out + (int64_t)m * N + n;
+        if (vec) {
+          *reinterpret_cast<u32x4_t*>(q) = v[e];
+        } else {
+#pragma unroll
+          for (int c = 0; c < kPer; ++c) {
+            if (n + c >= N) break;
+            if constexpr (sizeof(E) == 4) reinterpret_cast<uint32_t*>(q)[c] = v[e][c];
+            else q[c] = (E)(v[e][c >> 1] >> (16 * (c & 1)));
+          }
         }
       }
     }
-  }
+  };
+  if (gridDim.y > 1) store(planes + (int64_t)blockIdx.y * M * N);
+  else if (out_f32) store(static_cast<float*>(y));
+  else store(static_cast<uint16_t*>(y));
+}
+
+// Opt in to kLds bytes of LDS, once per kernel.
+template <auto Kernel, int kLds>
+hipError_t set_lds_limit() {
+  static std::atomic<bool> done{false};
+  if (kLds <= 65536 || done.load(std::memory_order_relaxed)) return hipSuccess;
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                     kLds);
+  if (e == hipSuccess) done.store(true, std::memory_order_relaxed);
+  return e;
 }
 
 template <int FMT, bool EXACT, typename T>
 hipError_t launch_tile(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        const MxPlan& plan, void* workspace, hipStream_t stream) {
-  using R = Tile<FMT, T::NT, T::MT, T::WN, T::S, 2>;  // scales through registers: two stages
   const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_n = (int)((n + T::TN - 1) / T::TN);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits);
-  hipError_t e;
-  auto go = [&](auto kernel, int lds) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), lds, stream, a_codes, a_scales, w_codes, w_scales, y,
-                       static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_n, plan.stages_per,
-                       out_f32);
-    return hipGetLastError();
-  };
-  if (k % 128 == 0) {
-    e = set_lds_limit<k_mx_tile<FMT, EXACT, true, T>>(T::kLds);
-    if (e == hipSuccess) e = go(k_mx_tile<FMT, EXACT, true, T>, T::kLds);
-  } else {
-    e = set_lds_limit<k_mx_tile<FMT, EXACT, false, R>>(R::kLds);
-    if (e == hipSuccess) e = go(k_mx_tile<FMT, EXACT, false, R>, R::kLds);
-  }
+  hipError_t e = set_lds_limit<k_mx_tile<FMT, EXACT, T>, T::kLds>();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_mx_tile<FMT, EXACT, T>), grid, dim3(256), T::kLds, stream, a_codes, a_scales, w_codes,
+                     w_scales, y, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_n,
+                     plan.stages_per, out_f32);
+  e = hipGetLastError();
   if (e != hipSuccess || plan.splits == 1) return e;
   return launch_plane_sum(static_cast<const float*>(workspace), y, m * n, plan.splits, out_f32, stream);
 }
@@ -612,8 +617,8 @@ hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
   constexpr int S = FMT == kMxFp4 ? 4 : 2;
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
-  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, S, FMT == kMxFp4 ? 2 : 3>>);
-  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile<FMT, 2, 2, 2, S, 2>>);
+  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, S, FMT == kMxFp4 ? 2 : 3, 4>>);
+  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile<FMT, 2, 2, 2, S, 2, 4>>);
   return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
 }
 }  // namespace
