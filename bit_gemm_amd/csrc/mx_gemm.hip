@@ -519,6 +519,20 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   else store(static_cast<uint16_t*>(y));
 }
 
+// The tiles the library has (plan_mx_gemm chooses).  256 k per stage, but 128
+// where the E4M3 rows of 128 or 256 would not fit twice in LDS.
+template <int FMT>
+using Tile256 = Tile<FMT, 4, 4, 2, FMT == kMxFp4 ? 4 : 2, FMT == kMxFp4 ? 2 : 3, 4>;
+template <int FMT>
+using Tile128 = Tile<FMT, 2, 2, 2, FMT == kMxFp4 ? 4 : 2, FMT == kMxFp4 ? 2 : 4, 4>;
+template <int FMT>
+using Tile64 = Tile<FMT, 1, 1, 2, 4, 3, 4>;
+// k per stage of a tile.
+int mx_tile_k(int fmt, int size) {
+  if (fmt == kMxFp4) return 64 * (size == 256 ? Tile256<kMxFp4>::S : size == 128 ? Tile128<kMxFp4>::S : Tile64<kMxFp4>::S);
+  return 64 * (size == 256 ? Tile256<kMxFp8>::S : size == 128 ? Tile128<kMxFp8>::S : Tile64<kMxFp8>::S);
+}
+
 // Opt in to kLds bytes of LDS, once per kernel.
 template <auto Kernel, int kLds>
 hipError_t set_lds_limit() {
@@ -594,20 +608,50 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
   return hipGetLastError();
 }
 
+// The kernel, tile and split with the least expected time, from times measured
+// on MI355X (microseconds, MXFP4 / MXFP8 activations).  A round of workgroups
+// over 256 of K takes
+//   64 x 64 tiles:   0.46 / 0.50 with at most one workgroup per CU, 0.60 / 0.75 with two
+//   128 x 128:       1.0 / 1.3, 1.5 with two (MXFP8: its LDS leaves room for one)
+//   256 x 256:       2.5 / 3.4
+// beside about 2 for a launch, and a split of K 3 for its second launch and the
+// planes' traffic.  So few outputs take small tiles, for more workgroups, and many
+// large ones, which read each operand less often: 1024 x 4096 x 4096 (m, n, k)
+// with MXFP4 took 21.5 / 17.6 / 32.0 with the three tiles, 512 x 4096 x 4096
+// 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
+// x 4096 281 / 175 / 158; 64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
+// four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
-  MxPlan p{0, 1, 0, 0};
-  // the tile kernel's offsets inside a tile are 32 bits wide; few rows, and
-  // rows beyond that, take the other kernel
-  if (m <= 64 || k > ((int64_t)1 << 22)) return p;
-  auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((n + t - 1) / t); };
-  p.tile = tiles(256) >= 192 ? 256 : 128;
-  const int64_t bk = a_fmt == kMxFp4 ? 256 : 128, stages = (k + bk - 1) / bk, count = tiles(p.tile);
-  int splits = 1;
-  while (count * splits * 2 <= 512 && stages / (splits * 2) >= 4) splits *= 2;
-  p.stages_per = (int)((stages + splits - 1) / splits);
-  p.splits = p.stages_per > 0 ? (int)((stages + p.stages_per - 1) / p.stages_per) : 1;
-  p.ws_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * sizeof(float) : 0;
-  return p;
+  MxPlan best{0, 1, 0, 0};
+  // up to 16 rows: the other kernel; also where a tile's rows pass 32-bit offsets
+  if (m <= 16 || k > ((int64_t)1 << 22)) return best;
+  struct Shape {
+    int size, slots;
+    double alone, full;  // time of a round of at most 256 workgroups, of `slots`
+  };
+  static const Shape kFp4[3] = {{64, 512, 0.46, 0.60}, {128, 512, 1.0, 1.5}, {256, 256, 2.5, 2.5}};
+  static const Shape kFp8[3] = {{64, 512, 0.50, 0.75}, {128, 256, 1.3, 1.3}, {256, 256, 3.4, 3.4}};
+  double least = 1e300;
+  for (int i = 0; i < 3; ++i) {
+    const Shape& t = a_fmt == kMxFp4 ? kFp4[i] : kFp8[i];
+    const int64_t bk = mx_tile_k(a_fmt, t.size), stages = (k + bk - 1) / bk;
+    const int64_t count = ((m + t.size - 1) / t.size) * ((n + t.size - 1) / t.size);
+    for (int64_t z = 1; z <= 16 && (z == 1 || (count * z <= 512 && stages / z >= 2)); z *= 2) {
+      const int64_t per = (stages + z - 1) / z, all = count * ((stages + per - 1) / per);
+      const int64_t rest = all % t.slots;
+      const double rounds = (double)(all / t.slots) * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full);
+      double time = 2.0 + rounds * (double)(per * bk) / 256.0;
+      if (z > 1) time += 3.0 + 8.0 * (double)z * (double)m * (double)n / 3.0e6;
+      if (time < least) {
+        least = time;
+        best.tile = t.size;
+        best.stages_per = (int)per;
+        best.splits = (int)((stages + per - 1) / per);
+      }
+    }
+  }
+  best.ws_bytes = best.splits > 1 ? (size_t)best.splits * (size_t)m * (size_t)n * sizeof(float) : 0;
+  return best;
 }
 
 namespace {
@@ -615,10 +659,10 @@ template <int FMT, bool EXACT>
 hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
-  constexpr int S = FMT == kMxFp4 ? 4 : 2;
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
-  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile<FMT, 4, 4, 2, S, FMT == kMxFp4 ? 2 : 3, 4>>);
-  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile<FMT, 2, 2, 2, S, 2, 4>>);
+  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile256<FMT>>);
+  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile128<FMT>>);
+  if (plan.tile == 64) return go(launch_tile<FMT, EXACT, Tile64<FMT>>);
   return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
 }
 }  // namespace
