@@ -68,76 +68,101 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32
 __device__ __forceinline__ u32x4_t load16(const uint8_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 // ---------------------------------------------------------------------------
-// k_mx_rows: 16 weight rows x 16 MT rows of a per workgroup, the whole K cut
-// over 8 waves in chunks of 512 (4 steps of 128), operands straight from
-// global memory, the waves' sums added in wave order through LDS.
+// k_mx_rows (up to 16 rows of a): 16 weight rows per workgroup, the whole K
+// cut over 8 waves in chunks of C steps of 128, operands straight from global
+// memory into registers, the waves' sums added in wave order through LDS.
+// Bound by the weights' way from HBM: every wave has two chunks' loads under
+// way, 72 KiB per CU with C = 4, more than latency times bandwidth.  A step's
+// weight load reads 64 consecutive bytes of 16 rows; C steps' scales are one
+// load per row, and a lane shifts its block's byte to the bottom.
 constexpr int kRowWaves = 8;
 
-template <int FMT, int MT, bool EXACT>
-__global__ __launch_bounds__(64 * kRowWaves) void k_mx_rows(const uint8_t* __restrict__ a_codes,
-                                                            const uint8_t* __restrict__ a_scales,
-                                                            const uint8_t* __restrict__ w_codes,
-                                                            const uint8_t* __restrict__ w_scales, void* __restrict__ y,
-                                                            int M, int N, int K, int out_f32) {
-  __shared__ f32x4_t red[kRowWaves][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int FMT, bool EXACT, int C>
+__global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __restrict__ a_codes,
+                                                               const uint8_t* __restrict__ a_scales,
+                                                               const uint8_t* __restrict__ w_codes,
+                                                               const uint8_t* __restrict__ w_scales,
+                                                               void* __restrict__ y, int M, int N, int K,
+                                                               int out_f32) {
+  __shared__ f32x4_t red[kRowWaves][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16 * MT;
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
   const int nb = K / 32;  // scale blocks per row
   constexpr int kBlockBytes = FMT == kMxFp4 ? 16 : 32;
-  const int64_t wrow = min(n0 + r, N - 1);  // rows past the end: computed, not stored
+  const int64_t wrow = min(n0 + r, N - 1), arow = min(m0 + r, M - 1);  // rows past the end: computed, not stored
   const uint8_t* wc = w_codes + wrow * (K / 2);
   const uint8_t* wsc = w_scales + wrow * nb;
-  const uint8_t *ac[MT], *asc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int64_t arow = min(m0 + 16 * t + r, M - 1);
-    ac[t] = a_codes + arow * ((int64_t)nb * kBlockBytes);
-    asc[t] = a_scales + arow * nb;
-  }
-  f32x4_t acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const uint8_t* ac = a_codes + arow * ((int64_t)nb * kBlockBytes);
+  const uint8_t* asc = a_scales + arow * nb;
 
-  for (int c = wave; c * 16 < nb; c += kRowWaves) {
+  struct Chunk {
+    u32x4_t w[C], a[C], a1[FMT == kMxFp8 ? C : 1];
+    uint32_t ws[C], as[C];
+  };
+  auto load = [&](Chunk& o, int c) {
+    const int b0 = 4 * C * c;  // first block
+    if (b0 + 4 * C <= nb) {
+      __builtin_memcpy(o.ws, wsc + b0, 4 * C);
+      __builtin_memcpy(o.as, asc + b0, 4 * C);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int b0 = 16 * c + 4 * j;  // the step's 4 blocks; those past K are read from the last and weigh zero
-      const int b = min(b0 + q, nb - 1);
-      u32x4_t w = load16(wc + 16 * (int64_t)b);
-      if (b0 + q >= nb) w = u32x4_t{0, 0, 0, 0};
-      const uint32_t ws = wsc[b];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        u32x4_t x0, x1;
+      for (int j = 0; j < C; ++j) {
+        o.w[j] = load16(wc + 16 * (int64_t)(b0 + 4 * j + q));
         if constexpr (FMT == kMxFp4) {
-          x0 = x1 = load16(ac[t] + 16 * (int64_t)b);
+          o.a[j] = load16(ac + 16 * (int64_t)(b0 + 4 * j + q));
         } else {
-          x0 = load16(ac[t] + 32 * (int64_t)min(b0 + q / 2, nb - 1) + 16 * (q & 1));
-          x1 = load16(ac[t] + 32 * (int64_t)min(b0 + 2 + q / 2, nb - 1) + 16 * (q & 1));
+          o.a[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 16 * q);
+          o.a1[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 64 + 16 * q);
         }
-        acc[t] = mma16<FMT, EXACT>(w, ws, x0, x1, asc[t][b], acc[t]);
+      }
+    } else {  // the last blocks of the rows: those past K are zeros with scale one
+      const u32x4_t zero = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int b = b0 + 4 * j;
+        o.w[j] = b + q < nb ? load16(wc + 16 * (int64_t)(b + q)) : zero;
+        o.ws[j] = (b + q < nb ? wsc[b + q] : 127u) << (8 * q);
+        o.as[j] = (b + q < nb ? asc[b + q] : 127u) << (8 * q);
+        if constexpr (FMT == kMxFp4) {
+          o.a[j] = b + q < nb ? load16(ac + 16 * (int64_t)(b + q)) : zero;
+        } else {
+          o.a[j] = b + q / 2 < nb ? load16(ac + 32 * (int64_t)b + 16 * q) : zero;
+          o.a1[j] = b + 2 + q / 2 < nb ? load16(ac + 32 * (int64_t)b + 64 + 16 * q) : zero;
+        }
       }
     }
-  }
+  };
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const Chunk& o) {
 #pragma unroll
-  for (int t = 0; t < MT; ++t) red[wave][t][lane] = acc[t];
+    for (int j = 0; j < C; ++j)
+      acc = mma16<FMT, EXACT>(o.w[j], o.ws[j] >> (8 * q), o.a[j], o.a1[FMT == kMxFp8 ? j : 0], o.as[j] >> (8 * q), acc);
+  };
+  Chunk even, odd;
+  int c = wave;
+  if (c * 4 * C < nb) load(even, c);
+  for (; c * 4 * C < nb; c += 2 * kRowWaves) {
+    if ((c + kRowWaves) * 4 * C < nb) load(odd, c + kRowWaves);
+    multiply(even);
+    if ((c + kRowWaves) * 4 * C < nb) {
+      if ((c + 2 * kRowWaves) * 4 * C < nb) load(even, c + 2 * kRowWaves);
+      multiply(odd);
+    }
+  }
+  red[wave][lane] = acc;
   __syncthreads();
   // D of a 16x16 tile: lane l, value v -> weight row 4 (l / 16) + v, row l % 16 of a
-  for (int e = threadIdx.x; e < MT * 64; e += 64 * kRowWaves) {
-    const int t = e >> 6, l = e & 63;
-    f32x4_t s = red[0][t][l];
+  if (wave != 0) return;
 #pragma unroll
-    for (int w = 1; w < kRowWaves; ++w) s += red[w][t][l];
-    const int m = m0 + 16 * t + (l & 15), n = n0 + 4 * (l >> 4);
-    if (m >= M) continue;
+  for (int w = 1; w < kRowWaves; ++w) acc += red[w][lane];
+  const int m = m0 + r, n = n0 + 4 * q;
+  if (m >= M) return;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (n + v >= N) break;
-      const int64_t idx = (int64_t)m * N + n + v;
-      if (out_f32) static_cast<float*>(y)[idx] = s[v];
-      else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(s[v], 0.0f);
-    }
+  for (int v = 0; v < 4; ++v) {
+    if (n + v >= N) break;
+    const int64_t idx = (int64_t)m * N + n + v;
+    if (out_f32) static_cast<float*>(y)[idx] = acc[v];
+    else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(acc[v], 0.0f);
   }
 }
 
@@ -586,16 +611,14 @@ template <int FMT, bool EXACT>
 hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        hipStream_t stream) {
-  const int mt = m <= 16 ? 1 : m <= 32 ? 2 : m <= 48 ? 3 : 4;
-  const dim3 grid((unsigned)((n + 15) / 16), (unsigned)((m + 16 * mt - 1) / (16 * mt))), block(64 * kRowWaves);
+  const dim3 grid((unsigned)((n + 15) / 16), (unsigned)((m + 15) / 16)), block(64 * kRowWaves);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a_codes, a_scales, w_codes, w_scales, y, (int)m, (int)n, (int)k,
                        out_f32);
   };
-  if (mt == 1) go(k_mx_rows<FMT, 1, EXACT>);
-  else if (mt == 2) go(k_mx_rows<FMT, 2, EXACT>);
-  else if (mt == 3) go(k_mx_rows<FMT, 3, EXACT>);
-  else go(k_mx_rows<FMT, 4, EXACT>);
+  // chunks of 512 once every wave has one
+  if (k >= 512 * kRowWaves) go(k_mx_rows<FMT, EXACT, 4>);
+  else go(k_mx_rows<FMT, EXACT, 1>);
   return hipGetLastError();
 }
 
