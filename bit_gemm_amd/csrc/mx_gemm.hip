@@ -68,14 +68,17 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32
 __device__ __forceinline__ u32x4_t load16(const uint8_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 // ---------------------------------------------------------------------------
-// k_mx_rows (up to 16 rows of a): 16 weight rows per workgroup, the whole K
-// cut over 8 waves in chunks of C steps of 128, operands straight from global
-// memory into registers, the waves' sums added in wave order through LDS.
-// Bound by the weights' way from HBM: every wave has two chunks' loads under
-// way, 72 KiB per CU with C = 4, more than latency times bandwidth.  A step's
-// weight load reads 64 consecutive bytes of 16 rows; C steps' scales are one
-// load per row, and a lane shifts its block's byte to the bottom.
+// k_mx_rows (up to 16 rows of a): a workgroup per CU walks tiles of 16 weight
+// rows, the whole K of each cut over its 8 waves in chunks of C steps of 128,
+// operands straight from global memory into registers, the waves' sums added in
+// wave order through LDS.  Bound by the weights' way from HBM: every wave has
+// two chunks' loads under way, 72 KiB per CU with C = 4, more than latency
+// times bandwidth, and they run on across tiles.  Where a wave has one chunk
+// of K, its part of a stays in registers.  A step's weight load reads 64
+// consecutive bytes of 16 rows; C steps' scales are one load per row, and a
+// lane shifts its block's byte to the bottom.
 constexpr int kRowWaves = 8;
+constexpr int kRowGroups = 256;  // workgroups: one per CU
 
 template <int FMT, bool EXACT, int C>
 __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __restrict__ a_codes,
@@ -84,15 +87,13 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
                                                                const uint8_t* __restrict__ w_scales,
                                                                void* __restrict__ y, int M, int N, int K,
                                                                int out_f32) {
-  __shared__ f32x4_t red[kRowWaves][64];
+  __shared__ f32x4_t red[2][kRowWaves][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = lane >> 4;
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
+  const int m0 = blockIdx.y * 16;
   const int nb = K / 32;  // scale blocks per row
   constexpr int kBlockBytes = FMT == kMxFp4 ? 16 : 32;
-  const int64_t wrow = min(n0 + r, N - 1), arow = min(m0 + r, M - 1);  // rows past the end: computed, not stored
-  const uint8_t* wc = w_codes + wrow * (K / 2);
-  const uint8_t* wsc = w_scales + wrow * nb;
+  const int64_t arow = min(m0 + r, M - 1);  // rows past the end: computed, not stored
   const uint8_t* ac = a_codes + arow * ((int64_t)nb * kBlockBytes);
   const uint8_t* asc = a_scales + arow * nb;
 
@@ -100,22 +101,35 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
     u32x4_t w[C], a[C], a1[FMT == kMxFp8 ? C : 1];
     uint32_t ws[C], as[C];
   };
-  auto load = [&](Chunk& o, int c) {
-    const int b0 = 4 * C * c;  // first block
+  const int per = max((nb + 4 * C * kRowWaves - 1) / (4 * C * kRowWaves), 1);  // chunks of a wave
+  // Item i of this wave: chunk wave + 8 (i % per) of tile blockIdx.x + gridDim.x (i / per).
+  const int tiles = (N + 15) / 16;
+  const int items = ((tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * per;
+  int at_tile = blockIdx.x, at_chunk = wave;  // of the next item to load
+  auto load = [&](Chunk& o, bool a_too) {
+    const int b0 = 4 * C * at_chunk;  // first block
+    const int64_t wrow = min(at_tile * 16 + r, N - 1);
+    const uint8_t* wc = w_codes + wrow * (K / 2);
+    const uint8_t* wsc = w_scales + wrow * nb;
+    at_chunk += kRowWaves;
+    if (at_chunk >= per * kRowWaves) at_chunk = wave, at_tile += gridDim.x;
     if (b0 + 4 * C <= nb) {
       __builtin_memcpy(o.ws, wsc + b0, 4 * C);
-      __builtin_memcpy(o.as, asc + b0, 4 * C);
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        o.w[j] = load16(wc + 16 * (int64_t)(b0 + 4 * j + q));
-        if constexpr (FMT == kMxFp4) {
-          o.a[j] = load16(ac + 16 * (int64_t)(b0 + 4 * j + q));
-        } else {
-          o.a[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 16 * q);
-          o.a1[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 64 + 16 * q);
+      for (int j = 0; j < C; ++j) o.w[j] = load16(wc + 16 * (int64_t)(b0 + 4 * j + q));
+      if (a_too) {
+        __builtin_memcpy(o.as, asc + b0, 4 * C);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+          if constexpr (FMT == kMxFp4) {
+            o.a[j] = load16(ac + 16 * (int64_t)(b0 + 4 * j + q));
+          } else {
+            o.a[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 16 * q);
+            o.a1[j] = load16(ac + 32 * (int64_t)(b0 + 4 * j) + 64 + 16 * q);
+          }
         }
       }
-    } else {  // the last blocks of the rows: those past K are zeros with scale one
+    } else {  // the end of the rows: blocks past K are zeros with scale one
       const u32x4_t zero = {0, 0, 0, 0};
 #pragma unroll
       for (int j = 0; j < C; ++j) {
@@ -138,31 +152,44 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
     for (int j = 0; j < C; ++j)
       acc = mma16<FMT, EXACT>(o.w[j], o.ws[j] >> (8 * q), o.a[j], o.a1[FMT == kMxFp8 ? j : 0], o.as[j] >> (8 * q), acc);
   };
-  Chunk even, odd;
-  int c = wave;
-  if (c * 4 * C < nb) load(even, c);
-  for (; c * 4 * C < nb; c += 2 * kRowWaves) {
-    if ((c + kRowWaves) * 4 * C < nb) load(odd, c + kRowWaves);
-    multiply(even);
-    if ((c + kRowWaves) * 4 * C < nb) {
-      if ((c + 2 * kRowWaves) * 4 * C < nb) load(even, c + 2 * kRowWaves);
-      multiply(odd);
+  // the sums of tile t, the turn-th of this workgroup: one wave adds and stores
+  auto finish = [&](int t, int turn) {
+    red[turn & 1][wave][lane] = acc;  // last read two turns ago, before the last turn's barrier
+    acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    __syncthreads();
+    if (wave != turn % kRowWaves) return;
+    f32x4_t s = red[turn & 1][0][lane];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) s += red[turn & 1][w][lane];
+    // D of a 16x16 tile: lane l, value v -> weight row 4 (l / 16) + v, row l % 16 of a
+    const int m = m0 + r, n = 16 * t + 4 * q;
+    if (m >= M) return;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (n + v >= N) break;
+      const int64_t idx = (int64_t)m * N + n + v;
+      if (out_f32) static_cast<float*>(y)[idx] = s[v];
+      else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(s[v], 0.0f);
     }
-  }
-  red[wave][lane] = acc;
-  __syncthreads();
-  // D of a 16x16 tile: lane l, value v -> weight row 4 (l / 16) + v, row l % 16 of a
-  if (wave != 0) return;
-#pragma unroll
-  for (int w = 1; w < kRowWaves; ++w) acc += red[w][lane];
-  const int m = m0 + r, n = n0 + 4 * q;
-  if (m >= M) return;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (n + v >= N) break;
-    const int64_t idx = (int64_t)m * N + n + v;
-    if (out_f32) static_cast<float*>(y)[idx] = acc[v];
-    else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(acc[v], 0.0f);
+  };
+  Chunk even, odd;
+  int turn = 0, left = per, t = blockIdx.x;
+  auto item = [&](const Chunk& o) {
+    multiply(o);
+    if (--left == 0) {
+      finish(t, turn++);
+      left = per;
+      t += gridDim.x;
+    }
+  };
+  load(even, true);
+  for (int i = 0; i < items; i += 2) {
+    if (i + 1 < items) load(odd, per > 1 || i == 0);
+    item(even);
+    if (i + 1 < items) {
+      if (i + 2 < items) load(even, per > 1);
+      item(odd);
+    }
   }
 }
 
@@ -611,7 +638,8 @@ template <int FMT, bool EXACT>
 hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        hipStream_t stream) {
-  const dim3 grid((unsigned)((n + 15) / 16), (unsigned)((m + 15) / 16)), block(64 * kRowWaves);
+  const int64_t tiles = (n + 15) / 16;
+  const dim3 grid((unsigned)(tiles < kRowGroups ? tiles : kRowGroups), (unsigned)((m + 15) / 16)), block(64 * kRowWaves);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a_codes, a_scales, w_codes, w_scales, y, (int)m, (int)n, (int)k,
                        out_f32);
