@@ -585,25 +585,36 @@ _OUT_CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
 def _need_all(dev, parts):
     """_need over (tensor, name, dtype, shape) parts, None tensors skipped:
-    every type and shape first, then GPU residence on device dev."""
+    every type and shape first, then GPU residence on device dev.  The
+    message is looked for only once something is wrong (a call at one token
+    is bound by the host)."""
+    index = dev.index
+    for t, _, dtype, shape in parts:
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda
+                                  and t.get_device() == index and t.is_contiguous()
+                                  and (shape is None or t.shape == shape)):
+            break
+    else:
+        return
     for t, name, dtype, shape in parts:
         if t is not None:
             _need(t, name, dtype, shape, gpu=False)
-    for t, name, _, _ in parts:
+    for t, name, dtype, _ in parts:
         if t is not None:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a GPU tensor")
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, the other arguments on {dev}")
+            _need(t, name, dtype, None, dev)
 
 
 def _call(dev, fn, *args):
     """fn(*args, stream) on dev's current stream, with dev as the current
     device (the library launches on the current one)."""
-    if torch.cuda.current_device() == dev.index:
-        return _check(fn(*args, _stream(dev)))
-    with torch.cuda.device(dev):
-        _check(fn(*args, _stream(dev)))
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != NVFP4_OK:
+        _check(status)
 
 
 def _out_code(dtype, name="out_dtype"):
@@ -635,16 +646,20 @@ class MXTensor:
         return (self.codes.shape[0], self.codes.shape[1] * (2 if self.fmt == MXFP4 else 1))
 
     def parts(self, name: str = ""):
-        """The (tensor, name, dtype, shape) pieces of a consistent matrix;
-        raises ValueError if its sizes are not those of one."""
-        if self.fmt != MXFP4 and self.fmt != MXFP8:
-            raise ValueError(f"{name}fmt must be MXFP4 or MXFP8, got {self.fmt}")
-        if not isinstance(self.codes, torch.Tensor) or self.codes.dim() != 2:
+        """(m, k, the (tensor, name, dtype, shape) pieces) of a consistent
+        matrix; raises ValueError if its sizes are not those of one."""
+        codes, fmt = self.codes, self.fmt
+        if fmt != MXFP4 and fmt != MXFP8:
+            raise ValueError(f"{name}fmt must be MXFP4 or MXFP8, got {fmt}")
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
             raise ValueError(f"{name}codes must be a 2-D uint8 tensor")
-        m, k = self.shape
+        m, k = codes.shape
+        if fmt == MXFP4:
+            k *= 2
         if k % 32 != 0:
             raise ValueError(f"{name}codes imply k={k}, not a multiple of 32")
-        return [(self.codes, name + "codes", torch.uint8, None), (self.scales, name + "scales", torch.uint8, (m, k // 32))]
+        return m, k, [(codes, name + "codes", torch.uint8, None),
+                      (self.scales, name + "scales", torch.uint8, (m, k // 32))]
 
     @staticmethod
     def empty(m: int, k: int, fmt: int, device) -> "MXTensor":
@@ -663,7 +678,7 @@ def _mx_out(out, m, k, fmt, dev):
         return MXTensor.empty(m, k, fmt, dev), []
     if not isinstance(out, MXTensor):
         raise ValueError("out must be an MXTensor")
-    parts = out.parts("out.")
+    parts = out.parts("out.")[2]
     if out.fmt != fmt or out.shape != (m, k):
         raise ValueError(f"out holds a {out.shape} matrix in format {out.fmt}, the result is {(m, k)} in format {fmt}")
     return out, parts
@@ -687,8 +702,7 @@ def quantize_mx(x: torch.Tensor, fmt: int = MXFP4, out: Optional[MXTensor] = Non
 
 def dequant_mx(q: MXTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of an MX matrix, as float32 or bfloat16."""
-    parts = q.parts()
-    m, k = q.shape
+    m, k, parts = q.parts()
     code = _out_code(dtype, "dtype")
     dev = q.codes.device
     _need_all(dev, parts + [(out, "out", dtype, (m, k))])
@@ -705,15 +719,15 @@ def mx_gemm_workspace_size(m: int, n: int, k: int, a_fmt: int) -> int:
 def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[m, n] = a[m, k] @ w[n, k]^T for MXFP4 or MXFP8 a and MXFP4 w."""
-    parts = a.parts("a.") + w.parts("w.")
-    m, k = a.shape
-    n, kw = w.shape
+    m, k, parts = a.parts("a.")
+    n, kw, w_parts = w.parts("w.")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if kw != k:
         raise ValueError(f"a has k={k}, w k={kw}")
     code = _out_code(out_dtype)
     dev = w.codes.device
+    parts += w_parts
     parts.append((out, "out", out_dtype, (m, n)))
     _need_all(dev, parts)
     L = lib()
@@ -733,8 +747,7 @@ def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfl
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx = dy @ w for bf16 [m, n] dy and MXFP4 w [n, k]: mx_gemm's gradient
     with respect to its activations, straight through their quantization."""
-    parts = w.parts("w.")
-    n, k = w.shape
+    n, k, parts = w.parts("w.")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2 or dy.shape[1] != n:
@@ -742,7 +755,8 @@ def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfl
     m = dy.shape[0]
     code = _out_code(out_dtype)
     dev = w.codes.device
-    _need_all(dev, [(dy, "dy", torch.bfloat16, None)] + parts + [(out, "out", out_dtype, (m, k))])
+    parts += [(dy, "dy", torch.bfloat16, None), (out, "out", out_dtype, (m, k))]
+    _need_all(dev, parts)
     L = lib()
     workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_mx_gemm_dx_workspace_size(m, n, k), dev)
     if out is None:
@@ -780,7 +794,7 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     if out is None:
         out = MXTensor.empty(m, k, fmt, dev)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(x)
+        residual_out = torch.empty_like(residual)
     if rstd is None:
         rstd = torch.empty(m, dtype=torch.float32, device=dev)
     _call(dev, lib().nvfp4_add_rmsnorm_mx, x.data_ptr(), _ptr(residual), weight.data_ptr(), wcode, eps, m, k, fmt,
