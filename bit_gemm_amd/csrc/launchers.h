@@ -191,11 +191,11 @@ hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uin
 hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits, int out_f32, hipStream_t stream);
 
 // Residual addition + RMS norm with MX output, and its gradient (workspace:
-// rmsnorm_backward_planes(m) fp32 rows of k).
+// rmsnorm_backward_planes(m, k) fp32 rows of k).
 hipError_t launch_add_rmsnorm_mx(const void* x, const void* residual, const void* weight, int w_f32, double eps,
                                  int64_t m, int64_t k, int fmt, void* residual_out, float* rstd, uint8_t* codes,
                                  uint8_t* scales, hipStream_t stream);
-int rmsnorm_backward_planes(int64_t m);
+int rmsnorm_backward_planes(int64_t m, int64_t k);
 hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd,
                                    const void* ds, void* dx, float* dweight, int64_t m, int64_t k, void* workspace,
                                    hipStream_t stream);

@@ -193,7 +193,7 @@ NVFP4_API int nvfp4_add_rmsnorm_mx(const void* x, const void* residual, const vo
 
 NVFP4_API size_t nvfp4_add_rmsnorm_backward_workspace_size(int64_t m, int64_t k) {
   if (m <= 0 || k <= 0 || k % 32 != 0 || k > kMaxNormK || m > kMaxTokens) return 0;
-  return (size_t)nvfp4::rmsnorm_backward_planes(m) * (size_t)k * sizeof(float);
+  return (size_t)nvfp4::rmsnorm_backward_planes(m, k) * (size_t)k * sizeof(float);
 }
 
 NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const void* weight, int weight_dtype,
@@ -205,6 +205,8 @@ NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const vo
   if (!dweight) return fail(NVFP4_ERR_INVALID_VALUE, "dweight is required");
   if (m > 0 && (!dh || !s || !weight || !rstd || !dx))
     return fail(NVFP4_ERR_INVALID_VALUE, "dh, s, weight, rstd and dx are required");
+  if (m > 0 && (dx == dh || dx == s))
+    return fail(NVFP4_ERR_INVALID_VALUE, "dx cannot be dh's or s's buffer: dweight reads them beside it");
   if (!aligned(dweight, 16) || (m > 0 && (!aligned(dh, 16) || !aligned(s, 16) || !aligned(weight, 16) ||
                                           !aligned(ds, 16) || !aligned(dx, 16))))
     return fail(NVFP4_ERR_MISALIGNED, "dh, s, weight, ds, dx and dweight must be 16-byte aligned");

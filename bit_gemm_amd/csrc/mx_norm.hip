@@ -43,7 +43,7 @@ __device__ __forceinline__ F row_sum(F v, F* part) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
   if constexpr (T > 64) {
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x % T >> 6] = v;
     __syncthreads();
     v = part[0];
 #pragma unroll
@@ -146,69 +146,134 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_rmsnorm_mx(
   }
 }
 
-// A workgroup of T threads walks rows blockIdx.x, + gridDim.x, ..., keeping
-// its share of dweight in registers; plane blockIdx.x of `planes` receives it.
-template <int T, int P, bool WF32>
-__global__ __launch_bounds__(T) void k_rmsnorm_backward(const u32x4_t* __restrict__ dh, const u32x4_t* __restrict__ s,
-                                                        const void* __restrict__ weight,
-                                                        const float* __restrict__ rstd, const u32x4_t* ds,
-                                                        u32x4_t* dx, float* __restrict__ planes, int64_t m, int k) {
-  __shared__ float part[2][T / 64];
-  const int t = threadIdx.x;
+// R rows at a time per workgroup, T threads each, rows R blockIdx.x + group,
+// + R gridDim.x, ...; every thread keeps its columns' share of dweight in
+// registers, the groups' shares meet in LDS at the end, and plane blockIdx.x of
+// `planes` receives the workgroup's.  Up to P = 2 pieces per thread the next
+// row is loaded before the current one's sum and the weight stays in registers;
+// wider rows have enough loads of their own under way.
+template <int T, int P, int R, bool WF32>
+__global__ __launch_bounds__(T* R) void k_rmsnorm_backward(const u32x4_t* __restrict__ dh,
+                                                           const u32x4_t* __restrict__ s,
+                                                           const void* __restrict__ weight,
+                                                           const float* __restrict__ rstd, const u32x4_t* ds,
+                                                           u32x4_t* dx, float* __restrict__ planes, int64_t m, int k) {
+  constexpr bool kAhead = P <= 2;
+  __shared__ float part[2][R][T > 64 ? T / 64 : 1];
+  __shared__ f32x4_t share[R > 1 ? 2 * T * P : 1];
+  const int t = threadIdx.x % T, group = threadIdx.x / T;
   const int np = k / 8;
-  float w[P][8], dw[P][8];
+  struct Row {
+    u32x4_t dh[P], s[P], ds[P];
+    float rstd;
+  };
+  auto load = [&](Row& o, int64_t row) {
+    const int64_t r0 = row * np;
+    o.rstd = rstd[row];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = t + T * i;
+      o.dh[i] = o.s[i] = o.ds[i] = u32x4_t{0, 0, 0, 0};
+      if (p < np) {
+        o.dh[i] = __builtin_nontemporal_load(dh + r0 + p);
+        o.s[i] = __builtin_nontemporal_load(s + r0 + p);
+        if (ds) o.ds[i] = __builtin_nontemporal_load(ds + r0 + p);
+      }
+    }
+  };
+  float w[kAhead ? P : 1][8], dw[P][8];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[i][j] = dw[i][j] = 0.0f;
-    if (t + T * i < np) load_weight8<WF32>(weight, t + T * i, w[i]);
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] = 0.0f;
+      if (t + T * i < np) load_weight8<WF32>(weight, t + T * i, w[i]);
+    }
   }
-  int parity = 0;
-  for (int64_t row = blockIdx.x; row < m; row += gridDim.x, parity ^= 1) {
-    const int64_t r0 = row * np;
-    const float rs = rstd[row];
-    u32x4_t a[P], b[P], d[P];
+  auto piece_weight = [&](int i, float (&o)[8]) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int p = t + T * i;
-      a[i] = b[i] = d[i] = u32x4_t{0, 0, 0, 0};
-      if (p < np) {
-        a[i] = dh[r0 + p];
-        b[i] = s[r0 + p];
-        if (ds) d[i] = ds[r0 + p];
-      }
+    for (int j = 0; j < 8; ++j) o[j] = kAhead ? w[kAhead ? i : 0][j] : 0.0f;
+    if constexpr (!kAhead) {
+      if (t + T * i < np) load_weight8<WF32>(weight, t + T * i, o);
     }
+  };
+  auto lo_hi = [](const u32x4_t& v, int j) { return j & 1 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]); };
+
+  const int64_t step = (int64_t)R * gridDim.x, first = (int64_t)R * blockIdx.x + group;
+  // the same number of turns in every group: the sums meet at barriers
+  const int turns = (int)((m - (int64_t)R * blockIdx.x + step - 1) / step);
+  Row cur, next;
+  if (kAhead && first < m) load(cur, first);
+  for (int turn = 0; turn < turns; ++turn) {
+    const int64_t row = first + turn * step;
+    const bool live = row < m;
+    if constexpr (kAhead) {
+      if (row + step < m) load(next, row + step);
+    } else {
+      if (live) load(cur, row);
+    }
+    const float rs = live ? cur.rstd : 0.0f;
     float dot = 0.0f;
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+      for (int i = 0; i < P; ++i) {
+        float wi[8];
+        piece_weight(i, wi);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float gh = j & 1 ? bf16_hi(a[i][j / 2]) : bf16_lo(a[i][j / 2]);
-        const float xh = (j & 1 ? bf16_hi(b[i][j / 2]) : bf16_lo(b[i][j / 2])) * rs;
-        dot = __builtin_fmaf(gh * w[i][j], xh, dot);
-        dw[i][j] = __builtin_fmaf(gh, xh, dw[i][j]);
-      }
-    }
-    const float c = row_sum<T>(dot, part[parity]) / (float)k;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int p = t + T * i;
-      if (p >= np) continue;
-      u32x4_t o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float gh = e ? bf16_hi(a[i][j]) : bf16_lo(a[i][j]);
-          const float xh = (e ? bf16_hi(b[i][j]) : bf16_lo(b[i][j])) * rs;
-          v[e] = rs * __builtin_fmaf(-xh, c, gh * w[i][2 * j + e]);
-          if (ds) v[e] += e ? bf16_hi(d[i][j]) : bf16_lo(d[i][j]);
+        for (int j = 0; j < 8; ++j) {
+          const float gh = lo_hi(cur.dh[i], j), xh = lo_hi(cur.s[i], j) * rs;
+          dot = __builtin_fmaf(gh * wi[j], xh, dot);
+          dw[i][j] = __builtin_fmaf(gh, xh, dw[i][j]);
         }
-        o[j] = pack_bf16(v[0], v[1]);
       }
-      dx[r0 + p] = o;
     }
+    const float c = row_sum<T>(dot, part[turn & 1][group]) / (float)k;
+    if (live) {
+      const int64_t r0 = row * np;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int p = t + T * i;
+        if (p >= np) continue;
+        float wi[8];
+        piece_weight(i, wi);
+        u32x4_t o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float xh = lo_hi(cur.s[i], 2 * j + e) * rs;
+            v[e] = rs * __builtin_fmaf(-xh, c, lo_hi(cur.dh[i], 2 * j + e) * wi[2 * j + e]);
+            if (ds) v[e] += lo_hi(cur.ds[i], 2 * j + e);
+          }
+          o[j] = pack_bf16(v[0], v[1]);
+        }
+        __builtin_nontemporal_store(o, dx + r0 + p);
+      }
+    }
+    if constexpr (kAhead) cur = next;
+  }
+  if constexpr (R > 1) {
+    for (int g = 1; g < R; ++g) {
+      __syncthreads();
+      if (group == g) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            share[2 * (t + T * i) + e] = f32x4_t{dw[i][4 * e], dw[i][4 * e + 1], dw[i][4 * e + 2], dw[i][4 * e + 3]};
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dw[i][j] += share[2 * (t + T * i) + j / 4][j % 4];
+      }
+    }
+    if (group != 0) return;
   }
   float* plane = planes + (int64_t)blockIdx.x * k;
 #pragma unroll
@@ -218,6 +283,85 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward(const u32x4_t* __restric
     f32x4_t* q = reinterpret_cast<f32x4_t*>(plane) + 2 * p;
     q[0] = f32x4_t{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
     q[1] = f32x4_t{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// Few rows (up to kFewRows): one launch, the first m workgroups a row each, the
+// others 64 columns of dweight each, which they sum from dh and s themselves:
+// 4 bytes per element read a second time, from the caches, against 8 per
+// element of a plane per one or two rows, and no second launch.
+template <int T, int P, bool WF32>
+__global__ __launch_bounds__(T) void k_rmsnorm_backward_few(const u32x4_t* __restrict__ dh,
+                                                            const u32x4_t* __restrict__ s,
+                                                            const void* __restrict__ weight,
+                                                            const float* __restrict__ rstd, const u32x4_t* ds,
+                                                            u32x4_t* dx, float* __restrict__ dweight, int m, int k) {
+  __shared__ float part[T / 64];
+  __shared__ float column[T / 8][65];
+  const int t = threadIdx.x, np = k / 8;
+  auto lo_hi = [](const u32x4_t& v, int j) { return j & 1 ? bf16_hi(v[j / 2]) : bf16_lo(v[j / 2]); };
+  if ((int)blockIdx.x >= m) {
+    const int c0 = 8 * ((int)blockIdx.x - m), p = c0 + (t & 7), slice = t >> 3;  // pieces of 8 columns
+    float dw[8] = {};
+    if (p < np) {
+      for (int row = slice; row < m; row += T / 8) {
+        const u32x4_t a = dh[(int64_t)row * np + p], b = s[(int64_t)row * np + p];
+        const float rs = rstd[row];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[j] = __builtin_fmaf(lo_hi(a, j), lo_hi(b, j) * rs, dw[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) column[slice][8 * (t & 7) + j] = dw[j];
+    __syncthreads();
+    if (t < 64 && 8 * c0 + t < k) {
+      float v = column[0][t];
+      for (int i = 1; i < T / 8; ++i) v += column[i][t];
+      dweight[8 * c0 + t] = v;
+    }
+    return;
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * np;
+  const float rs = rstd[blockIdx.x];
+  u32x4_t a[P], b[P], d[P];
+  float g[P][8];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = t + T * i;
+    a[i] = b[i] = d[i] = u32x4_t{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[i][j] = 0.0f;
+    if (p < np) {
+      a[i] = dh[r0 + p];
+      b[i] = s[r0 + p];
+      if (ds) d[i] = ds[r0 + p];
+      load_weight8<WF32>(weight, p, g[i]);
+    }
+  }
+  float dot = 0.0f;
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      g[i][j] *= lo_hi(a[i], j);
+      dot = __builtin_fmaf(g[i][j], lo_hi(b[i], j) * rs, dot);
+    }
+  const float c = row_sum<T>(dot, part) / (float)k;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    if (t + T * i >= np) continue;
+    u32x4_t o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[e] = rs * __builtin_fmaf(-(lo_hi(b[i], 2 * j + e) * rs), c, g[i][2 * j + e]);
+        if (ds) v[e] += lo_hi(d[i], 2 * j + e);
+      }
+      o[j] = pack_bf16(v[0], v[1]);
+    }
+    dx[r0 + t + T * i] = o;
   }
 }
 
@@ -238,8 +382,6 @@ __global__ __launch_bounds__(256) void k_dweight_sum(const float* __restrict__ p
   }
 }
 
-constexpr int kMaxPlanes = 512;  // two workgroups per CU
-
 template <int T, int P>
 void norm_rows(const void* x, const void* residual, const void* weight, int w_f32, double eps, int64_t m, int k,
                int fmt, void* residual_out, float* rstd, uint8_t* codes, uint8_t* scales, hipStream_t stream) {
@@ -256,16 +398,30 @@ void norm_rows(const void* x, const void* residual, const void* weight, int w_f3
     w_f32 ? go(k_add_rmsnorm_mx<T, P, kMxFp8, true>) : go(k_add_rmsnorm_mx<T, P, kMxFp8, false>);
 }
 
-template <int T, int P>
+template <int T, int P, int R>
 void backward_rows(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd, const void* ds,
                    void* dx, float* planes, int count, int64_t m, int k, hipStream_t stream) {
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(T), 0, stream, static_cast<const u32x4_t*>(dh),
+    hipLaunchKernelGGL(kernel, dim3((unsigned)count), dim3(T * R), 0, stream, static_cast<const u32x4_t*>(dh),
                        static_cast<const u32x4_t*>(s), weight, rstd, static_cast<const u32x4_t*>(ds),
                        static_cast<u32x4_t*>(dx), planes, m, k);
   };
-  w_f32 ? go(k_rmsnorm_backward<T, P, true>) : go(k_rmsnorm_backward<T, P, false>);
+  w_f32 ? go(k_rmsnorm_backward<T, P, R, true>) : go(k_rmsnorm_backward<T, P, R, false>);
 }
+
+template <int T, int P>
+void backward_few(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd, const void* ds,
+                  void* dx, float* dweight, int64_t m, int k, hipStream_t stream) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(m + (k + 63) / 64)), dim3(T), 0, stream,
+                       static_cast<const u32x4_t*>(dh), static_cast<const u32x4_t*>(s), weight, rstd,
+                       static_cast<const u32x4_t*>(ds), static_cast<u32x4_t*>(dx), dweight, (int)m, k);
+  };
+  w_f32 ? go(k_rmsnorm_backward_few<T, P, true>) : go(k_rmsnorm_backward_few<T, P, false>);
+}
+
+// Rows that a workgroup of the gradient works on at one time.
+int backward_group(int64_t k) { return k <= 512 ? 16 : k <= 4096 ? 4 : k <= 8192 ? 2 : 1; }
 
 }  // namespace
 
@@ -284,25 +440,44 @@ hipError_t launch_add_rmsnorm_mx(const void* x, const void* residual, const void
   return hipGetLastError();
 }
 
-int rmsnorm_backward_planes(int64_t m) { return (int)(m < kMaxPlanes ? m : kMaxPlanes); }
+// Up to here the columns are summed from dh and s again (both ways 2 KiB per
+// column at this number of rows).
+constexpr int64_t kFewRows = 512;
+
+// Planes of dweight (workgroups of 1024 threads): one per CU where there are
+// rows enough for each to take more than two turns, since a plane costs 8 bytes
+// of traffic per column.
+int rmsnorm_backward_planes(int64_t m, int64_t k) {
+  if (m <= kFewRows) return 0;
+  const int64_t groups = (m + backward_group(k) - 1) / backward_group(k), halves = (groups + 1) / 2;
+  return (int)(groups <= 64 ? groups : halves < 64 ? 64 : halves < 256 ? halves : 256);
+}
 
 hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd,
                                    const void* ds, void* dx, float* dweight, int64_t m, int64_t k, void* workspace,
                                    hipStream_t stream) {
-  const int kk = (int)k, count = rmsnorm_backward_planes(m);
+  const int kk = (int)k, count = rmsnorm_backward_planes(m, k);
+  if (count == 0) {
+    auto call = [&](auto f) { f(dh, s, weight, w_f32, rstd, ds, dx, dweight, m, kk, stream); };
+    if (k <= 2048) call(backward_few<256, 1>);
+    else if (k <= 4096) call(backward_few<512, 1>);
+    else if (k <= 8192) call(backward_few<1024, 1>);
+    else if (k <= 16384) call(backward_few<1024, 2>);
+    else if (k <= 32768) call(backward_few<1024, 4>);
+    else call(backward_few<1024, 8>);
+    return hipGetLastError();
+  }
   float* planes = static_cast<float*>(workspace);
   auto call = [&](auto f) { f(dh, s, weight, w_f32, rstd, ds, dx, planes, count, m, kk, stream); };
-  if (count > 0) {
-    if (k <= 512) call(backward_rows<64, 1>);
-    else if (k <= 2048) call(backward_rows<256, 1>);
-    else if (k <= 4096) call(backward_rows<256, 2>);
-    else if (k <= 8192) call(backward_rows<256, 4>);
-    else if (k <= 16384) call(backward_rows<512, 4>);
-    else if (k <= 32768) call(backward_rows<1024, 4>);
-    else call(backward_rows<1024, 8>);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  if (k <= 512) call(backward_rows<64, 1, 16>);
+  else if (k <= 2048) call(backward_rows<256, 1, 4>);
+  else if (k <= 4096) call(backward_rows<256, 2, 4>);
+  else if (k <= 8192) call(backward_rows<512, 2, 2>);
+  else if (k <= 16384) call(backward_rows<1024, 2, 1>);
+  else if (k <= 32768) call(backward_rows<1024, 4, 1>);
+  else call(backward_rows<1024, 8, 1>);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_dweight_sum, dim3((unsigned)(k / 32)), dim3(256), 0, stream, planes, dweight, count, kk);
   return hipGetLastError();
 }

@@ -506,11 +506,12 @@ NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uin
  * s, rstd    residual_out (x without a residual) and rstd of the forward.
  * ds         device bf16 [m, k] or NULL: the gradient that reaches s by the
  *            residual branch; may be dx's own buffer.
- * dx         device bf16 [m, k].
+ * dx         device bf16 [m, k]; not dh's or s's buffer.
  * dweight    device fp32 [k], written whole (zeros when m == 0).
  * workspace  device, >= nvfp4_add_rmsnorm_backward_workspace_size(m, k)
- *            bytes, 16-byte aligned: fp32 partial sums of dweight, added in
- *            a fixed order by a second launch.
+ *            bytes, 16-byte aligned (0 for few rows: NULL allowed, one
+ *            launch): fp32 partial sums of dweight, added in a fixed order by
+ *            a second launch.
  */
 NVFP4_API int nvfp4_add_rmsnorm_mx(const void* x, const void* residual, const void* weight, int weight_dtype,
                                    float eps, int64_t m, int64_t k, int format, void* residual_out, float* rstd,

@@ -75,13 +75,17 @@ def test_norm(L):
     assert f(x=ODD) == 3 and f(w=ODD) == 3 and f(rs=FAKE + 2) == 3 and f(r=FAKE, ro=ODD) == 3
     assert f(m=0, x=None, w=None, c=None, s=None, rs=None) == 0
 
-    def b(dh=FAKE, s=FAKE, w=FAKE, wt=0, rs=FAKE, ds=None, dx=FAKE, dw=FAKE, m=4, k=64, wsp=FAKE, wsb=1 << 30):
+    def b(dh=FAKE, s=FAKE, w=FAKE, wt=0, rs=FAKE, ds=None, dx=FAKE + 16, dw=FAKE, m=4, k=64, wsp=FAKE, wsb=1 << 30):
         return L.nvfp4_add_rmsnorm_backward(dh, s, w, wt, rs, ds, dx, dw, m, k, wsp, wsb, None)
 
     assert b(k=48) == 2 and b(k=0) == 2 and b(m=-1) == 1 and b(wt=2) == 1 and b(dw=None) == 1 and b(dx=None) == 1
     assert b(rs=None) == 1 and b(dh=ODD) == 3 and b(ds=ODD) == 3 and b(dw=ODD) == 3
-    need = L.nvfp4_add_rmsnorm_backward_workspace_size(4, 64)
-    assert need >= 64 * 4 and b(wsb=need - 1) == 4 and b(wsp=None, wsb=need) == 1 and b(wsp=ODD, wsb=need) == 3
+    assert b(dx=FAKE + 64, dh=FAKE + 64) == 1 and b(dx=FAKE + 64, s=FAKE + 64) == 1  # only ds may be dx
+    assert L.nvfp4_add_rmsnorm_backward_workspace_size(4, 64) == 0  # few rows: one launch
+    need = L.nvfp4_add_rmsnorm_backward_workspace_size(9000, 64)
+    big = dict(m=9000, dx=FAKE + 64)
+    assert need >= 64 * 4 and b(**big, wsb=need - 1) == 4
+    assert b(**big, wsp=None, wsb=need) == 1 and b(**big, wsp=ODD, wsb=need) == 3
     assert L.nvfp4_add_rmsnorm_backward_workspace_size(0, 64) == 0
 
 
