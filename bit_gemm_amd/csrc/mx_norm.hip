@@ -365,21 +365,31 @@ __global__ __launch_bounds__(T) void k_rmsnorm_backward_few(const u32x4_t* __res
   }
 }
 
-// dweight = sum of the planes [count, k]: 32 columns per workgroup (8 lanes
-// of 4), the planes cut over 32 slices, summed in a fixed order.
+// dweight = sum of the planes [count, k], count <= 256: 32 columns per
+// workgroup (8 lanes of 4), the planes cut over 32 slices of up to 8 loads, all
+// under way at once, summed in a fixed order.
+constexpr int kMaxPlanes = 256;
 __global__ __launch_bounds__(256) void k_dweight_sum(const float* __restrict__ planes, float* __restrict__ dweight,
                                                      int count, int k) {
-  __shared__ f32x4_t part[32][8];
+  __shared__ f32x4_t part[4][8];
   const int c = threadIdx.x & 7, slice = threadIdx.x >> 3;
   const f32x4_t* p = reinterpret_cast<const f32x4_t*>(planes) + (int64_t)blockIdx.x * 8 + c;
-  f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int g = slice; g < count; g += 32) v += p[(int64_t)g * (k / 4)];
-  part[slice][c] = v;
-  __syncthreads();
-  if (slice == 0) {
-    for (int i = 1; i < 32; ++i) v += part[i][c];
-    reinterpret_cast<f32x4_t*>(dweight)[blockIdx.x * 8 + c] = v;
+  f32x4_t v[kMaxPlanes / 32];
+#pragma unroll
+  for (int i = 0; i < kMaxPlanes / 32; ++i) {
+    const int g = slice + 32 * i;
+    v[i] = g < count ? p[(int64_t)g * (k / 4)] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
+#pragma unroll
+  for (int i = 1; i < kMaxPlanes / 32; ++i) v[0] += v[i];
+#pragma unroll
+  for (int off = 8; off < 64; off <<= 1)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[0][e] += __shfl_xor(v[0][e], off, 64);
+  if ((threadIdx.x & 63) < 8) part[threadIdx.x >> 6][c] = v[0];
+  __syncthreads();
+  if (threadIdx.x < 8)
+    reinterpret_cast<f32x4_t*>(dweight)[blockIdx.x * 8 + c] = (part[0][c] + part[1][c]) + (part[2][c] + part[3][c]);
 }
 
 template <int T, int P>
@@ -444,13 +454,11 @@ hipError_t launch_add_rmsnorm_mx(const void* x, const void* residual, const void
 // column at this number of rows).
 constexpr int64_t kFewRows = 512;
 
-// Planes of dweight (workgroups of 1024 threads): one per CU where there are
-// rows enough for each to take more than two turns, since a plane costs 8 bytes
-// of traffic per column.
+// Planes of dweight: workgroups of 1024 threads, at most one per CU.
 int rmsnorm_backward_planes(int64_t m, int64_t k) {
   if (m <= kFewRows) return 0;
-  const int64_t groups = (m + backward_group(k) - 1) / backward_group(k), halves = (groups + 1) / 2;
-  return (int)(groups <= 64 ? groups : halves < 64 ? 64 : halves < 256 ? halves : 256);
+  const int64_t groups = (m + backward_group(k) - 1) / backward_group(k);
+  return (int)(groups < kMaxPlanes ? groups : kMaxPlanes);
 }
 
 hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* weight, int w_f32, const float* rstd,
