@@ -23,7 +23,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["quantize.hip", "dequant.hip", "gemm_skinny.hip", "gemm_tiled.hip", "gptq.hip", "act_quant.hip", "gemm_dx.hip", "selftest.hip", "stream.hip", "noalloc.hip", "hessian.hip",
-           "mx_quant.hip", "mx_gemm.hip", "mx_norm.hip", "mx_api.cpp", "api.cpp"]
+           "mx_quant.hip", "mx_gemm.hip", "mx_dx.hip", "mx_norm.hip", "mx_api.cpp", "api.cpp"]
 
 
 def hipcc() -> str:

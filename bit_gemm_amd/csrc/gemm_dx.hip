@@ -406,9 +406,7 @@ hipError_t launch_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_
 hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
                              int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace,
                              hipStream_t stream) {
-  hipError_t e = launch_dx<true>(dy, codes, scales, nullptr, dx, m, n, k, out_f32, p, workspace, stream);
-  if (e != hipSuccess || p.splits == 1) return e;
-  return launch_plane_sum(static_cast<const float*>(workspace), dx, m * k, p.splits, out_f32, stream);
+  return launch_dx<true>(dy, codes, scales, nullptr, dx, m, n, k, out_f32, p, workspace, stream);
 }
 
 }  // namespace nvfp4

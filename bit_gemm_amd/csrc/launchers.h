@@ -167,10 +167,9 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, void* 
                              int out_f32, hipStream_t stream);
 
 // y[m, n] = a[m, k] . w[n, k]^T, a in MXFP4 or MXFP8, w in MXFP4.  tile: 0 =
-// the kernel for few rows of a, else 64, 128 or 256: that many squared
-// outputs per workgroup with K
-// split over `splits` of them, `stages_per` LDS stages each (fp32 planes
-// [splits, m, n] in the workspace, then launch_plane_sum).
+// the kernel for few rows of a, else 64, 128 or 256: that many squared outputs
+// per workgroup with K split over `splits` of them, `stages_per` LDS stages
+// each (fp32 planes [splits, m, n] in the workspace, then launch_plane_sum).
 struct MxPlan {
   int tile;
   int splits;
@@ -182,7 +181,12 @@ hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream);
 
-// dx[m, k] = dy[m, n] . w[n, k], w in MXFP4 (the plan of launch_gemm_dx).
+// dx[m, k] = dy[m, n] . w[n, k], w in MXFP4.  tile as above (128 or 256; 0 =
+// the kernel of launch_gemm_dx), stages_per in steps of 64 n.
+MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k);
+hipError_t launch_mx_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
+                        int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream);
+// The same by launch_gemm_dx's kernel (its plan), without the sum of its planes.
 hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
                              int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace, hipStream_t stream);
 

@@ -147,7 +147,7 @@ NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
 }
 
 NVFP4_API size_t nvfp4_mx_gemm_dx_workspace_size(int64_t m, int64_t n, int64_t k) {
-  return product_sizes_ok(m, n, k) ? nvfp4::plan_gemm_dx(m, n, k).ws_bytes : 0;
+  return product_sizes_ok(m, n, k) ? nvfp4::plan_mx_dx(m, n, k).ws_bytes : 0;
 }
 
 NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uint8_t* w_scales, void* dx, int64_t m,
@@ -162,9 +162,9 @@ NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uin
     return fail(NVFP4_ERR_INVALID_VALUE, "dy, w_codes and w_scales are required");
   if (!aligned(dx, 16) || (n > 0 && (!aligned(dy, 16) || !aligned(w_codes, 16) || !aligned(w_scales, 16))))
     return fail(NVFP4_ERR_MISALIGNED, "dy, w_codes, w_scales and dx must be 16-byte aligned");
-  const nvfp4::DxPlan plan = nvfp4::plan_gemm_dx(m, n, k);
+  const nvfp4::MxPlan plan = nvfp4::plan_mx_dx(m, n, k);
   if ((st = check_workspace(workspace, workspace_bytes, plan.ws_bytes)) || (st = device_ok())) return st;
-  return done(nvfp4::launch_mx_gemm_dx(static_cast<const uint16_t*>(dy), w_codes, w_scales, dx, m, n, k,
+  return done(nvfp4::launch_mx_dx(static_cast<const uint16_t*>(dy), w_codes, w_scales, dx, m, n, k,
                                        out_dtype == NVFP4_F32, plan, workspace, hs(stream)),
               "mx_gemm_dx launch");
 }

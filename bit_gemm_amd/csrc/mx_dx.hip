@@ -1,0 +1,297 @@
+// Input gradient of a product with MXFP4 weights on gfx950: dx[m, k] = sum over
+// n of dy[m, n] w[n, k], bf16 dy, fp32 accumulation, one rounding to the output
+// type, on v_mfma_f32_32x32x16_bf16 (the reduction runs across the weights'
+// blocks, so the scaled instructions, one scale per 32 of the reduction, do not
+// apply).
+//
+// 4 waves, 2 x 2, each NT x MT products of 32 x 32: 64 NT weight columns x 64 MT
+// rows of dy per workgroup, the reduction in steps of 64 weight rows, two LDS
+// buffers:
+//  * dy (64 MT rows x 64 n) by DMA, 16-byte pieces permuted (swizzle);
+//  * the weights dequantized: the conversion turns two codes and their scale
+//    into two bf16 values, exactly (at most 2 significant bits times a power of
+//    two), in one instruction; a thread converts 16 NT columns of one row and
+//    stores them in 16-byte pieces of a row-major LDS row.
+// A product's weight operand (8 consecutive n of one column per lane) is two
+// transposing LDS reads: within each 16-lane group, lane i receives element i %
+// 4 of the 4-element reads of lanes i / 4 + 4 j, j = 0 .. 3.
+//
+// What bounds it: at 256 x 256 a step is 256 products per SIMD's worth of 32
+// clocks (2048) against 192 KiB through LDS (about 1500); at 128 x 128 the LDS
+// needs longer than the products, so that tile serves where there are too few
+// outputs for the large one.  Operands are read a step of 16 ahead, and the
+// waves meet before the last of a buffer's four steps, as in mx_gemm.hip.
+#include "launchers.h"
+#include "mx_tile.h"
+
+#pragma clang fp contract(off)
+
+namespace nvfp4 {
+namespace {
+
+// LDS DMA of 16 bytes per lane to LDS address `to` (wave-uniform) + 16 lane,
+// from src, or from base + a 32-bit offset per lane.  As inline asm: the
+// compiler holds back every transposing LDS read until all copies it knows of
+// have landed, the ones into the other buffer too.  They write no register, and
+// the kernel waits for them itself (wait_vm_all before the waves meet).
+__device__ __forceinline__ void copy16_unseen(const uint8_t* src, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "m0");
+#endif
+}
+__device__ __forceinline__ void copy16_unseen(const uint8_t* base, uint32_t offset, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(offset), "s"(base) : "m0");
+#endif
+}
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p);
+}
+
+typedef short v4i16_t __attribute__((ext_vector_type(4)));
+typedef short v8i16_t __attribute__((ext_vector_type(8)));
+
+template <int NT_, int MT_>
+struct DxTile {
+  static constexpr int NT = NT_, MT = MT_, TK = 64 * NT, TM = 64 * MT;
+  static constexpr int kRow = 2 * TK + 32;  // bytes of an LDS row of weights, padded
+  static constexpr int kDy = TM * 128, kW = 64 * kRow, kBuffer = kDy + kW;
+  static constexpr int ND = kDy / 4096;     // DMA instructions per wave and step
+  static constexpr int kLds = 2 * kBuffer > 4 * kSlabBytes<NT> ? 2 * kBuffer : 4 * kSlabBytes<NT>;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
+    const uint16_t* __restrict__ dy, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+    void* __restrict__ dx, float* __restrict__ planes, int M, int N, int K, int tiles_m, int tiles_k, int steps_per,
+    int out_f32) {
+  constexpr int NT = T::NT, MT = T::MT, TK = T::TK, TM = T::TM;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const TilePlace place = tile_place(tiles_m, tiles_k);
+  const int m0 = place.m * TM, k0 = place.n * TK;
+  const int s0 = blockIdx.y * steps_per, ns = min((N + 63) / 64 - s0, steps_per);  // >= 1
+
+  // dy: instruction i of this wave copies 8 rows, lane l piece (l % 8) ^ swizzle
+  // of row l / 8 (rows past M read row M - 1, pieces past N zeros)
+  uint32_t off[T::ND];
+  const uint8_t* dbase = reinterpret_cast<const uint8_t*>(dy + (int64_t)m0 * N);
+#pragma unroll
+  for (int i = 0; i < T::ND; ++i) {
+    const int r = 8 * (wave + 4 * i) + (lane >> 3);
+    off[i] = (uint32_t)min(r, M - 1 - m0) * (uint32_t)(2 * N) + 16 * ((lane & 7) ^ swizzle<8>(r));
+  }
+  const uint32_t lds0 = lds_address(lds);
+  auto copy = [&](int s, int buf, int i, auto wholec) {  // instruction i of step s
+    const uint8_t* p = dbase + 128 * (int64_t)(s0 + s);
+    const uint32_t to = lds0 + buf * T::kBuffer + 1024 * (wave + 4 * i);
+    if (decltype(wholec)::value || 64 * (s0 + s) + 64 <= N) {
+      copy16_unseen(p, off[i], to);
+    } else {
+      const int r = 8 * (wave + 4 * i) + (lane >> 3);
+      copy16_unseen(64 * (s0 + s) + 8 * ((lane & 7) ^ swizzle<8>(r)) < N ? p + off[i] : kZeros, to);
+    }
+  };
+  // weights: thread -> row wr of the step, columns 16 NT wq .. of the tile, in
+  // runs of 32 (or one of 32 at NT = 2: K is a multiple of 32, a run is inside
+  // or outside)
+  constexpr int kRuns = NT / 2;
+  const int wr = tid >> 2, wq = tid & 3;
+  struct Weights {
+    u32x4_t c[kRuns];
+    uint32_t s[kRuns];
+  };
+  auto load = [&](Weights& o, int s, auto wholec) {
+    const int n = 64 * (s0 + s) + wr;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const int k = k0 + 32 * (kRuns * wq + i);
+      o.c[i] = u32x4_t{0, 0, 0, 0};
+      o.s[i] = 127;
+      if ((decltype(wholec)::value || n < N) && k < K) {
+        o.c[i] = load16(codes + (int64_t)n * (K / 2) + k / 2);
+        o.s[i] = scales[(int64_t)n * (K / 32) + k / 32];
+      }
+    }
+  };
+  auto store = [&](const Weights& o, int buf) {
+    uint8_t* w = lds + buf * T::kBuffer + T::kDy + wr * T::kRow + 64 * kRuns * wq;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const float s = mx_scale(o.s[i]);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        const u32x4_t v = {
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 0)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 1)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 2)),
+            __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 3))};
+        *reinterpret_cast<u32x4_t*>(w + 64 * i + 16 * d) = v;
+      }
+    }
+  };
+  // The loads of w have arrived (they are counted with the copies: a use later
+  // on would wait for those as well).
+  auto arrived = [](Weights& o) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) asm volatile("" : "+v"(o.c[i]), "+v"(o.s[i]));
+#endif
+  };
+
+  f32x16_t acc[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.0f;
+  const int wk = (wave >> 1) * 32 * NT, wm = (wave & 1) * 32 * MT;
+  const int r = lane & 31, h = lane >> 5, sl = lane & 15, grp = lane >> 4;
+  struct Operands {
+    bf16x8_t d[MT];
+    v4i16_t lo[NT], hi[NT];
+  };
+  auto read = [&](Operands& o, int buf, int ks) {
+    const uint8_t* d = lds + buf * T::kBuffer + (wm + r) * 128 + 16 * ((2 * ks + h) ^ swizzle<8>(r));
+#pragma unroll
+    for (int i = 0; i < MT; ++i) o.d[i] = *reinterpret_cast<const bf16x8_t*>(d + 32 * 128 * i);
+    const uint8_t* w = lds + buf * T::kBuffer + T::kDy + (16 * ks + 8 * (grp >> 1) + (sl >> 2)) * T::kRow +
+                       2 * (wk + 16 * (grp & 1) + 4 * (sl & 3));
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      o.lo[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(w + 64 * i));
+      o.hi[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) v4i16_t*)(w + 64 * i + 4 * T::kRow));
+    }
+  };
+  // product p of a step's NT MT
+  auto multiply = [&](const Operands& o, int p) {
+    const int i = p / MT, j = p % MT;
+    const bf16x8_t w = __builtin_bit_cast(
+        bf16x8_t, v8i16_t{o.lo[i][0], o.lo[i][1], o.lo[i][2], o.lo[i][3], o.hi[i][0], o.hi[i][1], o.hi[i][2], o.hi[i][3]});
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w, o.d[j], acc[i][j], 0, 0, 0);
+  };
+  auto multiply_all = [&](const Operands& o) {
+#pragma unroll
+    for (int p = 0; p < NT * MT; ++p) multiply(o, p);
+  };
+  constexpr int kReads = 2 * NT + MT, kProducts = NT * MT;
+
+  // Step s reads buffer s % 2.  Its weights were loaded during step s - 2 and
+  // stored during step s - 1, its dy copied during step s - 1.
+  constexpr std::true_type kWhole;
+  constexpr std::false_type kAny;
+  Weights first, following;  // following: of step s + 1
+  load(first, 0, kAny);
+#pragma unroll
+  for (int i = 0; i < T::ND; ++i) copy(0, 0, i, kAny);
+  if (ns > 1) load(following, 1, kAny);
+  store(first, 0);
+  wait_vm_all();
+  __syncthreads();
+  arrived(following);
+  Operands o[2];
+  read(o[0], 0, 0);
+  if (ns > 1) {
+#pragma unroll
+    for (int i = 0; i < T::ND; ++i) copy(1, 1, i, kAny);
+  }
+  auto step = [&](int s, auto wholec) {
+    constexpr bool kAll = decltype(wholec)::value;  // step s + 2 exists and is whole
+    const int buf = s & 1;
+    Weights spare = following;
+    if (kAll || s + 2 < ns) load(spare, s + 2, wholec);
+    read(o[1], buf, 1);
+    multiply_all(o[0]);
+    interleave_step<kProducts, kReads, 0>();
+    hold_sums(acc);
+    read(o[0], buf, 2);
+    if (kAll || s + 1 < ns) store(following, buf ^ 1);
+    multiply_all(o[1]);
+#pragma unroll
+    for (int p = 0; p < kProducts; ++p) {
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a product
+      __builtin_amdgcn_sched_group_barrier(0x2, 5, 0);   // conversions
+      __builtin_amdgcn_sched_group_barrier(0x80, 2, 0);  // LDS reads and writes
+    }
+    hold_sums(acc);
+    read(o[1], buf, 3);
+    multiply_all(o[0]);
+    interleave_step<kProducts, kReads, 0>();
+    hold_sums(acc);
+    wait_vm_all();
+    meet();
+    arrived(spare);
+    read(o[0], buf ^ 1, 0);  // behind the last step: stale values, not used
+#pragma unroll
+    for (int p = 0; p < kProducts; ++p) {
+      multiply(o[1], p);
+      hold_sum<NT, MT, false>(acc[p / MT][p % MT]);
+      if ((p + 1) * T::ND / kProducts > p * T::ND / kProducts) {
+#pragma unroll
+        for (int i = p * T::ND / kProducts; i < (p + 1) * T::ND / kProducts; ++i)
+          if (kAll || s + 2 < ns) copy(s + 2, buf, i, wholec);
+      }
+    }
+    hold_sums(acc);
+    following = spare;
+  };
+  int s = 0;
+  for (const int all = min(ns, N / 64 - s0) - 2; s < all; ++s) step(s, kWhole);
+  for (; s < ns; ++s) step(s, kAny);
+  __syncthreads();  // the buffers' LDS becomes the output's
+  uint8_t* slab = lds + wave * kSlabBytes<NT>;
+  if (gridDim.y > 1) store_tile(acc, slab, planes + (int64_t)blockIdx.y * M * K, m0 + wm, k0 + wk, M, K);
+  else if (out_f32) store_tile(acc, slab, static_cast<float*>(dx), m0 + wm, k0 + wk, M, K);
+  else store_tile(acc, slab, static_cast<uint16_t*>(dx), m0 + wm, k0 + wk, M, K);
+}
+
+template <typename T>
+hipError_t launch_dx_tile(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
+                          int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream) {
+  hipError_t e = set_tile_lds<k_mx_dx<T>, T::kLds>();
+  if (e != hipSuccess) return e;
+  const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_k = (int)((k + T::TK - 1) / T::TK);
+  hipLaunchKernelGGL((k_mx_dx<T>), dim3((unsigned)(tiles_m * tiles_k), (unsigned)p.splits), dim3(256), T::kLds, stream,
+                     dy, codes, scales, dx, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_k,
+                     p.stages_per, out_f32);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k) {
+  MxPlan p{0, 1, 0, 0};
+  const int64_t steps = (n + 63) / 64;
+  auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((k + t - 1) / t); };
+  if (n % 8 != 0 || n == 0 || n > ((int64_t)1 << 22)) {  // rows of dy that DMA cannot read: k_gemm_dx
+    const DxPlan d = plan_gemm_dx(m, n, k);
+    p.splits = d.splits;
+    p.stages_per = d.steps_per;
+  } else {
+    p.tile = tiles(256) >= 160 ? 256 : 128;
+    int64_t splits = 1;
+    while (tiles(p.tile) * splits * 2 <= (p.tile == 256 ? 256 : 512) && steps / (splits * 2) >= 4) splits *= 2;
+    p.stages_per = (int)((steps + splits - 1) / splits);
+    p.splits = (int)((steps + p.stages_per - 1) / p.stages_per);
+  }
+  p.ws_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)k * sizeof(float) : 0;
+  return p;
+}
+
+hipError_t launch_mx_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
+                        int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream) {
+  hipError_t e;
+  if (p.tile == 256)
+    e = launch_dx_tile<DxTile<4, 4>>(dy, codes, scales, dx, m, n, k, out_f32, p, workspace, stream);
+  else if (p.tile == 128)
+    e = launch_dx_tile<DxTile<2, 2>>(dy, codes, scales, dx, m, n, k, out_f32, p, workspace, stream);
+  else
+    e = launch_mx_gemm_dx(dy, codes, scales, dx, m, n, k, out_f32, DxPlan{p.splits, p.stages_per, p.ws_bytes}, workspace,
+                          stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return launch_plane_sum(static_cast<const float*>(workspace), dx, m * k, p.splits, out_f32, stream);
+}
+
+}  // namespace nvfp4

@@ -19,9 +19,7 @@
 // of the other part) and multiplied twice: each part's products then span
 // fewer bits than the instruction keeps, and the sums are those of fp32.
 #include "launchers.h"
-#include "mx_device.h"
-
-#include <type_traits>
+#include "mx_tile.h"
 
 #pragma clang fp contract(off)
 
@@ -64,8 +62,6 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32
                                                             (int)as);
   }
 }
-
-__device__ __forceinline__ u32x4_t load16(const uint8_t* p) { return *reinterpret_cast<const u32x4_t*>(p); }
 
 // ---------------------------------------------------------------------------
 // k_mx_rows (up to 16 rows of a): a workgroup per CU walks tiles of 16 weight
@@ -223,21 +219,6 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
 // K / 32 bytes apart, so every row is a memory access of its own: fetching a
 // stage's 8 bytes per row cost as much time as the stage's codes (a 256 x 256
 // tile's 512 rows: 0.5 us against 0.65 us for 64 KiB of codes in whole lines).
-__device__ __align__(16) const uint8_t kZeros[16] = {};
-
-// A barrier behind this wave's LDS accesses that leaves its copies under way
-// (__syncthreads would wait for all of them).
-__device__ __forceinline__ void meet() {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-#endif
-}
-
-template <int P>
-__device__ __forceinline__ int swizzle(int r) {
-  return (r / (16 / P)) & (P - 1);
-}
-
 template <int FMT, int NT_, int MT_, int WN_, int S_, int B_, int G_>
 struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
@@ -249,7 +230,7 @@ struct Tile {
   static constexpr int SR = 2 * S * G;                                // scale bytes of a row per G stages
   static constexpr int NS = ((TM + TN) * SR / 16 + 255) / 256;        // 16-byte loads per thread for them
   static constexpr int kScales = (TM + TN) * SR, kAll = B * kStage + 2 * kScales;
-  static constexpr int kEpilogue = 4 * 32 * (32 * NT * 4 + 16);              // a padded 32-row fp32 slab per wave
+  static constexpr int kEpilogue = 4 * kSlabBytes<NT>;
   static constexpr int kLds = kAll > kEpilogue ? kAll : kEpilogue;
   static_assert(kA % 4096 == 0 && kW % 4096 == 0, "whole instructions");
   static_assert(B >= 2 && (S == 2 || S == 4) && G >= 2 && SR % 16 == 0 && kLds <= 160 * 1024, "stages");
@@ -266,14 +247,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   const int nb = K / 32;
   const int stages = (nb + 2 * S - 1) / (2 * S), whole = nb / (2 * S);
 
-  // Workgroups go round the 8 XCDs; each XCD takes a contiguous run of tiles,
-  // ordered in panels of 4 rows of tiles, so that the tiles it works on at one
-  // time share few rows of a and w in its L2.
-  const int tiles = tiles_m * tiles_n;
-  const int per = tiles / 8, rest = tiles % 8, xcd = blockIdx.x % 8;
-  const int tile = xcd * per + min(xcd, rest) + blockIdx.x / 8;
-  const int panel = tile / (4 * tiles_n), in = tile % (4 * tiles_n), high = min(4, tiles_m - 4 * panel);
-  const int m0 = (4 * panel + in % high) * TM, n0 = in / high * TN;
+  const TilePlace place = tile_place(tiles_m, tiles_n);
+  const int m0 = place.m * TM, n0 = place.n * TN;
   const int s0 = blockIdx.y * stages_per, ns = min(stages - s0, stages_per);  // >= 1
 
   const uint32_t apitch = nb * (FMT == kMxFp4 ? 16 : 32), wpitch = nb * 16;
@@ -427,39 +402,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
                                                                       j, (int)c.w[i], j, (int)c.a[m]);
       }
   };
-  // Order of a step: products of this one between the operand reads and the
-  // copies of later ones (reads first: a copy may not pass a read of LDS).
   constexpr int kReads = NT + (FMT == kMxFp8 ? 2 : 1) * MT, kProducts = NT * MT * (EXACT ? 2 : 1);
-  auto interleave = [&](auto readsc, auto copiesc) {
-    constexpr int reads = decltype(readsc)::value, slots = reads + decltype(copiesc)::value;
-#pragma unroll
-    for (int i = 0; i < slots; ++i) {
-      const int products = (i + 1) * kProducts / slots - i * kProducts / slots;
-      if (i == 0 || products > 0) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-      if (i > 0 && products > 1) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-      if (i > 0 && products > 2) __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
-      if (i < reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // an LDS read
-      else __builtin_amdgcn_sched_group_barrier(0x20, 1, 0);             // a copy
-    }
-  };
-
-  // Holds the sums where they are at this point.  At the end of a step: the
-  // compiler sees products as plain arithmetic and would gather those of a
-  // whole stage behind its reads and barrier.  (Sums of more than 128 registers
-  // live in the accumulation half of the register file.)
-  auto hold = [&](f32x16_t& v) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    if constexpr (NT * MT > 8) asm volatile("" : "+a"(v) : : "memory");
-    else asm volatile("" : "+v"(v) : : "memory");
-#endif
-  };
-  auto pin = [&] {
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int m = 0; m < MT; ++m) hold(acc[i][m]);
-  };
-
   // The copies of stage s + B go into the buffer of stage s: one half during
   // the last step of stage s, the other during the first of the next stage.
   constexpr std::true_type kWhole;
@@ -489,8 +432,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
       read(o[(j + 1) & 1], buf, j + 1);
       if (j == 0 && (kAll || s + B - 1 < ns)) copy(s + B - 1, prev, 1, wholec);
       multiply(o[j & 1], sc, jc);
-      interleave(std::integral_constant<int, kReads>{}, std::integral_constant<int, j == 0 ? NC - kFirst : 0>{});
-      pin();
+      interleave_step<kProducts, kReads, j == 0 ? NC - kFirst : 0>();
+      hold_sums(acc);
     };
     inner(std::integral_constant<int, 0>{});
     if constexpr (S == 4) {
@@ -509,8 +452,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     read(o[0], following, 0);
     if (kAll || s + B < ns) copy(s + B, buf, 0, wholec);
     multiply(o[(S - 1) & 1], sc, std::integral_constant<int, S - 1>{});
-    interleave(std::integral_constant<int, kReads + NT + MT>{}, std::integral_constant<int, kFirst>{});
-    pin();
+    interleave_step<kProducts, kReads + NT + MT, kFirst>();
+    hold_sums(acc);
     sc = next;
     prev = buf;
     buf = following;
@@ -520,55 +463,10 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   for (; s < ns; ++s) stage(s, kAny);
   __syncthreads();  // the stages' LDS becomes the output's
 
-  // D of a 32 x 32 product: lane l, value v -> weight row 8 (v / 4) + 4 h +
-  // v % 4, row l % 32 of a.  Each wave turns its rows of a, 32 at a time, in
-  // LDS, and stores whole runs of 32 NT outputs.
   uint8_t* slab = lds + wave * (T::kEpilogue / 4);
-  auto store = [&](auto* out) {
-    using E = std::remove_reference_t<decltype(*out)>;
-    constexpr int kPer = 16 / sizeof(E), kRuns = 32 * NT / kPer;  // outputs of a 16-byte piece, pieces of a slab row
-    constexpr int kPitch = 32 * NT * sizeof(E) + 16;
-    const bool vec = N % kPer == 0;
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) hold(acc[i][j]);  // no earlier copy of them in other registers
-#pragma unroll
-      for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4_t v = {acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
-          uint8_t* p = slab + r * kPitch + (32 * i + 8 * g + 4 * h) * sizeof(E);
-          if constexpr (sizeof(E) == 4) *reinterpret_cast<f32x4_t*>(p) = v;
-          else *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        }
-      u32x4_t v[kRuns / 2];
-#pragma unroll
-      for (int e = 0; e < kRuns / 2; ++e) {
-        const int at = lane + 64 * e;
-        v[e] = *reinterpret_cast<const u32x4_t*>(slab + at / kRuns * kPitch + at % kRuns * 16);
-      }
-#pragma unroll
-      for (int e = 0; e < kRuns / 2; ++e) {
-        const int at = lane + 64 * e, m = m0 + wm + 32 * j + at / kRuns, n = n0 + wn + at % kRuns * kPer;
-        if (m >= M || n >= N) continue;
-        E* q = out + (int64_t)m * N + n;
-        if (vec) {
-          *reinterpret_cast<u32x4_t*>(q) = v[e];
-        } else {
-#pragma unroll
-          for (int c = 0; c < kPer; ++c) {
-            if (n + c >= N) break;
-            if constexpr (sizeof(E) == 4) reinterpret_cast<uint32_t*>(q)[c] = v[e][c];
-            else q[c] = (E)(v[e][c >> 1] >> (16 * (c & 1)));
-          }
-        }
-      }
-    }
-  };
-  if (gridDim.y > 1) store(planes + (int64_t)blockIdx.y * M * N);
-  else if (out_f32) store(static_cast<float*>(y));
-  else store(static_cast<uint16_t*>(y));
+  if (gridDim.y > 1) store_tile(acc, slab, planes + (int64_t)blockIdx.y * M * N, m0 + wm, n0 + wn, M, N);
+  else if (out_f32) store_tile(acc, slab, static_cast<float*>(y), m0 + wm, n0 + wn, M, N);
+  else store_tile(acc, slab, static_cast<uint16_t*>(y), m0 + wm, n0 + wn, M, N);
 }
 
 // The tiles the library has (plan_mx_gemm chooses).  256 k per stage, but 128
@@ -585,24 +483,13 @@ int mx_tile_k(int fmt, int size) {
   return 64 * (size == 256 ? Tile256<kMxFp8>::S : size == 128 ? Tile128<kMxFp8>::S : Tile64<kMxFp8>::S);
 }
 
-// Opt in to kLds bytes of LDS, once per kernel.
-template <auto Kernel, int kLds>
-hipError_t set_lds_limit() {
-  static std::atomic<bool> done{false};
-  if (kLds <= 65536 || done.load(std::memory_order_relaxed)) return hipSuccess;
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(Kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                     kLds);
-  if (e == hipSuccess) done.store(true, std::memory_order_relaxed);
-  return e;
-}
-
 template <int FMT, bool EXACT, typename T>
 hipError_t launch_tile(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        const MxPlan& plan, void* workspace, hipStream_t stream) {
   const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_n = (int)((n + T::TN - 1) / T::TN);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits);
-  hipError_t e = set_lds_limit<k_mx_tile<FMT, EXACT, T>, T::kLds>();
+  hipError_t e = set_tile_lds<k_mx_tile<FMT, EXACT, T>, T::kLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_mx_tile<FMT, EXACT, T>), grid, dim3(256), T::kLds, stream, a_codes, a_scales, w_codes,
                      w_scales, y, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_n,

@@ -193,7 +193,7 @@ def test_gemm_empty():
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 64, 128), (17, 100, 96), (128, 256, 256), (300, 1001, 1056), (64, 4096, 1024),
-                                   (5, 33, 32), (200, 1024, 384)])
+                                   (5, 33, 32), (200, 1024, 384), (130, 72, 160), (3, 8, 32), (257, 584, 1312)])
 def test_gemm_dx(m, n, k):
     print("mx gemm_dx", m, n, k, flush=True)
     wc, ws = weights(n, k, 60 + n)
@@ -208,14 +208,31 @@ def test_gemm_dx(m, n, k):
         assert np.all(np.abs(y - ref) <= bound), dt
 
 
+@pytest.mark.parametrize("m,n,k", [(3500, 520, 3700 // 32 * 32), (4096, 64, 4128), (2600, 1000, 4096)])
+def test_gemm_dx_many_tiles(m, n, k):
+    # enough outputs for the large tile; sampled rows against the oracle
+    print("mx gemm_dx", m, n, k, flush=True)
+    g = torch.Generator(device="cuda").manual_seed(m)
+    dy = torch.randn(m, n, generator=g, device="cuda").bfloat16()
+    w = nv.quantize_mx(torch.randn(n, k, generator=g, device="cuda"))
+    wv = mx.dequant_mx(w.codes.cpu().numpy(), w.scales.cpu().numpy(), mx.FP4)
+    pick = np.unique(np.concatenate([[0, 31, 32, 127, 128, 255, 256, m - 1], np.random.default_rng(m).integers(0, m, 30)]))
+    d = _np(dy[torch.from_numpy(pick).cuda()])
+    ref, mag = d @ wv, np.abs(d) @ np.abs(wv)
+    for dt, half in ((torch.bfloat16, UBF16), (torch.float32, U32)):
+        bound = (n + 64) * 2 * U32 * mag * (1 + half) + half * np.abs(ref)
+        y = _np(nv.mx_gemm_dx(dy, w, out_dtype=dt)[torch.from_numpy(pick).cuda()])
+        assert np.all(np.abs(y - ref) <= bound), dt
+
+
 def test_gemm_dx_rows_and_empty():
     # one-hot gradients give the weights' rows exactly; scales span the format, a NaN scale stays in its block
     n, k = 128, 256
     g = np.random.default_rng(62)
     wc = g.integers(0, 256, (n, k // 2)).astype(np.uint8)
-    ws = g.integers(20, 230, (n, k // 32)).astype(np.uint8)
+    ws = g.integers(0, 252, (n, k // 32)).astype(np.uint8)
     w = mx.dequant_mx(wc, ws, mx.FP4).astype(np.float32)
-    for rows_ in (n, n - 3):  # both kernels: whole 64-row steps or not
+    for rows_ in (n, n - 3, n - 8):  # every kernel: whole 64-row steps or not, rows of dy of whole 16 bytes or not
         dx = nv.mx_gemm_dx(torch.eye(rows_, device="cuda").bfloat16(), _mx(wc[:rows_], ws[:rows_], nv.MXFP4),
                            out_dtype=torch.float32).cpu().numpy()
         assert np.array_equal(dx, w[:rows_])
