@@ -203,27 +203,29 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     Weights spare = following;
     if (kAll || s + 2 < ns) load(spare, s + 2, wholec);
     read(o[1], buf, 1);
+    __builtin_amdgcn_sched_barrier(0);
     multiply_all(o[0]);
-    interleave_step<kProducts, kReads, 0>();
     hold_sums(acc);
     read(o[0], buf, 2);
+    __builtin_amdgcn_sched_barrier(0);
     if (kAll || s + 1 < ns) store(following, buf ^ 1);
     multiply_all(o[1]);
 #pragma unroll
     for (int p = 0; p < kProducts; ++p) {
-      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);   // a product
-      __builtin_amdgcn_sched_group_barrier(0x2, 5, 0);   // conversions
-      __builtin_amdgcn_sched_group_barrier(0x80, 2, 0);  // LDS reads and writes
+      __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);    // a product
+      __builtin_amdgcn_sched_group_barrier(0x2, 4, 0);    // conversions
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // an LDS write
     }
     hold_sums(acc);
     read(o[1], buf, 3);
+    __builtin_amdgcn_sched_barrier(0);
     multiply_all(o[0]);
-    interleave_step<kProducts, kReads, 0>();
     hold_sums(acc);
     wait_vm_all();
     meet();
     arrived(spare);
     read(o[0], buf ^ 1, 0);  // behind the last step: stale values, not used
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int p = 0; p < kProducts; ++p) {
       multiply(o[1], p);
