@@ -21,12 +21,8 @@
 // the split reduction).  fp32 accumulation; s_t applied once.
 // Where n % 64 == 0 and k % 128 == 0, k_gemm_dx_tr replaces the transposed
 // stores with transposing LDS reads and brings dy in by LDS DMA (below).
-//
-// Both kernels take NVFP4 weights (MX = false: an E4M3 scale per 16 codes and
-// a tensor scale) or MXFP4 weights (MX = true: a power-of-two scale per 32
-// codes, no tensor scale; val * scale is a bf16 value there too).
 #include "launchers.h"
-#include "mx_device.h"
+#include "nvfp4_device.h"
 
 #pragma clang fp contract(off)
 
@@ -38,14 +34,6 @@ constexpr int kTM = 128;        // dy rows per workgroup
 constexpr int kTK = 128;        // weight columns (outputs) per workgroup
 constexpr int kTN = 64;         // weight rows (reduction) per step
 constexpr int kRow = kTN + 8;   // LDS row of 64 bf16 + 16 bytes of padding (bank spread, 16-byte aligned)
-
-// Codes per scale byte, and the factor of the whole product.
-template <bool MX>
-constexpr int kScaleRun = MX ? 32 : 16;
-template <bool MX>
-__device__ __forceinline__ float tensor_factor(const float* tensor_scale) {
-  return MX ? 1.0f : tensor_scale[0];
-}
 
 __device__ __forceinline__ uint32_t bf16_hi_exact(float f) { return __float_as_uint(f) >> 16; }
 
@@ -59,13 +47,12 @@ struct DxLoads {
 // D of a 32 x 32 tile: lane l, value v -> dy row 8 (v / 4) + 4 (l / 32) + v % 4,
 // weight column l % 32.  With a split reduction: raw fp32 partials to plane
 // z of the workspace (the reduction kernel applies s_t).
-template <bool MX>
 __device__ __forceinline__ void store_dx(const f32x16_t (&acc)[2][2], const float* tensor_scale, void* dx, float* ws,
                                          int M, int K, int mw, int kw, int out_f32) {
   const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
   const bool partial = gridDim.z > 1;
   float* plane = ws + (int64_t)blockIdx.z * M * K;
-  const float s_t = partial ? 1.0f : tensor_factor<MX>(tensor_scale);
+  const float s_t = partial ? 1.0f : tensor_scale[0];
 #pragma unroll
   for (int a = 0; a < 2; ++a) {
 #pragma unroll
@@ -89,7 +76,6 @@ __device__ __forceinline__ void store_dx(const f32x16_t (&acc)[2][2], const floa
   }
 }
 
-template <bool MX>
 __global__ __launch_bounds__(256) void k_gemm_dx(const uint16_t* __restrict__ dy,
                                                  const uint8_t* __restrict__ codes,
                                                  const uint8_t* __restrict__ scales,
@@ -137,7 +123,7 @@ __global__ __launch_bounds__(256) void k_gemm_dx(const uint16_t* __restrict__ dy
       const int n = n0 + 2 * wp + r;
       if (kin && n < N) {  // rows past N and blocks past K contribute zero
         L.code[r] = *reinterpret_cast<const uint2*>(codes + (int64_t)n * (K / 2) + kcol / 2);
-        L.sc[r] = scales[(int64_t)n * (K / kScaleRun<MX>) + kcol / kScaleRun<MX>];
+        L.sc[r] = scales[(int64_t)n * (K / 16) + kcol / 16];
       } else {
         L.code[r] = make_uint2(0u, 0u);
         L.sc[r] = 0u;
@@ -152,8 +138,7 @@ __global__ __launch_bounds__(256) void k_gemm_dx(const uint16_t* __restrict__ dy
       *reinterpret_cast<u32x4_t*>(&as[ar * kRow + 32 * ah + 8 * i]) = L.dy[i];
     // rows 2p and 2p + 1 of one block: 16 columns, each a bf16 pair (n, n + 1)
     float v0[16], v1[16];
-    const float s0 = MX ? mx_scale(L.sc[0]) : e4m3_decode(L.sc[0] & 0x7Fu);
-    const float s1 = MX ? mx_scale(L.sc[1]) : e4m3_decode(L.sc[1] & 0x7Fu);
+    const float s0 = e4m3_decode(L.sc[0] & 0x7Fu), s1 = e4m3_decode(L.sc[1] & 0x7Fu);
     dequant8_f32<kConvHw>(L.code[0].x, s0, v0);
     dequant8_f32<kConvHw>(L.code[0].y, s0, v0 + 8);
     dequant8_f32<kConvHw>(L.code[1].x, s1, v1);
@@ -208,7 +193,7 @@ __global__ __launch_bounds__(256) void k_gemm_dx(const uint16_t* __restrict__ dy
     __syncthreads();
   }
 
-  store_dx<MX>(acc, tensor_scale, dx, ws, M, K, m0 + wm, k0 + wk, out_f32);
+  store_dx(acc, tensor_scale, dx, ws, M, K, m0 + wm, k0 + wk, out_f32);
 }
 
 // ---------------------------------------------------------------------------
@@ -237,7 +222,6 @@ constexpr int kTrStage = kDyStage + kWStage;
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 
-template <bool MX>
 __global__ __launch_bounds__(256, 2) void k_gemm_dx_tr(const uint16_t* __restrict__ dy,
                                                     const uint8_t* __restrict__ codes,
                                                     const uint8_t* __restrict__ scales,
@@ -261,17 +245,15 @@ __global__ __launch_bounds__(256, 2) void k_gemm_dx_tr(const uint16_t* __restric
   // weights: thread -> row wr of the step, columns 32 wq .. +32 of the tile
   const int wr = tid >> 2, wq = tid & 3;
   const uint8_t* cp = codes + (int64_t)(s_begin * kTN + wr) * (K / 2) + k0 / 2 + 16 * wq;
-  constexpr int kRun = kScaleRun<MX>;
-  const uint8_t* sp = scales + (int64_t)(s_begin * kTN + wr) * (K / kRun) + k0 / kRun + 32 / kRun * wq;
+  const uint8_t* sp = scales + (int64_t)(s_begin * kTN + wr) * (K / 16) + k0 / 16 + 2 * wq;
   struct WRegs {
     u32x4_t c;   // 32 codes
-    uint32_t s;  // their scales: 2 bytes, MX 1
+    uint32_t s;  // 2 scale bytes
   };
   auto issue_w = [&](WRegs& R, int s) {
     s = min(s, nst - 1);  // past the last step: the last step again (not used)
     load_b128_async<0>(R.c, cp + (int64_t)s * kTN * (K / 2));
-    if constexpr (MX) load_u8_async<0>(R.s, sp + (int64_t)s * kTN * (K / kRun));
-    else load_u16_async<0>(R.s, sp + (int64_t)s * kTN * (K / kRun));
+    load_u16_async<0>(R.s, sp + (int64_t)s * kTN * (K / 16));
   };
   auto issue_dy = [&](int s) {
     const int st = s & 1;
@@ -282,8 +264,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_dx_tr(const uint16_t* __restric
   };
   auto store_w = [&](const WRegs& R, int st) {
     uint16_t* wl = reinterpret_cast<uint16_t*>(lds + st * kTrStage + kDyStage);
-    const float sg0 = MX ? mx_scale(R.s) : scale_at<kConvHw, 0>(R.s);
-    const float sg1 = MX ? sg0 : scale_at<kConvHw, 1>(R.s);
+    const float sg0 = scale_at<kConvHw, 0>(R.s), sg1 = scale_at<kConvHw, 1>(R.s);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<u32x4_t*>(wl + wr * kWRow + 32 * wq + 8 * i) = dequant8_bf16<kConvHw>(R.c[i], i < 2 ? sg0 : sg1);
@@ -353,7 +334,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_dx_tr(const uint16_t* __restric
     if (s + 1 < nst) step(s + 1, R1);
   }
   wait_vm_all();  // the tail's clamped loads land before the workgroup's LDS is released
-  store_dx<MX>(acc, tensor_scale, dx, ws, M, K, m0 + wm, k0 + wk, out_f32);
+  store_dx(acc, tensor_scale, dx, ws, M, K, m0 + wm, k0 + wk, out_f32);
 }
 
 }  // namespace
@@ -373,40 +354,24 @@ DxPlan plan_gemm_dx(int64_t m, int64_t n, int64_t k) {
   return p;
 }
 
-namespace {
-template <bool MX>
-hipError_t launch_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, const float* tensor_scale,
-                     void* dx, int64_t m, int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace,
-                     hipStream_t stream) {
+hipError_t launch_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales,
+                          const float* tensor_scale, void* dx, int64_t m, int64_t n, int64_t k,
+                          int out_f32, const DxPlan& p, void* workspace, hipStream_t stream) {
   const dim3 grid((unsigned)((k + kTK - 1) / kTK), (unsigned)((m + kTM - 1) / kTM), (unsigned)p.splits);
   float* ws = reinterpret_cast<float*>(workspace);
   if (n > 0 && n % kTN == 0 && k % kTK == 0) {  // n == 0 (zeros) stays with k_gemm_dx, which loads nothing then
     constexpr size_t lds = 2 * (size_t)kTrStage;
-    hipError_t e = set_lds_limit<k_gemm_dx_tr<MX>>(lds);
+    hipError_t e = set_lds_limit<k_gemm_dx_tr>(lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_gemm_dx_tr<MX>, grid, dim3(256), lds, stream, dy, codes, scales, tensor_scale, dx, ws, (int)m,
+    hipLaunchKernelGGL(k_gemm_dx_tr, grid, dim3(256), lds, stream, dy, codes, scales, tensor_scale, dx, ws, (int)m,
                        (int)n, (int)k, p.steps_per, out_f32);
   } else {
-    hipLaunchKernelGGL(k_gemm_dx<MX>, grid, dim3(256), 0, stream, dy, codes, scales, tensor_scale, dx, ws,
+    hipLaunchKernelGGL(k_gemm_dx, grid, dim3(256), 0, stream, dy, codes, scales, tensor_scale, dx, ws,
                        (int)m, (int)n, (int)k, p.steps_per, out_f32);
   }
-  return hipGetLastError();
-}
-}  // namespace
-
-hipError_t launch_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales,
-                          const float* tensor_scale, void* dx, int64_t m, int64_t n, int64_t k,
-                          int out_f32, const DxPlan& p, void* workspace, hipStream_t stream) {
-  hipError_t e = launch_dx<false>(dy, codes, scales, tensor_scale, dx, m, n, k, out_f32, p, workspace, stream);
+  hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  return launch_split_reduce(static_cast<const float*>(workspace), RowScale::one(tensor_scale), dx, m * k, k, p.splits,
-                             out_f32, stream);
-}
-
-hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
-                             int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace,
-                             hipStream_t stream) {
-  return launch_dx<true>(dy, codes, scales, nullptr, dx, m, n, k, out_f32, p, workspace, stream);
+  return launch_split_reduce(ws, RowScale::one(tensor_scale), dx, m * k, k, p.splits, out_f32, stream);
 }
 
 }  // namespace nvfp4

@@ -181,14 +181,11 @@ hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream);
 
-// dx[m, k] = dy[m, n] . w[n, k], w in MXFP4.  tile as above (128 or 256; 0 =
-// the kernel of launch_gemm_dx), stages_per in steps of 64 n.
+// dx[m, k] = dy[m, n] . w[n, k], w in MXFP4.  tile as above (128 or 256),
+// stages_per in steps of 64 n.
 MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k);
 hipError_t launch_mx_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
                         int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream);
-// The same by launch_gemm_dx's kernel (its plan), without the sum of its planes.
-hipError_t launch_mx_gemm_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
-                             int64_t n, int64_t k, int out_f32, const DxPlan& p, void* workspace, hipStream_t stream);
 
 // y = the sum of `splits` fp32 planes [splits, mn] in plane order, rounded
 // to the output type.

@@ -60,7 +60,9 @@ struct DxTile {
   static constexpr int kLds = 2 * kBuffer > 4 * kSlabBytes<NT> ? 2 * kBuffer : 4 * kSlabBytes<NT>;
 };
 
-template <typename T>
+// kDma = false: rows of dy that are not whole 16-byte pieces (N % 8 != 0, which
+// DMA cannot read) pass through registers, on the weights' schedule.
+template <bool kDma, typename T>
 __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     const uint16_t* __restrict__ dy, const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
     void* __restrict__ dx, float* __restrict__ planes, int M, int N, int K, int tiles_m, int tiles_k, int steps_per,
@@ -70,7 +72,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const TilePlace place = tile_place(tiles_m, tiles_k);
   const int m0 = place.m * TM, k0 = place.n * TK;
-  const int s0 = blockIdx.y * steps_per, ns = min((N + 63) / 64 - s0, steps_per);  // >= 1
+  const int s0 = blockIdx.y * steps_per, ns = min((N + 63) / 64 - s0, steps_per);
 
   // dy: instruction i of this wave copies 8 rows, lane l piece (l % 8) ^ swizzle
   // of row l / 8 (rows past M read row M - 1, pieces past N zeros)
@@ -90,6 +92,36 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     } else {
       const int r = 8 * (wave + 4 * i) + (lane >> 3);
       copy16_unseen(64 * (s0 + s) + 8 * ((lane & 7) ^ swizzle<8>(r)) < N ? p + off[i] : kZeros, to);
+    }
+  };
+  struct Dy {
+    u32x4_t d[kDma ? 1 : T::ND];
+  };
+  auto load_dy = [&](Dy& o, int s, auto wholec) {
+    if constexpr (!kDma) {
+#pragma unroll
+      for (int i = 0; i < T::ND; ++i) {
+        const int r = 8 * (wave + 4 * i) + (lane >> 3), n = 64 * (s0 + s) + 8 * (lane & 7);
+        const uint16_t* p = dy + (int64_t)min(m0 + r, M - 1) * N + n;
+        if (decltype(wholec)::value || n + 8 <= N) {
+          __builtin_memcpy(&o.d[i], p, 16);
+        } else {
+          uint32_t v[4] = {};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e < N) v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+          o.d[i] = u32x4_t{v[0], v[1], v[2], v[3]};
+        }
+      }
+    }
+  };
+  auto store_dy = [&](const Dy& o, int buf) {
+    if constexpr (!kDma) {
+#pragma unroll
+      for (int i = 0; i < T::ND; ++i) {
+        const int r = 8 * (wave + 4 * i) + (lane >> 3);
+        *reinterpret_cast<u32x4_t*>(lds + buf * T::kBuffer + 128 * r + 16 * ((lane & 7) ^ swizzle<8>(r))) = o.d[i];
+      }
     }
   };
   // weights: thread -> row wr of the step, columns 16 NT wq .. of the tile, in
@@ -132,10 +164,14 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   };
   // The loads of w have arrived (they are counted with the copies: a use later
   // on would wait for those as well).
-  auto arrived = [](Weights& o) {
+  auto arrived = [](Weights& o, Dy& y) {
 #if defined(__HIP_DEVICE_COMPILE__)
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) asm volatile("" : "+v"(o.c[i]), "+v"(o.s[i]));
+    if constexpr (!kDma) {
+#pragma unroll
+      for (int i = 0; i < T::ND; ++i) asm volatile("" : "+v"(y.d[i]));
+    }
 #endif
   };
 
@@ -179,21 +215,27 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   constexpr int kReads = 2 * NT + MT, kProducts = NT * MT;
 
   // Step s reads buffer s % 2.  Its weights were loaded during step s - 2 and
-  // stored during step s - 1, its dy copied during step s - 1.
+  // stored during step s - 1, its dy copied during step s - 1 (or as the weights).
   constexpr std::true_type kWhole;
   constexpr std::false_type kAny;
   Weights first, following;  // following: of step s + 1
+  Dy first_dy, following_dy;
   load(first, 0, kAny);
+  load_dy(first_dy, 0, kAny);
+  if constexpr (kDma) {
 #pragma unroll
-  for (int i = 0; i < T::ND; ++i) copy(0, 0, i, kAny);
-  if (ns > 1) load(following, 1, kAny);
+    for (int i = 0; i < T::ND; ++i) copy(0, 0, i, kAny);
+  }
+  load(following, 1, kAny);
+  load_dy(following_dy, 1, kAny);
   store(first, 0);
+  store_dy(first_dy, 0);
   wait_vm_all();
   __syncthreads();
-  arrived(following);
+  arrived(following, following_dy);
   Operands o[2];
   read(o[0], 0, 0);
-  if (ns > 1) {
+  if (kDma && ns > 1) {
 #pragma unroll
     for (int i = 0; i < T::ND; ++i) copy(1, 1, i, kAny);
   }
@@ -201,14 +243,21 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     constexpr bool kAll = decltype(wholec)::value;  // step s + 2 exists and is whole
     const int buf = s & 1;
     Weights spare = following;
-    if (kAll || s + 2 < ns) load(spare, s + 2, wholec);
+    Dy spare_dy = following_dy;
+    if (kAll || s + 2 < ns) {
+      load(spare, s + 2, wholec);
+      load_dy(spare_dy, s + 2, wholec);
+    }
     read(o[1], buf, 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply_all(o[0]);
     hold_sums(acc);
     read(o[0], buf, 2);
     __builtin_amdgcn_sched_barrier(0);
-    if (kAll || s + 1 < ns) store(following, buf ^ 1);
+    if (kAll || s + 1 < ns) {
+      store(following, buf ^ 1);
+      store_dy(following_dy, buf ^ 1);
+    }
     multiply_all(o[1]);
 #pragma unroll
     for (int p = 0; p < kProducts; ++p) {
@@ -223,7 +272,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     hold_sums(acc);
     wait_vm_all();
     meet();
-    arrived(spare);
+    arrived(spare, spare_dy);
     read(o[0], buf ^ 1, 0);  // behind the last step: stale values, not used
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -233,11 +282,12 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
       if ((p + 1) * T::ND / kProducts > p * T::ND / kProducts) {
 #pragma unroll
         for (int i = p * T::ND / kProducts; i < (p + 1) * T::ND / kProducts; ++i)
-          if (kAll || s + 2 < ns) copy(s + 2, buf, i, wholec);
+          if (kDma && (kAll || s + 2 < ns)) copy(s + 2, buf, i, wholec);
       }
     }
     hold_sums(acc);
     following = spare;
+    following_dy = spare_dy;
   };
   int s = 0;
   for (const int all = min(ns, N / 64 - s0) - 2; s < all; ++s) step(s, kWhole);
@@ -249,17 +299,20 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   else store_tile(acc, slab, static_cast<uint16_t*>(dx), m0 + wm, k0 + wk, M, K);
 }
 
-template <typename T>
+template <bool kDma, typename T>
 hipError_t launch_dx_tile(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
                           int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream) {
-  hipError_t e = set_tile_lds<k_mx_dx<T>, T::kLds>();
+  hipError_t e = set_tile_lds<k_mx_dx<kDma, T>, T::kLds>();
   if (e != hipSuccess) return e;
   const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_k = (int)((k + T::TK - 1) / T::TK);
-  hipLaunchKernelGGL((k_mx_dx<T>), dim3((unsigned)(tiles_m * tiles_k), (unsigned)p.splits), dim3(256), T::kLds, stream,
-                     dy, codes, scales, dx, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_k,
-                     p.stages_per, out_f32);
+  hipLaunchKernelGGL((k_mx_dx<kDma, T>), dim3((unsigned)(tiles_m * tiles_k), (unsigned)p.splits), dim3(256), T::kLds,
+                     stream, dy, codes, scales, dx, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m,
+                     tiles_k, p.stages_per, out_f32);
   return hipGetLastError();
 }
+
+// Rows of dy that DMA reads: whole 16-byte pieces, 32-bit offsets in a tile.
+bool dma_rows(int64_t n) { return n % 8 == 0 && n <= ((int64_t)1 << 22); }
 
 }  // namespace
 
@@ -267,31 +320,21 @@ MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k) {
   MxPlan p{0, 1, 0, 0};
   const int64_t steps = (n + 63) / 64;
   auto tiles = [&](int64_t t) { return ((m + t - 1) / t) * ((k + t - 1) / t); };
-  if (n % 8 != 0 || n == 0 || n > ((int64_t)1 << 22)) {  // rows of dy that DMA cannot read: k_gemm_dx
-    const DxPlan d = plan_gemm_dx(m, n, k);
-    p.splits = d.splits;
-    p.stages_per = d.steps_per;
-  } else {
-    p.tile = tiles(256) >= 160 ? 256 : 128;
-    int64_t splits = 1;
-    while (tiles(p.tile) * splits * 2 <= (p.tile == 256 ? 256 : 512) && steps / (splits * 2) >= 4) splits *= 2;
-    p.stages_per = (int)((steps + splits - 1) / splits);
-    p.splits = (int)((steps + p.stages_per - 1) / p.stages_per);
-  }
+  p.tile = dma_rows(n) && tiles(256) >= 160 ? 256 : 128;
+  int64_t splits = 1;
+  while (tiles(p.tile) * splits * 2 <= (p.tile == 256 ? 256 : 512) && steps / (splits * 2) >= 4) splits *= 2;
+  p.stages_per = (int)((steps + splits - 1) / splits);
+  p.splits = p.stages_per > 0 ? (int)((steps + p.stages_per - 1) / p.stages_per) : 1;
   p.ws_bytes = p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)k * sizeof(float) : 0;
   return p;
 }
 
 hipError_t launch_mx_dx(const uint16_t* dy, const uint8_t* codes, const uint8_t* scales, void* dx, int64_t m,
                         int64_t n, int64_t k, int out_f32, const MxPlan& p, void* workspace, hipStream_t stream) {
-  hipError_t e;
-  if (p.tile == 256)
-    e = launch_dx_tile<DxTile<4, 4>>(dy, codes, scales, dx, m, n, k, out_f32, p, workspace, stream);
-  else if (p.tile == 128)
-    e = launch_dx_tile<DxTile<2, 2>>(dy, codes, scales, dx, m, n, k, out_f32, p, workspace, stream);
-  else
-    e = launch_mx_gemm_dx(dy, codes, scales, dx, m, n, k, out_f32, DxPlan{p.splits, p.stages_per, p.ws_bytes}, workspace,
-                          stream);
+  auto go = [&](auto f) { return f(dy, codes, scales, dx, m, n, k, out_f32, p, workspace, stream); };
+  hipError_t e = p.tile == 256  ? go(launch_dx_tile<true, DxTile<4, 4>>)
+                 : dma_rows(n) ? go(launch_dx_tile<true, DxTile<2, 2>>)
+                               : go(launch_dx_tile<false, DxTile<2, 2>>);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_plane_sum(static_cast<const float*>(workspace), dx, m * k, p.splits, out_f32, stream);
 }

@@ -196,12 +196,6 @@ __device__ __forceinline__ void load_u16_async(uint32_t& d, const uint8_t* p) {
   asm volatile("global_load_ushort %0, %1, off offset:%2" : "=v"(d) : "v"(p), "i"(OFF) : "memory");
 #endif
 }
-template <int OFF>
-__device__ __forceinline__ void load_u8_async(uint32_t& d, const uint8_t* p) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("global_load_ubyte %0, %1, off offset:%2" : "=v"(d) : "v"(p), "i"(OFF) : "memory");
-#endif
-}
 // Wait until at most V vector-memory operations of this wave are
 // outstanding (loads return in issue order); V is capped at 63, the
 // counter's limit, which only waits longer.
