@@ -581,21 +581,23 @@ def w4a4_gemm(x: torch.Tensor, q: NVFP4Weight, out_dtype: torch.dtype = torch.bf
 
 
 _OUT_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+_U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
+
+# The microscaled operators serve single tokens, where a call's time on the
+# host is longer than its kernel's: each first asks for every property of its
+# tensors in one expression, and looks for the message of what is wrong (parts,
+# _need_all) only if that fails.
+
+
+def _fits(t, dtype, shape, index) -> bool:
+    """Whether t is a contiguous GPU tensor of this type and shape on device index."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.get_device() == index and t.is_contiguous())
 
 
 def _need_all(dev, parts):
     """_need over (tensor, name, dtype, shape) parts, None tensors skipped:
-    every type and shape first, then GPU residence on device dev.  The
-    message is looked for only once something is wrong (a call at one token
-    is bound by the host)."""
-    index = dev.index
-    for t, _, dtype, shape in parts:
-        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda
-                                  and t.get_device() == index and t.is_contiguous()
-                                  and (shape is None or t.shape == shape)):
-            break
-    else:
-        return
+    every type and shape first, then GPU residence on device dev."""
     for t, name, dtype, shape in parts:
         if t is not None:
             _need(t, name, dtype, shape, gpu=False)
@@ -604,14 +606,13 @@ def _need_all(dev, parts):
             _need(t, name, dtype, None, dev)
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) on dev's current stream, with dev as the current
-    device (the library launches on the current one)."""
-    index = dev.index
+def _run(index, fn, *args):
+    """fn(*args, stream) on device index's current stream, with that device
+    as the current one (the library launches on the current one)."""
     if torch.cuda.current_device() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != NVFP4_OK:
         _check(status)
@@ -624,12 +625,15 @@ def _out_code(dtype, name="out_dtype"):
     return code
 
 
-def _mx_workspace(workspace, need, dev):
+def _mx_workspace(workspace, need, like):
+    """(pointer, bytes, tensor) of the caller's workspace, or of a new one of `need` bytes beside tensor `like`."""
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, None, dev)  # its size: checked by the library
+        _need(workspace, "workspace", _U8, None, like.device)  # its size: checked by the library
     elif need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return workspace, 0 if workspace is None else workspace.numel()
+        workspace = like.new_empty(need, dtype=_U8)
+    else:
+        return None, 0, None
+    return workspace.data_ptr(), workspace.numel(), workspace
 
 
 @dataclass
@@ -645,9 +649,8 @@ class MXTensor:
     def shape(self):
         return (self.codes.shape[0], self.codes.shape[1] * (2 if self.fmt == MXFP4 else 1))
 
-    def parts(self, name: str = ""):
-        """(m, k, the (tensor, name, dtype, shape) pieces) of a consistent
-        matrix; raises ValueError if its sizes are not those of one."""
+    def sizes(self, name: str = ""):
+        """(m, k); raises ValueError unless codes and fmt are those of a matrix."""
         codes, fmt = self.codes, self.fmt
         if fmt != MXFP4 and fmt != MXFP8:
             raise ValueError(f"{name}fmt must be MXFP4 or MXFP8, got {fmt}")
@@ -658,8 +661,17 @@ class MXTensor:
             k *= 2
         if k % 32 != 0:
             raise ValueError(f"{name}codes imply k={k}, not a multiple of 32")
-        return m, k, [(codes, name + "codes", torch.uint8, None),
-                      (self.scales, name + "scales", torch.uint8, (m, k // 32))]
+        return m, k
+
+    def fits(self, m: int, k: int, index: int) -> bool:
+        """Whether codes and scales are those of an [m, k] matrix on GPU index."""
+        return (_fits(self.codes, _U8, (m, k // 2 if self.fmt == MXFP4 else k), index)
+                and _fits(self.scales, _U8, (m, k // 32), index))
+
+    def parts(self, name: str = ""):
+        """The (tensor, name, dtype, shape) pieces that _need_all checks."""
+        m, k = self.sizes(name)
+        return [(self.codes, name + "codes", _U8, None), (self.scales, name + "scales", _U8, (m, k // 32))]
 
     @staticmethod
     def empty(m: int, k: int, fmt: int, device) -> "MXTensor":
@@ -668,20 +680,26 @@ class MXTensor:
             raise ValueError(f"fmt must be MXFP4 or MXFP8, got {fmt}")
         if k % 32 != 0:
             raise ValueError(f"k={k} is not a multiple of 32")
-        return MXTensor(torch.empty((m, k // 2 if fmt == MXFP4 else k), dtype=torch.uint8, device=device),
-                        torch.empty((m, k // 32), dtype=torch.uint8, device=device), fmt)
+        return MXTensor(torch.empty((m, k // 2 if fmt == MXFP4 else k), dtype=_U8, device=device),
+                        torch.empty((m, k // 32), dtype=_U8, device=device), fmt)
 
 
-def _mx_out(out, m, k, fmt, dev):
-    """(out or a new MXTensor, its parts), for an operator that writes an [m, k] matrix in format fmt."""
+def _mx_out(out, m, k, fmt, like):
+    """out, checked to be an [m, k] matrix in format fmt beside tensor `like`, or a new one."""
     if out is None:
-        return MXTensor.empty(m, k, fmt, dev), []
+        if fmt != MXFP4 and fmt != MXFP8:
+            raise ValueError(f"fmt must be MXFP4 or MXFP8, got {fmt}")
+        if k % 32 != 0:
+            raise ValueError(f"k={k} is not a multiple of 32")
+        return MXTensor(like.new_empty((m, k // 2 if fmt == MXFP4 else k), dtype=_U8),
+                        like.new_empty((m, k // 32), dtype=_U8), fmt)
     if not isinstance(out, MXTensor):
         raise ValueError("out must be an MXTensor")
-    parts = out.parts("out.")[2]
+    parts = out.parts("out.")
     if out.fmt != fmt or out.shape != (m, k):
         raise ValueError(f"out holds a {out.shape} matrix in format {out.fmt}, the result is {(m, k)} in format {fmt}")
-    return out, parts
+    _need_all(like.device, parts)
+    return out
 
 
 def quantize_mx(x: torch.Tensor, fmt: int = MXFP4, out: Optional[MXTensor] = None) -> MXTensor:
@@ -690,25 +708,27 @@ def quantize_mx(x: torch.Tensor, fmt: int = MXFP4, out: Optional[MXTensor] = Non
         raise ValueError("x must be a 2-D tensor")
     code = _out_code(x.dtype, "x's dtype")
     m, k = x.shape
-    dev = x.device
-    if out is None:  # checked before anything is allocated
-        _need_all(dev, [(x, "x", x.dtype, None)])
-    out, parts = _mx_out(out, m, k, fmt, dev)
-    if parts:
-        _need_all(dev, [(x, "x", x.dtype, None)] + parts)
-    _call(dev, lib().nvfp4_mx_quantize, x.data_ptr(), code, m, k, fmt, out.codes.data_ptr(), out.scales.data_ptr())
+    if out is not None and isinstance(out, MXTensor) and (out.fmt != fmt or out.shape != (m, k)):
+        _mx_out(out, m, k, fmt, x)
+    if not (x.is_cuda and x.is_contiguous()):
+        _need(x, "x", x.dtype)
+    out = _mx_out(out, m, k, fmt, x)
+    _run(x.get_device(), lib().nvfp4_mx_quantize, x.data_ptr(), code, m, k, fmt, out.codes.data_ptr(),
+         out.scales.data_ptr())
     return out
 
 
 def dequant_mx(q: MXTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of an MX matrix, as float32 or bfloat16."""
-    m, k, parts = q.parts()
+    m, k = q.sizes()
     code = _out_code(dtype, "dtype")
-    dev = q.codes.device
-    _need_all(dev, parts + [(out, "out", dtype, (m, k))])
+    codes = q.codes
+    index = codes.get_device()
+    if not (q.fits(m, k, index) and (out is None or _fits(out, dtype, (m, k), index))):
+        _need_all(codes.device, q.parts() + [(out, "out", dtype, (m, k))])
     if out is None:
-        out = torch.empty((m, k), dtype=dtype, device=dev)
-    _call(dev, lib().nvfp4_mx_dequant, q.codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), m, k, q.fmt, code)
+        out = codes.new_empty((m, k), dtype=dtype)
+    _run(index, lib().nvfp4_mx_dequant, codes.data_ptr(), q.scales.data_ptr(), out.data_ptr(), m, k, q.fmt, code)
     return out
 
 
@@ -719,23 +739,23 @@ def mx_gemm_workspace_size(m: int, n: int, k: int, a_fmt: int) -> int:
 def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[m, n] = a[m, k] @ w[n, k]^T for MXFP4 or MXFP8 a and MXFP4 w."""
-    m, k, parts = a.parts("a.")
-    n, kw, w_parts = w.parts("w.")
+    m, k = a.sizes("a.")
+    n, kw = w.sizes("w.")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if kw != k:
         raise ValueError(f"a has k={k}, w k={kw}")
     code = _out_code(out_dtype)
-    dev = w.codes.device
-    parts += w_parts
-    parts.append((out, "out", out_dtype, (m, n)))
-    _need_all(dev, parts)
+    codes = w.codes
+    index = codes.get_device()
+    if not (a.fits(m, k, index) and w.fits(n, k, index) and (out is None or _fits(out, out_dtype, (m, n), index))):
+        _need_all(codes.device, a.parts("a.") + w.parts("w.") + [(out, "out", out_dtype, (m, n))])
     L = lib()
-    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_mx_gemm_workspace_size(m, n, k, a.fmt), dev)
+    ws, ws_bytes, keep = _mx_workspace(workspace, L.nvfp4_mx_gemm_workspace_size(m, n, k, a.fmt), codes)
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    _call(dev, L.nvfp4_mx_gemm, a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, w.codes.data_ptr(),
-          w.scales.data_ptr(), out.data_ptr(), m, n, k, code, _ptr(workspace), ws_bytes)
+        out = codes.new_empty((m, n), dtype=out_dtype)
+    _run(index, L.nvfp4_mx_gemm, a.codes.data_ptr(), a.scales.data_ptr(), a.fmt, codes.data_ptr(),
+         w.scales.data_ptr(), out.data_ptr(), m, n, k, code, ws, ws_bytes)
     return out
 
 
@@ -747,22 +767,24 @@ def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfl
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx = dy @ w for bf16 [m, n] dy and MXFP4 w [n, k]: mx_gemm's gradient
     with respect to its activations, straight through their quantization."""
-    n, k, parts = w.parts("w.")
+    n, k = w.sizes("w.")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2 or dy.shape[1] != n:
         raise ValueError(f"dy must be [m, {n}], got {tuple(getattr(dy, 'shape', ()))}")
     m = dy.shape[0]
     code = _out_code(out_dtype)
-    dev = w.codes.device
-    parts += [(dy, "dy", torch.bfloat16, None), (out, "out", out_dtype, (m, k))]
-    _need_all(dev, parts)
+    codes = w.codes
+    index = codes.get_device()
+    if not (w.fits(n, k, index) and _fits(dy, _BF16, (m, n), index)
+            and (out is None or _fits(out, out_dtype, (m, k), index))):
+        _need_all(codes.device, w.parts("w.") + [(dy, "dy", _BF16, None), (out, "out", out_dtype, (m, k))])
     L = lib()
-    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_mx_gemm_dx_workspace_size(m, n, k), dev)
+    ws, ws_bytes, keep = _mx_workspace(workspace, L.nvfp4_mx_gemm_dx_workspace_size(m, n, k), codes)
     if out is None:
-        out = torch.empty((m, k), dtype=out_dtype, device=dev)
-    _call(dev, L.nvfp4_mx_gemm_dx, dy.data_ptr(), w.codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), m, n, k,
-          code, _ptr(workspace), ws_bytes)
+        out = codes.new_empty((m, k), dtype=out_dtype)
+    _run(index, L.nvfp4_mx_gemm_dx, dy.data_ptr(), codes.data_ptr(), w.scales.data_ptr(), out.data_ptr(), m, n, k,
+         code, ws, ws_bytes)
     return out
 
 
@@ -778,27 +800,31 @@ def add_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, residual: Optional[tor
     residual or x."""
     if not isinstance(x, torch.Tensor) or x.dim() != 2:
         raise ValueError("x must be a 2-D tensor")
-    m, k = x.shape
-    dev = x.device
+    m, k = shape = x.shape
     if not isinstance(weight, torch.Tensor):
         raise ValueError("weight must be a torch.Tensor")
     wcode = _out_code(weight.dtype, "weight's dtype")
     if residual is None and residual_out is not None:
         raise ValueError("residual_out without a residual: the residual stream is x itself")
-    parts = [(x, "x", torch.bfloat16, None), (weight, "weight", weight.dtype, (k,)),
-             (residual, "residual", torch.bfloat16, (m, k)), (residual_out, "residual_out", torch.bfloat16, (m, k)),
-             (rstd, "rstd", torch.float32, (m,))]
-    if out is not None:
-        parts += _mx_out(out, m, k, fmt, dev)[1]
-    _need_all(dev, parts)
-    if out is None:
-        out = MXTensor.empty(m, k, fmt, dev)
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+    index = x.get_device()
+    if not (_fits(x, _BF16, shape, index) and _fits(weight, weight.dtype, (k,), index)
+            and (residual is None or _fits(residual, _BF16, shape, index))
+            and (residual_out is None or _fits(residual_out, _BF16, shape, index))
+            and (rstd is None or _fits(rstd, _F32, (m,), index))):
+        _need_all(x.device, [(x, "x", _BF16, None), (weight, "weight", weight.dtype, (k,)),
+                             (residual, "residual", _BF16, shape), (residual_out, "residual_out", _BF16, shape),
+                             (rstd, "rstd", _F32, (m,))])
+    out = _mx_out(out, m, k, fmt, x)
+    if residual is None:
+        residual_ptr = s_ptr = None
+    else:
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        residual_ptr, s_ptr = residual.data_ptr(), residual_out.data_ptr()
     if rstd is None:
-        rstd = torch.empty(m, dtype=torch.float32, device=dev)
-    _call(dev, lib().nvfp4_add_rmsnorm_mx, x.data_ptr(), _ptr(residual), weight.data_ptr(), wcode, eps, m, k, fmt,
-          _ptr(residual_out), rstd.data_ptr(), out.codes.data_ptr(), out.scales.data_ptr())
+        rstd = x.new_empty(m, dtype=_F32)
+    _run(index, lib().nvfp4_add_rmsnorm_mx, x.data_ptr(), residual_ptr, weight.data_ptr(), wcode, eps, m, k, fmt,
+         s_ptr, rstd.data_ptr(), out.codes.data_ptr(), out.scales.data_ptr())
     return out, x if residual is None else residual_out, rstd
 
 
@@ -816,23 +842,26 @@ def add_rmsnorm_backward(dh: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
     residual, and float32 [k].  dx may be ds."""
     if not isinstance(s, torch.Tensor) or s.dim() != 2:
         raise ValueError("s must be a 2-D tensor")
-    m, k = s.shape
-    dev = s.device
+    m, k = shape = s.shape
     if not isinstance(weight, torch.Tensor):
         raise ValueError("weight must be a torch.Tensor")
     wcode = _out_code(weight.dtype, "weight's dtype")
-    _need_all(dev, [(dh, "dh", torch.bfloat16, (m, k)), (s, "s", torch.bfloat16, None),
-                    (weight, "weight", weight.dtype, (k,)), (rstd, "rstd", torch.float32, (m,)),
-                    (ds, "ds", torch.bfloat16, (m, k)), (dx, "dx", torch.bfloat16, (m, k)),
-                    (dweight, "dweight", torch.float32, (k,))])
+    index = s.get_device()
+    if not (_fits(s, _BF16, shape, index) and _fits(dh, _BF16, shape, index)
+            and _fits(weight, weight.dtype, (k,), index) and _fits(rstd, _F32, (m,), index)
+            and (ds is None or _fits(ds, _BF16, shape, index)) and (dx is None or _fits(dx, _BF16, shape, index))
+            and (dweight is None or _fits(dweight, _F32, (k,), index))):
+        _need_all(s.device, [(dh, "dh", _BF16, shape), (s, "s", _BF16, None), (weight, "weight", weight.dtype, (k,)),
+                             (rstd, "rstd", _F32, (m,)), (ds, "ds", _BF16, shape), (dx, "dx", _BF16, shape),
+                             (dweight, "dweight", _F32, (k,))])
     L = lib()
-    workspace, ws_bytes = _mx_workspace(workspace, L.nvfp4_add_rmsnorm_backward_workspace_size(m, k), dev)
+    ws, ws_bytes, keep = _mx_workspace(workspace, L.nvfp4_add_rmsnorm_backward_workspace_size(m, k), s)
     if dx is None:
         dx = torch.empty_like(s)
     if dweight is None:
-        dweight = torch.empty(k, dtype=torch.float32, device=dev)
-    _call(dev, L.nvfp4_add_rmsnorm_backward, dh.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, rstd.data_ptr(),
-          _ptr(ds), dx.data_ptr(), dweight.data_ptr(), m, k, _ptr(workspace), ws_bytes)
+        dweight = s.new_empty(k, dtype=_F32)
+    _run(index, L.nvfp4_add_rmsnorm_backward, dh.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, rstd.data_ptr(),
+         _ptr(ds), dx.data_ptr(), dweight.data_ptr(), m, k, ws, ws_bytes)
     return dx, dweight
 
 
