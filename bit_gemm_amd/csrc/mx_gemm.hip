@@ -572,7 +572,7 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   double least = 1e300;
   for (int i = 0; i < 3; ++i) {
     const Shape& t = a_fmt == kMxFp4 ? kFp4[i] : kFp8[i];
-    const int64_t bk = mx_tile_k(a_fmt, t.size), stages = (k + bk - 1) / bk;
+    const int64_t bk = mx_tile_k(a_fmt, t.size), stages = k > 0 ? (k + bk - 1) / bk : 1;  // k = 0: a stage of none
     const int64_t count = ((m + t.size - 1) / t.size) * ((n + t.size - 1) / t.size);
     for (int64_t z = 1; z <= 16 && (z == 1 || (count * z <= 512 && stages / z >= 2)); z *= 2) {
       const int64_t per = (stages + z - 1) / z, all = count * ((stages + per - 1) / per);

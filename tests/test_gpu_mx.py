@@ -182,6 +182,29 @@ def test_gemm_writes_only_its_output(fmt):
             assert torch.equal(y, nv.mx_gemm(qa, qw, out_dtype=dt))
 
 
+@FMTS
+@pytest.mark.parametrize("m,n", [(17, 5), (300, 70), (70000, 9)])
+def test_gemm_over_nothing(fmt, m, n):
+    a, w = (nv.quantize_mx(torch.zeros((r, 0), device="cuda"), f) for r, f in ((m, fmt), (n, nv.MXFP4)))
+    for dt in (torch.bfloat16, torch.float32):
+        y = nv.mx_gemm(a, w, out=torch.full((m, n), 7.0, dtype=dt, device="cuda"), out_dtype=dt)
+        assert not bool(y.any())
+
+
+def test_gemm_rows_longer_than_tiles_take():
+    # k past the tiles' 32-bit offsets, more than 16 rows: the kernel of few rows in several groups.  Values 0,
+    # 1/2, 1 of either sign: products are quarters, sums (random walks) stay far below 2^24 of them: exact in any order
+    m, n, k = 17, 2, (1 << 22) + 32
+    g = np.random.default_rng(26)
+    code = np.array([0, 1, 2, 9, 10], dtype=np.uint8)
+    ac, wc = (code[g.integers(0, 5, (r, k))] for r in (m, n))
+    sa, sw = (np.full((r, k // 32), 127, dtype=np.uint8) for r in (m, n))
+    a, w = mx.dequant_mx(mx.pack(ac, mx.FP4), sa, mx.FP4), mx.dequant_mx(mx.pack(wc, mx.FP4), sw, mx.FP4)
+    y = _np(nv.mx_gemm(_mx(mx.pack(ac, mx.FP4), sa, nv.MXFP4), _mx(mx.pack(wc, mx.FP4), sw, nv.MXFP4),
+                       out_dtype=torch.float32))
+    assert np.array_equal(y, a @ w.T)
+
+
 def test_gemm_empty():
     w = nv.quantize_mx(torch.zeros((6, 0), device="cuda"))
     y = nv.mx_gemm(nv.quantize_mx(torch.zeros((3, 0), device="cuda"), nv.MXFP8), w, out_dtype=torch.float32)

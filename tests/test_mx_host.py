@@ -48,6 +48,11 @@ def test_gemm(L):
     assert g(y=ODD) == 3 and g(w=ODD) == 3 and g(s=ODD) == 3
     assert g(m=(1 << 22) + 1) == 2 and g(n=1 << 27) == 2 and g(k=1 << 31) == 2
     assert g(m=0, a=None, y=None) == 0 and g(n=0, w=None, y=None) == 0
+    # k = 0: planned like any other size (it needs no operands and no workspace), not divided by
+    for m in (3, 100, 1 << 22):
+        assert g(m=m, k=0, a=None, s=None, w=None, ws=None, y=ODD) == 3
+        if not torch.cuda.is_available():  # past every check, no device here
+            assert g(m=m, k=0, a=None, s=None, w=None, ws=None) > 4
     size = L.nvfp4_mx_gemm_workspace_size
     assert size(0, 8, 64, 0) == 0 and size(4, 8, 48, 0) == 0 and size(4, 8, 64, 7) == 0 and size(4, -8, 64, 0) == 0
 
