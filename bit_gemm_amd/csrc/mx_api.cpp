@@ -83,7 +83,8 @@ int check_norm(int64_t m, int64_t k, int weight_dtype) {
   if (st) return st;
   if (k == 0 || k > kMaxNormK)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "k=%lld: 32 .. %lld", (long long)k, (long long)kMaxNormK);
-  if (m > kMaxTokens) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large", (long long)m);
+  // a row of more than 16384 elements has a workgroup of 1024 threads
+  if (m >= kMaxTokens) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large", (long long)m);
   return check_type(weight_dtype, "weight_dtype");
 }
 
@@ -192,7 +193,7 @@ NVFP4_API int nvfp4_add_rmsnorm_mx(const void* x, const void* residual, const vo
 }
 
 NVFP4_API size_t nvfp4_add_rmsnorm_backward_workspace_size(int64_t m, int64_t k) {
-  if (m <= 0 || k <= 0 || k % 32 != 0 || k > kMaxNormK || m > kMaxTokens) return 0;
+  if (m <= 0 || k <= 0 || k % 32 != 0 || k > kMaxNormK || m >= kMaxTokens) return 0;
   return (size_t)nvfp4::rmsnorm_backward_planes(m, k) * (size_t)k * sizeof(float);
 }
 

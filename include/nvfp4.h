@@ -494,7 +494,7 @@ NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uin
  * residual_out  device bf16 [m, k]: s (NULL exactly when residual is NULL);
  *            may be residual's or x's own buffer.
  * rstd       device fp32 [m] or NULL (the gradient needs it).
- * m, k       m >= 0, m <= 2^22; 32 <= k <= 65536, k % 32 == 0.
+ * m, k       m >= 0, m < 2^22; 32 <= k <= 65536, k % 32 == 0.
  * One launch.  A row with an infinity or NaN follows the formulas.
  *
  * nvfp4_add_rmsnorm_backward - its gradient, straight through the

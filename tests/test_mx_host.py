@@ -75,6 +75,7 @@ def test_norm(L):
         return L.nvfp4_add_rmsnorm_mx(x, r, w, wt, eps, m, k, fmt, ro, rs, c, s, None)
 
     assert f(k=48) == 2 and f(k=0) == 2 and f(k=65568) == 2 and f(m=-1) == 1 and f(m=(1 << 22) + 1) == 2
+    assert f(m=1 << 22, k=16416) == 2  # 2^32 work-items
     assert f(wt=4) == 1 and f(fmt=9) == 1 and f(eps=-1.0) == 1 and f(eps=float("nan")) == 1 and f(eps=float("inf")) == 1
     assert f(r=FAKE) == 1 and f(ro=FAKE) == 1 and f(x=None) == 1 and f(c=None) == 1 and f(w=None) == 1
     assert f(x=ODD) == 3 and f(w=ODD) == 3 and f(rs=FAKE + 2) == 3 and f(r=FAKE, ro=ODD) == 3
