@@ -224,15 +224,16 @@ struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
   static constexpr int TN = 32 * NT * WN, TM = 32 * MT * WM;
   static constexpr int WP = 2 * S, AP = FMT == kMxFp4 ? 2 * S : 4 * S;  // 16-byte pieces of a row per stage
-  static constexpr int kA = TM * 16 * AP, kW = TN * 16 * WP;
+  static constexpr int kA = TM * 16 * AP, kW = (TN * 16 * WP + 4095) / 4096 * 4096;  // whole DMA instructions
   static constexpr int NA = kA / 4096, NW = kW / 4096;  // DMA instructions per wave and stage
   static constexpr int kStage = kA + kW;
   static constexpr int SR = 2 * S * G;                                // scale bytes of a row per G stages
   static constexpr int NS = ((TM + TN) * SR / 16 + 255) / 256;        // 16-byte loads per thread for them
-  static constexpr int kScales = (TM + TN) * SR, kAll = B * kStage + 2 * kScales;
+  static constexpr int kRows = (TM + TN + 63) / 64 * 64;              // scale_at exchanges 32 of 64
+  static constexpr int kScales = kRows * SR, kAll = B * kStage + 2 * kScales;
   static constexpr int kEpilogue = 4 * kSlabBytes<NT>;
   static constexpr int kLds = kAll > kEpilogue ? kAll : kEpilogue;
-  static_assert(kA % 4096 == 0 && kW % 4096 == 0, "whole instructions");
+  static_assert(kA % 4096 == 0, "whole instructions");
   static_assert(B >= 2 && (S == 2 || S == 4) && G >= 2 && SR % 16 == 0 && kLds <= 160 * 1024, "stages");
 };
 
@@ -297,7 +298,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   // bytes each; a thread takes 16-byte pieces tid, + 256, ... of them.  In LDS
   // word d of every row lies in an array of its own, odd arrays with rows 32
   // apart exchanged: a wave's read of two words of 32 rows meets 64 banks.
-  constexpr int SR = T::SR, kRows = TN + TM;
+  constexpr int SR = T::SR, kRows = T::kRows;
   auto scale_at = [](int row, int d) { return 4 * (d * kRows + (row ^ (d & 1) * 32)); };
   u32x4_t sreg[T::NS];
   auto load_scales = [&](int u) {
@@ -325,7 +326,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
 #pragma unroll
     for (int i = 0; i < T::NS; ++i) {
       const int e = (int)threadIdx.x + 256 * i;
-      if (kRows * SR / 16 % 256 != 0 && e >= kRows * SR / 16) break;
+      if ((TM + TN) * SR / 16 % 256 != 0 && e >= (TM + TN) * SR / 16) break;
 #pragma unroll
       for (int d = 0; d < 4; ++d)
         *reinterpret_cast<uint32_t*>(sl + scale_at(e / (SR / 16), e % (SR / 16) * 4 + d)) = sreg[i][d];
@@ -469,18 +470,21 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   else store_tile(acc, slab, static_cast<uint16_t*>(y), m0 + wm, n0 + wn, M, N);
 }
 
-// The tiles the library has (plan_mx_gemm chooses).  256 k per stage, but 128
+// The tiles the library has (plan_mx_gemm chooses): square, and 256 rows of a
+// x 224 of w, its four waves below one another.  256 k per stage, but 128
 // where the E4M3 rows of 128 or 256 would not fit twice in LDS.
 template <int FMT>
 using Tile256 = Tile<FMT, 4, 4, 2, FMT == kMxFp4 ? 4 : 2, FMT == kMxFp4 ? 2 : 3, 4>;
+template <int FMT>
+using Tile224 = Tile<FMT, 7, 2, 1, FMT == kMxFp4 ? 4 : 2, FMT == kMxFp4 ? 2 : 3, 4>;
 template <int FMT>
 using Tile128 = Tile<FMT, 2, 2, 2, FMT == kMxFp4 ? 4 : 2, FMT == kMxFp4 ? 2 : 4, 4>;
 template <int FMT>
 using Tile64 = Tile<FMT, 1, 1, 2, 4, 3, 4>;
 // k per stage of a tile.
 int mx_tile_k(int fmt, int size) {
-  if (fmt == kMxFp4) return 64 * (size == 256 ? Tile256<kMxFp4>::S : size == 128 ? Tile128<kMxFp4>::S : Tile64<kMxFp4>::S);
-  return 64 * (size == 256 ? Tile256<kMxFp8>::S : size == 128 ? Tile128<kMxFp8>::S : Tile64<kMxFp8>::S);
+  if (fmt == kMxFp4) return 64 * (size >= 224 ? Tile256<kMxFp4>::S : size == 128 ? Tile128<kMxFp4>::S : Tile64<kMxFp4>::S);
+  return 64 * (size >= 224 ? Tile256<kMxFp8>::S : size == 128 ? Tile128<kMxFp8>::S : Tile64<kMxFp8>::S);
 }
 
 template <int FMT, bool EXACT, typename T>
@@ -552,12 +556,16 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 //   64 x 64 tiles:   0.46 / 0.50 with at most one workgroup per CU, 0.60 / 0.75 with two
 //   128 x 128:       1.0 / 1.3, 1.5 with two (MXFP8: its LDS leaves room for one)
 //   256 x 256:       2.5 / 3.4
+//   256 x 224 (n):   2.27 / 3.0
 // beside about 2 for a launch, and a split of K 3 for its second launch and the
 // planes' traffic.  So few outputs take small tiles, for more workgroups, and many
 // large ones, which read each operand less often: 1024 x 4096 x 4096 (m, n, k)
 // with MXFP4 took 21.5 / 17.6 / 32.0 with the three tiles, 512 x 4096 x 4096
 // 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
-// x 4096 281 / 175 / 158; 64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
+// x 4096 281 / 175 / 158.  The 256 x 224 tile is for n = 7 2^i, whose rounds it
+// fills: 4096 x 14336 x 4096 in four rounds instead of three and a half of the
+// square tile took 152 / 212 (329 with fp32 output) against 157 / 226 (379), but
+// 2048 x 8192 x 4096 64 / 95 against 40 / 61.  64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
 // four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   MxPlan best{0, 1, 0, 0};
@@ -567,13 +575,14 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
     int size, slots;
     double alone, full;  // time of a round of at most 256 workgroups, of `slots`
   };
-  static const Shape kFp4[3] = {{64, 512, 0.46, 0.60}, {128, 512, 1.0, 1.5}, {256, 256, 2.5, 2.5}};
-  static const Shape kFp8[3] = {{64, 512, 0.50, 0.75}, {128, 256, 1.3, 1.3}, {256, 256, 3.4, 3.4}};
+  static const Shape kFp4[4] = {{64, 512, 0.46, 0.60}, {128, 512, 1.0, 1.5}, {256, 256, 2.5, 2.5}, {224, 256, 2.27, 2.27}};
+  static const Shape kFp8[4] = {{64, 512, 0.50, 0.75}, {128, 256, 1.3, 1.3}, {256, 256, 3.4, 3.4}, {224, 256, 3.0, 3.0}};
   double least = 1e300;
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const Shape& t = a_fmt == kMxFp4 ? kFp4[i] : kFp8[i];
     const int64_t bk = mx_tile_k(a_fmt, t.size), stages = k > 0 ? (k + bk - 1) / bk : 1;  // k = 0: a stage of none
-    const int64_t count = ((m + t.size - 1) / t.size) * ((n + t.size - 1) / t.size);
+    const int64_t rows = t.size == 224 ? 256 : t.size;
+    const int64_t count = ((m + rows - 1) / rows) * ((n + t.size - 1) / t.size);
     for (int64_t z = 1; z <= 16 && (z == 1 || (count * z <= 512 && stages / z >= 2)); z *= 2) {
       const int64_t per = (stages + z - 1) / z, all = count * ((stages + per - 1) / per);
       const int64_t rest = all % t.slots;
@@ -599,6 +608,7 @@ hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
   if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile256<FMT>>);
+  if (plan.tile == 224) return go(launch_tile<FMT, EXACT, Tile224<FMT>>);
   if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile128<FMT>>);
   if (plan.tile == 64) return go(launch_tile<FMT, EXACT, Tile64<FMT>>);
   return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);

@@ -108,7 +108,8 @@ def test_gemm(fmt, m, n, k):
 
 
 @FMTS
-@pytest.mark.parametrize("m,n,k", [(3500, 3700, 544), (2300, 5000, 1024), (4096, 4224, 2080)])
+@pytest.mark.parametrize("m,n,k", [(3500, 3700, 544), (2300, 5000, 1024), (4096, 4224, 2080), (3990, 4090, 1056),
+                                   (2045, 7159, 544)])
 def test_gemm_many_tiles(fmt, m, n, k):
     # enough outputs for every workgroup tile the library has; sampled rows against the oracle
     print("mx gemm", fmt, m, n, k, flush=True)
