@@ -16,11 +16,16 @@
 // transposing LDS reads: within each 16-lane group, lane i receives element i %
 // 4 of the 4-element reads of lanes i / 4 + 4 j, j = 0 .. 3.
 //
-// What bounds it: at 256 x 256 a step is 256 products per SIMD's worth of 32
-// clocks (2048) against 192 KiB through LDS (about 1500); at 128 x 128 the LDS
-// needs longer than the products, so that tile serves where there are too few
-// outputs for the large one.  Operands are read a step of 16 ahead, and the
-// waves meet before the last of a buffer's four steps, as in mx_gemm.hip.
+// What bounds it: at 256 x 256 a step is 64 products of 32 clocks per SIMD
+// (2048) beside 192 KiB through LDS (about 1000) and the conversions; measured
+// 1.65 us per step with every CU at work, 3100 clocks at the 1.87 GHz that the
+// card then runs at, 1.29-1.31 PFLOP/s at 4096 x 14336 x 4096 (m, n, k; 370 us),
+// where a large bf16 library product of plain matrices reaches 1.38.  At 128 x
+// 128 the LDS needs longer than the products: 1.0 PFLOP/s, for where there are
+// too few outputs for the large tile.  A 256 x 224 tile (rounds that fill for k =
+// 7 2^i) was no faster: 118 against 115 us at 1024 x 4096 x 14336.  Operands are
+// read a step of 16 ahead, and the waves meet before the last of a buffer's four
+// steps, as in mx_gemm.hip.
 #include "launchers.h"
 #include "mx_tile.h"
 
@@ -54,7 +59,7 @@ typedef short v8i16_t __attribute__((ext_vector_type(8)));
 template <int NT_, int MT_>
 struct DxTile {
   static constexpr int NT = NT_, MT = MT_, TK = 64 * NT, TM = 64 * MT;
-  static constexpr int kRow = 2 * TK + 32;  // bytes of an LDS row of weights, padded
+  static constexpr int kRow = 2 * TK;  // bytes of an LDS row of weights
   static constexpr int kDy = TM * 128, kW = 64 * kRow, kBuffer = kDy + kW;
   static constexpr int ND = kDy / 4096;     // DMA instructions per wave and step
   static constexpr int kLds = 2 * kBuffer > 4 * kSlabBytes<NT> ? 2 * kBuffer : 4 * kSlabBytes<NT>;
@@ -124,11 +129,16 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
       }
     }
   };
-  // weights: thread -> row wr of the step, columns 16 NT wq .. of the tile, in
-  // runs of 32 (or one of 32 at NT = 2: K is a multiple of 32, a run is inside
-  // or outside)
+  // weights: thread -> row wr of the step, runs wq, wq + 4, .. of 32 columns (K
+  // is a multiple of 32: a run is inside or outside)
   constexpr int kRuns = NT / 2;
   const int wr = tid >> 2, wq = tid & 3;
+  // 16-byte piece p of an LDS row of weights lies at place_of: the four threads
+  // of two rows that write at one time, and the four rows that a transposing read
+  // takes 64 bytes of, then meet different banks (conflicts 40 % of the LDS'
+  // cycles in rows padded by 32 bytes, with adjacent runs per thread; 390 us
+  // against 366-374 at 4096 x 14336 x 4096)
+  auto place_of = [](int row, int p) { return 16 * (p ^ (p >> 2 & 2) ^ 5 * (row & 3)); };
   struct Weights {
     u32x4_t c[kRuns];
     uint32_t s[kRuns];
@@ -137,7 +147,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     const int n = 64 * (s0 + s) + wr;
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
-      const int k = k0 + 32 * (kRuns * wq + i);
+      const int k = k0 + 32 * (wq + 4 * i);
       o.c[i] = u32x4_t{0, 0, 0, 0};
       o.s[i] = 127;
       if ((decltype(wholec)::value || n < N) && k < K) {
@@ -147,7 +157,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     }
   };
   auto store = [&](const Weights& o, int buf) {
-    uint8_t* w = lds + buf * T::kBuffer + T::kDy + wr * T::kRow + 64 * kRuns * wq;
+    uint8_t* w = lds + buf * T::kBuffer + T::kDy + wr * T::kRow;
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) {
       const float s = mx_scale(o.s[i]);
@@ -158,7 +168,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 1)),
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 2)),
             __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(o.c[i][d], s, 3))};
-        *reinterpret_cast<u32x4_t*>(w + 64 * i + 16 * d) = v;
+        *reinterpret_cast<u32x4_t*>(w + 256 * i + place_of(wr, 4 * wq + d)) = v;
       }
     }
   };
@@ -192,13 +202,12 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     const uint8_t* d = lds + buf * T::kBuffer + (wm + r) * 128 + 16 * ((2 * ks + h) ^ swizzle<8>(r));
 #pragma unroll
     for (int i = 0; i < MT; ++i) o.d[i] = *reinterpret_cast<const bf16x8_t*>(d + 32 * 128 * i);
-    const uint8_t* w = lds + buf * T::kBuffer + T::kDy + (16 * ks + 8 * (grp >> 1) + (sl >> 2)) * T::kRow +
-                       2 * (wk + 16 * (grp & 1) + 4 * (sl & 3));
+    const uint8_t* wb = lds + buf * T::kBuffer + T::kDy + (16 * ks + 8 * (grp >> 1) + (sl >> 2)) * T::kRow;
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      o.lo[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(w + 64 * i));
-      o.hi[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) v4i16_t*)(w + 64 * i + 4 * T::kRow));
+      const uint8_t* w = wb + place_of(sl >> 2, wk / 8 + 4 * i + 2 * (grp & 1) + (sl >> 1 & 1)) + 8 * (sl & 1);
+      o.lo[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)w);
+      o.hi[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(w + 4 * T::kRow));
     }
   };
   // product p of a step's NT MT
@@ -318,28 +327,33 @@ bool dma_rows(int64_t n) { return n % 8 == 0 && n <= ((int64_t)1 << 22); }
 
 // The tile and split with the least expected time, from times measured on
 // MI355X (microseconds): a round of workgroups takes 0.69 per step of 64 n with
-// 128 x 128 tiles, 1.16 with two workgroups per CU, 1.9 with 256 x 256; a launch
+// 128 x 128 tiles, 1.1 with two workgroups per CU, 1.75 with 256 x 256; a launch
 // about 2.5 (8 with the large tile, whose first loads and stores nothing else
 // hides), a split 3 for its second launch and the planes' traffic.  1024 x 4096 x
-// 14336 (m, n, k) took 118 with the large tile, 138 with the small one, 2048 x
+// 14336 (m, n, k) took 115 with the large tile, 143 with the small one, 2048 x
 // 4096 x 4096 114 and 76, 512 x 4096 x 4096 with small tiles 43 whole, 33 split
 // in two or four, 44 in eight.
 MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k) {
   MxPlan best{128, 1, 0, 0};
   const int64_t steps = (n + 63) / 64;
   double least = 1e300;
-  for (int size = 128; size <= (dma_rows(n) ? 256 : 128); size *= 2) {
-    const int64_t count = ((m + size - 1) / size) * ((k + size - 1) / size), slots = size == 256 ? 256 : 512;
+  struct Shape {
+    int size, slots;
+    double start, alone, full;  // a launch; a step with at most 256 workgroups, with `slots`
+  };
+  static const Shape kShapes[2] = {{128, 512, 2.5, 0.69, 1.1}, {256, 256, 8.0, 1.75, 1.75}};
+  for (const Shape& t : kShapes) {
+    if (t.size != 128 && !dma_rows(n)) break;
+    const int64_t count = ((m + t.size - 1) / t.size) * ((k + t.size - 1) / t.size);
     for (int64_t z = 1; z <= 16 && (z == 1 || (count * z <= 512 && steps / z >= 2)); z *= 2) {
       const int64_t per = (steps + z - 1) / z, all = per > 0 ? count * ((steps + per - 1) / per) : count;
-      const int64_t rest = all % slots;
-      const double full = size == 256 ? 1.9 : 1.16, alone = size == 256 ? 1.9 : 0.69;
-      const double rounds = (double)(all / slots) * full + (rest == 0 ? 0.0 : rest <= 256 ? alone : full);
-      double time = (size == 256 ? 8.0 : 2.5) + rounds * (double)per;
+      const int64_t rest = all % t.slots;
+      const double rounds = (double)(all / t.slots) * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full);
+      double time = t.start + rounds * (double)per;
       if (z > 1) time += 3.0 + 8.0 * (double)z * (double)m * (double)k / 6.0e6;
       if (time < least) {
         least = time;
-        best.tile = size;
+        best.tile = t.size;
         best.stages_per = (int)per;
         best.splits = per > 0 ? (int)((steps + per - 1) / per) : 1;
       }
