@@ -310,12 +310,18 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
                                 : w_scales + (int64_t)(n0 + min(r - TM, wrows)) * nb;
       if (2 * S * s0 + SR * (u + 1) <= nb) {
         __builtin_memcpy(&sreg[i], p + at, 16);
-      } else {  // the end of the rows: byte by byte, ones behind it
+      } else {  // the end of the rows, ones behind it: all loads under way at once (one after another 0.3-2 us more)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
           uint32_t v = 0;
-#pragma unroll 1
-          for (int b = at + 4 * d; b < at + 4 * d + 4; ++b) v = (v >> 8) | (uint32_t)(b < nb ? p[b] : 127) << 24;
+const int b = at + 4 * d, left = nb - b;
+          v = 0x7F7F7F7Fu;
+          if (left >= 4) __builtin_memcpy(&v, p + b, 4);
+          else if (left > 0) {
+            v = p[b] | 0x7F7F7F00u;
+            if (left > 1) v = (v & 0xFFFF00FFu) | p[b + 1] << 8;
+            if (left > 2) v = (v & 0xFF00FFFFu) | p[b + 2] << 16;
+          }
           sreg[i][d] = v;
         }
       }
@@ -408,16 +414,19 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
   // the last step of stage s, the other during the first of the next stage.
   constexpr std::true_type kWhole;
   constexpr std::false_type kAny;
+  load_scales(0);
+  copy(0, 0, 0, kAny);  // no stage at all (K = 0): zeros
+  copy(0, 0, 1, kAny);
+  store_scales(0);
 #pragma unroll
-  for (int s = 0; s < B; ++s) {
+  for (int s = 1; s < B; ++s) {
     if (s >= ns) continue;
     copy(s, s * T::kStage, 0, kAny);
     if (s < B - 1) copy(s, s * T::kStage, 1, kAny);
   }
-  load_scales(0);
-  store_scales(0);
-  wait_vm_all();
-  __syncthreads();
+  if (ns >= B) wait_vm_count<(B - 2) * NC + kFirst>();  // stage 0 has landed
+  else wait_vm_all();
+  meet();
   Operands o[2];
   Scales sc, next;
   read_scales(sc, 0);

@@ -111,26 +111,24 @@ __device__ __forceinline__ void store_tile(f32x16_t (&acc)[NT][MT], uint8_t* sla
         if constexpr (sizeof(E) == 4) *reinterpret_cast<f32x4_t*>(p) = v;
         else *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
       }
-    u32x4_t v[kRuns / 2];
+    if (vec) {
+      u32x4_t v[kRuns / 2];
 #pragma unroll
-    for (int e = 0; e < kRuns / 2; ++e) {
-      const int at = lane + 64 * e;
-      v[e] = *reinterpret_cast<const u32x4_t*>(slab + at / kRuns * kPitch + at % kRuns * 16);
-    }
+      for (int e = 0; e < kRuns / 2; ++e) {
+        const int at = lane + 64 * e;
+        v[e] = *reinterpret_cast<const u32x4_t*>(slab + at / kRuns * kPitch + at % kRuns * 16);
+      }
 #pragma unroll
-    for (int e = 0; e < kRuns / 2; ++e) {
-      const int at = lane + 64 * e, m = m0 + 32 * j + at / kRuns, n = n0 + at % kRuns * kPer;
-      if (m >= M || n >= N) continue;
-      E* q = out + (int64_t)m * N + n;
-      if (vec) {
-        *reinterpret_cast<u32x4_t*>(q) = v[e];
-      } else {
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-          if (n + c >= N) break;
-          if constexpr (sizeof(E) == 4) reinterpret_cast<uint32_t*>(q)[c] = v[e][c];
-          else q[c] = (E)(v[e][c >> 1] >> (16 * (c & 1)));
-        }
+      for (int e = 0; e < kRuns / 2; ++e) {
+        const int at = lane + 64 * e, m = m0 + 32 * j + at / kRuns, n = n0 + at % kRuns * kPer;
+        if (m < M && n < N) *reinterpret_cast<u32x4_t*>(out + (int64_t)m * N + n) = v[e];
+      }
+    } else {  // rows that are not whole pieces: neighbouring outputs in neighbouring lanes
+#pragma unroll 8
+      for (int e = 0; e < 16 * NT; ++e) {
+        const int at = lane + 64 * e, m = m0 + 32 * j + at / (32 * NT), n = n0 + at % (32 * NT);
+        const E v = *reinterpret_cast<const E*>(slab + at / (32 * NT) * kPitch + at % (32 * NT) * sizeof(E));
+        if (m < M && n < N) out[(int64_t)m * N + n] = v;
       }
     }
   }
