@@ -123,13 +123,22 @@ __device__ __forceinline__ void store_tile(f32x16_t (&acc)[NT][MT], uint8_t* sla
         const int at = lane + 64 * e, m = m0 + 32 * j + at / kRuns, n = n0 + at % kRuns * kPer;
         if (m < M && n < N) *reinterpret_cast<u32x4_t*>(out + (int64_t)m * N + n) = v[e];
       }
-    } else {  // rows that are not whole pieces: neighbouring outputs in neighbouring lanes
+    } else {
+      // rows that are not whole pieces: the largest runs (8, 4 or 2 bytes) they are
+      // whole numbers of, neighbouring runs in neighbouring lanes
+      auto store_runs = [&](auto one) {
+        using Run = decltype(one);
+        constexpr int kIn = sizeof(Run) / sizeof(E), kRow = 32 * NT / kIn;
 #pragma unroll 8
-      for (int e = 0; e < 16 * NT; ++e) {
-        const int at = lane + 64 * e, m = m0 + 32 * j + at / (32 * NT), n = n0 + at % (32 * NT);
-        const E v = *reinterpret_cast<const E*>(slab + at / (32 * NT) * kPitch + at % (32 * NT) * sizeof(E));
-        if (m < M && n < N) out[(int64_t)m * N + n] = v;
-      }
+        for (int e = 0; e < kRow / 2; ++e) {
+          const int at = lane + 64 * e, m = m0 + 32 * j + at / kRow, n = n0 + at % kRow * kIn;
+          const Run v = *reinterpret_cast<const Run*>(slab + at / kRow * kPitch + at % kRow * sizeof(Run));
+          if (m < M && n < N) *reinterpret_cast<Run*>(out + (int64_t)m * N + n) = v;
+        }
+      };
+      if (N * sizeof(E) % 8 == 0) store_runs(u32x2_t{});
+      else if (N * sizeof(E) % 4 == 0) store_runs(uint32_t{});
+      else if constexpr (sizeof(E) == 2) store_runs(uint16_t{});
     }
   }
 }

@@ -90,7 +90,7 @@ def test_quantize_writes_only_its_rows():
 PRODUCTS = [(1, 1, 32), (1, 17, 64), (2, 16, 96), (15, 33, 128), (16, 100, 160), (17, 64, 512), (33, 48, 544),
             (48, 31, 1056), (49, 16, 4128), (64, 272, 2048), (65, 64, 96), (100, 300, 1056), (129, 257, 320),
             (257, 129, 256), (300, 515, 4192), (1, 4096, 4096), (16, 1001, 14336), (130, 1024, 2048),
-            (520, 1056, 1312), (64, 80, 33 * 512)]
+            (520, 1056, 1312), (64, 80, 33 * 512), (130, 90, 320), (300, 518, 288), (700, 2046, 160)]
 
 
 @FMTS
