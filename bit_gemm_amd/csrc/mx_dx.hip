@@ -18,14 +18,14 @@
 //
 // What bounds it: at 256 x 256 a step is 64 products of 32 clocks per SIMD
 // (2048) beside 192 KiB through LDS (about 1000) and the conversions; measured
-// 1.65 us per step with every CU at work, 3100 clocks at the 1.87 GHz that the
-// card then runs at, 1.29-1.31 PFLOP/s at 4096 x 14336 x 4096 (m, n, k; 370 us),
-// where a large bf16 library product of plain matrices reaches 1.38.  At 128 x
-// 128 the LDS needs longer than the products: 1.0 PFLOP/s, for where there are
-// too few outputs for the large tile.  A 256 x 224 tile (rounds that fill for k =
-// 7 2^i) was no faster: 118 against 115 us at 1024 x 4096 x 14336.  Operands are
-// read a step of 16 ahead, and the waves meet before the last of a buffer's four
-// steps, as in mx_gemm.hip.
+// 1.6 us per step with every CU at work, 3000 clocks at the 1.87 GHz that the
+// card then runs at, 1.34 PFLOP/s at 4096 x 14336 x 4096 (m, n, k; 357 us), where
+// a large bf16 library product of plain matrices reaches 1.38.  At 128 x 128 the
+// LDS needs longer than the products: 1.0 PFLOP/s, for where there are too few
+// outputs for the large tile.  A 256 x 224 tile (rounds that fill for k = 7 2^i)
+// was no faster: 118 against 115 us at 1024 x 4096 x 14336.  Operands are read a
+// step of 16 ahead (two ahead: no faster), and the waves meet before the last of
+// a buffer's four steps, as in mx_gemm.hip.
 #include "launchers.h"
 #include "mx_tile.h"
 
@@ -137,7 +137,7 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   // of two rows that write at one time, and the four rows that a transposing read
   // takes 64 bytes of, then meet different banks (conflicts 40 % of the LDS'
   // cycles in rows padded by 32 bytes, with adjacent runs per thread; 390 us
-  // against 366-374 at 4096 x 14336 x 4096)
+  // against 370 at 4096 x 14336 x 4096)
   auto place_of = [](int row, int p) { return 16 * (p ^ (p >> 2 & 2) ^ 5 * (row & 3)); };
   struct Weights {
     u32x4_t c[kRuns];
@@ -223,12 +223,13 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   };
   constexpr int kReads = 2 * NT + MT, kProducts = NT * MT;
 
-  // Step s reads buffer s % 2.  Its weights were loaded during step s - 2 and
-  // stored during step s - 1, its dy copied during step s - 1 (or as the weights).
+  // Step s reads buffer s % 2.  Its weights were loaded from the end of step s - 3
+  // on and stored during step s - 1, its dy copied from the end of step s - 2 on
+  // (or as the weights).
   constexpr std::true_type kWhole;
   constexpr std::false_type kAny;
-  Weights first, following;  // following: of step s + 1
-  Dy first_dy, following_dy;
+  Weights first, following, later;  // following: of step s + 1, later: of s + 2
+  Dy first_dy, following_dy, later_dy;
   load(first, 0, kAny);
   load_dy(first_dy, 0, kAny);
   if constexpr (kDma) {
@@ -242,6 +243,10 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
   wait_vm_all();
   __syncthreads();
   arrived(following, following_dy);
+  if (ns > 2) {
+    load(later, 2, kAny);
+    load_dy(later_dy, 2, kAny);
+  }
   Operands o[2];
   read(o[0], 0, 0);
   if (kDma && ns > 1) {
@@ -249,14 +254,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     for (int i = 0; i < T::ND; ++i) copy(1, 1, i, kAny);
   }
   auto step = [&](int s, auto wholec) {
-    constexpr bool kAll = decltype(wholec)::value;  // step s + 2 exists and is whole
+    constexpr bool kAll = decltype(wholec)::value;  // step s + 3 exists and is whole
     const int buf = s & 1;
-    Weights spare = following;
-    Dy spare_dy = following_dy;
-    if (kAll || s + 2 < ns) {
-      load(spare, s + 2, wholec);
-      load_dy(spare_dy, s + 2, wholec);
-    }
     read(o[1], buf, 1);
     __builtin_amdgcn_sched_barrier(0);
     multiply_all(o[0]);
@@ -281,7 +280,13 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
     hold_sums(acc);
     wait_vm_all();
     meet();
-    arrived(spare, spare_dy);
+    arrived(later, later_dy);
+    following = later;
+    following_dy = later_dy;
+    if (kAll || s + 3 < ns) {
+      load(later, s + 3, wholec);
+      load_dy(later_dy, s + 3, wholec);
+    }
     read(o[0], buf ^ 1, 0);  // behind the last step: stale values, not used
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -295,11 +300,9 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_dx(
       }
     }
     hold_sums(acc);
-    following = spare;
-    following_dy = spare_dy;
   };
   int s = 0;
-  for (const int all = min(ns, N / 64 - s0) - 2; s < all; ++s) step(s, kWhole);
+  for (const int all = min(ns, N / 64 - s0) - 3; s < all; ++s) step(s, kWhole);
   for (; s < ns; ++s) step(s, kAny);
   __syncthreads();  // the buffers' LDS becomes the output's
   uint8_t* slab = lds + wave * kSlabBytes<NT>;
