@@ -34,25 +34,6 @@
 namespace nvfp4 {
 namespace {
 
-// LDS DMA of 16 bytes per lane to LDS address `to` (wave-uniform) + 16 lane,
-// from src, or from base + a 32-bit offset per lane.  As inline asm: the
-// compiler holds back every transposing LDS read until all copies it knows of
-// have landed, the ones into the other buffer too.  They write no register, and
-// the kernel waits for them itself (wait_vm_all before the waves meet).
-__device__ __forceinline__ void copy16_unseen(const uint8_t* src, uint32_t to) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "m0");
-#endif
-}
-__device__ __forceinline__ void copy16_unseen(const uint8_t* base, uint32_t offset, uint32_t to) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(offset), "s"(base) : "m0");
-#endif
-}
-__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
-  return __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p);
-}
-
 typedef short v4i16_t __attribute__((ext_vector_type(4)));
 typedef short v8i16_t __attribute__((ext_vector_type(8)));
 

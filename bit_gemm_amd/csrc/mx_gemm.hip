@@ -46,20 +46,38 @@ __device__ __forceinline__ u32x4_t large_codes(u32x4_t v) {
   return r;
 }
 
-// D += W (16 rows, E2M1, scale byte in bits 0-7 of ws) x A (16 rows).
-template <int FMT, bool EXACT>
+// D += W (16 rows, E2M1, scale in byte J of ws) x A (16 rows, byte J of as).
+template <int FMT, bool EXACT, int J = 0>
 __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32x4_t a1, uint32_t as, f32x4_t d) {
   if constexpr (FMT == kMxFp4) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0), d, 4, 4, 0, (int)ws, 0, (int)as);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0), d, 4, 4, J, (int)ws, J, (int)as);
   } else if constexpr (!EXACT) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0, a1), d, 4, 0, 0, (int)ws, 0,
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0, a1), d, 4, 0, J, (int)ws, J,
                                                             (int)as);
   } else {
     const u32x4_t h0 = large_codes(a0), h1 = large_codes(a1);
-    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0 ^ h0, a1 ^ h1), d, 4, 0, 0, (int)ws, 0,
+    d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0 ^ h0, a1 ^ h1), d, 4, 0, J, (int)ws, J,
                                                          (int)as);
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(h0, h1), d, 4, 0, 0, (int)ws, 0,
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(h0, h1), d, 4, 0, J, (int)ws, J,
                                                             (int)as);
+  }
+}
+
+// Adds the NW waves' sums of a 16x16 tile and stores it.  D: lane l, value v ->
+// weight row 4 (l / 16) + v of tile t, row m0 + l % 16 of a.
+template <int NW>
+__device__ __forceinline__ void store_rows(const f32x4_t* red, void* y, int m0, int t, int M, int N, int out_f32) {
+  const int lane = threadIdx.x & 63, m = m0 + (lane & 15), n = 16 * t + 4 * (lane >> 4);
+  f32x4_t s = red[lane];
+#pragma unroll
+  for (int w = 1; w < NW; ++w) s += red[64 * w + lane];
+  if (m >= M) return;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    if (n + v >= N) break;
+    const int64_t idx = (int64_t)m * N + n + v;
+    if (out_f32) static_cast<float*>(y)[idx] = s[v];
+    else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(s[v], 0.0f);
   }
 }
 
@@ -72,13 +90,10 @@ __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32
 // times bandwidth, and they run on across tiles.  Where a wave has one chunk
 // of K, its part of a stays in registers.  A step's weight load reads 64
 // consecutive bytes of 16 rows; C steps' scales are one load per row, and a
-// lane shifts its block's byte to the bottom.  Measured (weights from HBM): 1 x
-// 4096 x 4096 (m, n, k) 4.4 us with MXFP4 a, 4.6 with MXFP8, 1 x 28672 x 4096
-// 15.7 (4.0 TB/s; 31 MB more weights cost 5.5 us, 5.7 TB/s, the rest is the
-// launch and the first loads' latency), 16 x 4096 x 14336 12.2 / 15.0, where
-// every CU reads all of a from L2 beside its weights.  Three or four chunks
-// ahead, or 16 waves: no faster; 64 consecutive bytes per lane (four loads of 16
-// separate pieces per row): 13.7 / 17.7.
+// lane shifts its block's byte to the bottom.  Three or four chunks ahead, or 16
+// waves: no faster; 64 consecutive bytes per lane (four loads of 16 separate
+// pieces per row): 13.7 / 17.7 us against 12.3 / 15.1 at 16 x 4096 x 14336 with
+// MXFP4 / MXFP8 a.  For every K that k_mx_rows_dma does not take.
 constexpr int kRowWaves = 8;
 constexpr int kRowGroups = 256;  // workgroups: one per CU
 
@@ -160,19 +175,7 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
     acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     __syncthreads();
     if (wave != turn % kRowWaves) return;
-    f32x4_t s = red[turn & 1][0][lane];
-#pragma unroll
-    for (int w = 1; w < kRowWaves; ++w) s += red[turn & 1][w][lane];
-    // D of a 16x16 tile: lane l, value v -> weight row 4 (l / 16) + v, row l % 16 of a
-    const int m = m0 + r, n = 16 * t + 4 * q;
-    if (m >= M) return;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if (n + v >= N) break;
-      const int64_t idx = (int64_t)m * N + n + v;
-      if (out_f32) static_cast<float*>(y)[idx] = s[v];
-      else static_cast<uint16_t*>(y)[idx] = (uint16_t)pack_bf16(s[v], 0.0f);
-    }
+    store_rows<kRowWaves>(red[turn & 1][0], y, m0, t, M, N, out_f32);
   };
   Chunk even, odd;
   int turn = 0, left = per, t = blockIdx.x;
@@ -192,6 +195,148 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
       if (i + 2 < items) load(even, per > 1);
       item(odd);
     }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// k_mx_rows_dma (up to 16 rows of a, K a multiple of 512 from 4096 on): the same
+// walk, each wave's chunks of 512 k staged by DMA in a ring of R slots of its
+// own LDS.  A load into registers reads 64 bytes of each of 16 rows, because a
+// lane can only load what its row of the product needs; the copies read whole
+// lines (rows of 256 bytes, or 512 of MXFP8 a), which brings the weights in
+// sooner and above all a, which every CU reads from L2.  Measured beside
+// k_mx_rows (us, weights from HBM, MXFP4 / MXFP8 a): 1 x 4096 x 4096 4.3 / 4.4
+// (4.4 / 4.6), 1 x 14336 x 4096 9.5 / 10.0 (10.4 / 10.8), 1 x 28672 x 4096 14.5
+// (16.0; 4.3 TB/s), 16 x 4096 x 14336 10.1 / 12.3 (12.3 / 15.1), 16 x 14336 x
+// 4096 9.8 / 10.6 (11.7 / 13.6).  Bound by the weights' way from HBM (31 MB more
+// cost 5.2 us, 6.0 TB/s) behind a launch and the first copies' latency.
+//
+// Step j's block q is the chunk's block 4 q + j in both operands: a lane's four
+// scales are one word, byte j of it picked by the instruction.  Piece p of row
+// r lies at p ^ r of its LDS row (256 bytes, or 512), so that 16 rows' reads of
+// one piece meet all banks.  KEEP (one chunk per wave: K = 4096): a stays in
+// registers and the ring is the weights' alone.  RA: rows of a that are staged.
+template <int FMT_, bool EXACT_, bool KEEP_, int RA_, int NW_, int R_>
+struct Ring {
+  static constexpr int FMT = FMT_, RA = RA_, NW = NW_, R = R_;
+  static constexpr bool EXACT = EXACT_, KEEP = KEEP_;
+  static constexpr int kRowA = FMT == kMxFp4 ? 256 : 512;  // bytes of a's row per chunk
+  static constexpr int kW = 4096, kA = KEEP ? 0 : RA * kRowA, kS = KEEP ? 256 : 512, kSlot = kW + kA + kS;
+  static constexpr int ND = 4 + kA / 1024 + 1;             // copies per chunk
+  static constexpr int kRed = NW * R * kSlot, kLds = kRed + 2 * NW * 1024;
+  static_assert(kA % 1024 == 0 && kLds <= 160 * 1024 && (R - 1) * ND <= 63, "ring");
+  static_assert(!KEEP || (RA == 16 && R == 4 && 16 * kRowA <= 2 * kSlot), "a's way through the ring");
+};
+
+template <typename T>
+__global__ __launch_bounds__(64 * T::NW, T::NW / 4) void k_mx_rows_dma(
+    const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, const uint8_t* __restrict__ w_codes,
+    const uint8_t* __restrict__ w_scales, void* __restrict__ y, int M, int N, int K, int out_f32) {
+  constexpr int FMT = T::FMT, NW = T::NW, R = T::R, kW = T::kW, kA = T::kA, kRowA = T::kRowA;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = lane >> 4;
+  const int nb = K / 32, chunks = K / 512, per = (chunks - wave + NW - 1) / NW;  // of this wave
+  const uint32_t wpitch = K / 2, apitch = FMT == kMxFp4 ? K / 2 : K;
+  const uint8_t* ring = lds + wave * (R * T::kSlot);
+  const uint32_t ring0 = lds_address(ring);
+
+  constexpr int NA = T::RA * kRowA / 1024;
+  uint32_t aoff[NA];
+#pragma unroll
+  for (int i = 0; i < NA; ++i) {
+    const int at = 1024 * i + 16 * lane, row = at / kRowA;
+    aoff[i] = (uint32_t)min(row, M - 1) * apitch + 16 * (at % kRowA / 16 ^ row);
+  }
+  auto copy_a = [&](int chunk, uint32_t to) {
+    const uint8_t* p = a_codes + kRowA * (int64_t)chunk;
+#pragma unroll
+    for (int i = 0; i < NA; ++i) copy16_unseen(p, aoff[i], to + 1024 * i);
+  };
+  struct A {
+    u32x4_t lo, hi;
+  };
+  auto read_a = [&](const uint8_t* p, int j) {  // step j's operand from rows staged at p
+    const int row = r & (T::RA - 1);
+    p += kRowA * row;
+    if constexpr (FMT == kMxFp4) return A{load16(p + 16 * ((4 * q + j) ^ row)), u32x4_t{}};
+    const int b = 4 * (q >> 1) + j;
+    return A{load16(p + 16 * ((2 * b + (q & 1)) ^ row)), load16(p + 16 * ((2 * (b + 8) + (q & 1)) ^ row))};
+  };
+  const int tiles = (N + 15) / 16, turns = (tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int items = turns * per;  // chunk wave + NW (i % per) of tile blockIdx.x + gridDim.x (i / per)
+  int to_tile = blockIdx.x, to_chunk = wave, to_slot = 0;  // of the next item to copy
+  auto copy = [&]() {
+    const uint32_t to = ring0 + to_slot * T::kSlot;
+    const uint8_t* wp = w_codes + (int64_t)to_tile * 16 * wpitch + 256 * (int64_t)to_chunk;
+    const int last = N - 1 - 16 * to_tile;  // rows past the end read the last one
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * i + q;
+      copy16_unseen(wp, (uint32_t)min(row, last) * wpitch + 16 * (r ^ row), to + 1024 * i);
+    }
+    if constexpr (!T::KEEP) copy_a(to_chunk, to + kW);
+    if (lane < T::kS / 16) {
+      const uint8_t* p = lane < 16 ? w_scales + ((int64_t)to_tile * 16 + min(r, last)) * nb
+                                   : a_scales + (int64_t)min(r, M - 1) * nb;
+      copy16_unseen(p + 16 * (int64_t)to_chunk, to + kW + kA);
+    }
+    to_slot = to_slot == R - 1 ? 0 : to_slot + 1;
+    to_chunk += NW;
+    if (to_chunk >= chunks) to_chunk = wave, to_tile += gridDim.x;
+  };
+
+  A kept[T::KEEP ? 4 : 1];
+  uint32_t kept_scales = 0;
+  int ahead = 0;  // items copied before the loop
+  if constexpr (T::KEEP) {  // a's chunk passes through the last two slots
+    copy_a(wave, ring0 + 2 * T::kSlot);
+    for (; ahead < min(2, items); ++ahead) copy();
+    kept_scales = *reinterpret_cast<const uint32_t*>(a_scales + (int64_t)min(r, M - 1) * nb + 16 * wave + 4 * q);
+    wait_vm_all();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) kept[j] = read_a(ring + 2 * T::kSlot, j);
+    wait_lds_all();
+  }
+  for (; ahead < min(R - 1, items); ++ahead) copy();
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto multiply = [&](const uint8_t* p) {
+    const uint8_t* sp = p + kW + kA + 16 * r + 4 * q;
+    const uint32_t ws = *reinterpret_cast<const uint32_t*>(sp);
+    const uint32_t as = T::KEEP ? kept_scales : *reinterpret_cast<const uint32_t*>(sp + (T::KEEP ? 0 : 256));
+    auto step = [&](auto jc) {
+      constexpr int j = decltype(jc)::value;
+      const u32x4_t w = load16(p + 256 * r + 16 * ((4 * q + j) ^ r));
+      const A a = T::KEEP ? kept[T::KEEP ? j : 0] : read_a(p + kW, j);
+      acc = mma16<FMT, T::EXACT, j>(w, ws, a.lo, a.hi, as, acc);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(lds + T::kRed);  // [2][NW][64]
+
+  int slot = 0, left = per, t = blockIdx.x, turn = 0;
+  for (int i = 0; i < items; ++i) {
+    if (i + R - 1 < items) {
+      wait_lds_all();  // the last item's reads of the slot that is filled next
+      copy();
+      wait_vm_count<(R - 1) * T::ND>();  // this item's copies, the oldest, have landed
+    } else {
+      wait_vm_all();
+    }
+    multiply(ring + slot * T::kSlot);
+    slot = slot == R - 1 ? 0 : slot + 1;
+    if (--left > 0) continue;
+    // the tile's sums: the waves' in wave order, one wave adds and stores
+    red[((turn & 1) * NW + wave) * 64 + lane] = acc;  // last read two turns ago, before the last turn's meeting
+    acc = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    meet();
+    if (wave == turn % NW) store_rows<NW>(red + (turn & 1) * NW * 64, y, 0, t, M, N, out_f32);
+    left = per;
+    t += gridDim.x;
+    ++turn;
   }
 }
 
@@ -558,6 +703,21 @@ hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const ui
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a_codes, a_scales, w_codes, w_scales, y, (int)m, (int)n, (int)k,
                        out_f32);
   };
+  if (m <= 16 && k >= 4096 && k % 512 == 0 && k <= ((int64_t)1 << 22)) {  // whole chunks, 32-bit offsets in a tile
+    auto ring = [&](auto tc) {
+      using T = decltype(tc);
+      hipError_t e = set_tile_lds<k_mx_rows_dma<T>, T::kLds>();
+      if (e != hipSuccess) return e;
+      hipLaunchKernelGGL(k_mx_rows_dma<T>, grid, dim3(64 * T::NW), T::kLds, stream, a_codes, a_scales, w_codes,
+                         w_scales, y, (int)m, (int)n, (int)k, out_f32);
+      return hipGetLastError();
+    };
+    // a stays in registers where its way there is paid for by several tiles (one tile: 4.3 against 4.5 us at 1 x
+    // 4096 x 4096; four: 9.8 against 11.0 at 16 x 14336 x 4096)
+    if (k == 4096 && tiles > kRowGroups) return ring(Ring<FMT, EXACT, true, 16, 8, 4>{});
+    if (m <= 4) return ring(Ring<FMT, EXACT, false, 4, 8, FMT == kMxFp4 ? 3 : 2>{});
+    return ring(Ring<FMT, EXACT, false, 16, FMT == kMxFp4 ? 8 : 4, FMT == kMxFp4 ? 2 : 3>{});
+  }
   // chunks of 512 once every wave has one
   if (k >= 512 * kRowWaves) go(k_mx_rows<FMT, EXACT, 4>);
   else go(k_mx_rows<FMT, EXACT, 1>);

@@ -22,6 +22,32 @@ __device__ __forceinline__ void meet() {
 #endif
 }
 
+// Wait until every LDS access of this wave has completed.
+__device__ __forceinline__ void wait_lds_all() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#endif
+}
+
+// LDS DMA of 16 bytes per lane to LDS address `to` (wave-uniform) + 16 lane,
+// from src, or from base + a 32-bit offset per lane.  As inline asm: the
+// compiler holds back transposing LDS reads until all copies it knows of have
+// landed, the ones into other buffers too, and counts them in its own waits.
+// They write no register, and the kernel waits for them itself.
+__device__ __forceinline__ void copy16_unseen(const uint8_t* src, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "m0");
+#endif
+}
+__device__ __forceinline__ void copy16_unseen(const uint8_t* base, uint32_t offset, uint32_t to) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(offset), "s"(base) : "m0");
+#endif
+}
+__device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
+  return __builtin_amdgcn_readfirstlane((int)(uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)p);
+}
+
 // LDS rows of P 16-byte pieces, piece p of row r at slot p ^ swizzle<P>(r): the
 // 16 rows that a quarter of a read instruction takes then lie in 16 different
 // bank groups.

@@ -90,7 +90,8 @@ def test_quantize_writes_only_its_rows():
 PRODUCTS = [(1, 1, 32), (1, 17, 64), (2, 16, 96), (15, 33, 128), (16, 100, 160), (17, 64, 512), (33, 48, 544),
             (48, 31, 1056), (49, 16, 4128), (64, 272, 2048), (65, 64, 96), (100, 300, 1056), (129, 257, 320),
             (257, 129, 256), (300, 515, 4192), (1, 4096, 4096), (16, 1001, 14336), (130, 1024, 2048),
-            (520, 1056, 1312), (64, 80, 33 * 512), (130, 90, 320), (300, 518, 288), (700, 2046, 160)]
+            (520, 1056, 1312), (64, 80, 33 * 512), (130, 90, 320), (300, 518, 288), (700, 2046, 160),
+            (3, 4200, 4096), (16, 5000, 4096), (4, 700, 5120), (2, 4500, 4608), (9, 4500, 4608), (13, 50, 8192)]
 
 
 @FMTS
