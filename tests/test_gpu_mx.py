@@ -437,6 +437,53 @@ def test_captured_and_replayed_on_another_stream():
         torch.cuda.synchronize()
 
 
+def test_calls_at_once_on_two_streams():
+    # every operator under way on both streams at one time, own buffers each: the results of calls one by one
+    x = [rows(m, 4096, 140 + m, torch.bfloat16, 3).cuda() for m in (3, 700)]
+    w = _mx(*weights(600, 4096, 141), nv.MXFP4)
+    gain = torch.ones(4096, device="cuda")
+
+    def chain(x):
+        h, s, rstd = nv.add_rmsnorm_mx(x, gain, residual=x)
+        y = nv.mx_gemm(h, w)
+        dh = nv.mx_gemm_dx(y, w)
+        return [h.codes, y, nv.dequant_mx(nv.quantize_mx(y[:, :544].contiguous())), dh,
+                *nv.add_rmsnorm_backward(dh, s, gain, rstd, ds=x)]
+
+    want = [chain(t) for t in x]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in x]
+    got = [[], []]
+    for _ in range(4):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(chain(x[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(run, want[i]))
+
+
+@pytest.mark.parametrize("m,k", [(16, 4096), (40, 1056)])
+def test_gemm_of_a_matrix_with_itself(m, k):
+    q = _mx(*weights(m, k, 150), nv.MXFP4)
+    v = mx.dequant_mx(q.codes.cpu().numpy(), q.scales.cpu().numpy(), mx.FP4)
+    ref, bound = product_bound(v, v, mx.FP4, torch.float32)
+    assert np.all(np.abs(_np(nv.mx_gemm(q, q, out_dtype=torch.float32)) - ref) <= bound)
+
+
+def test_refuses_views_off_sixteen_bytes():
+    flat = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    x, odd = flat[8:].view(4, 64), flat[4:-4].view(4, 64)
+    w = nv.quantize_mx(x)
+    for call in (lambda: nv.quantize_mx(odd), lambda: nv.add_rmsnorm_mx(odd, torch.ones(64, device="cuda")),
+                 lambda: nv.mx_gemm(w, w, out=torch.zeros(24, device="cuda").bfloat16()[4:20].view(4, 4)),
+                 lambda: nv.mx_gemm_dx(flat[4:20].view(4, 4), w)):
+        with pytest.raises(RuntimeError, match="aligned"):
+            call()
+    assert nv.quantize_mx(x).shape == (4, 64)
+
+
 def test_large_offsets():
     # codes past 2^31 bytes: a [m, k] MXFP8 matrix of 2.2e9 elements, its last rows against the oracle
     m, k = 33600, 65536
