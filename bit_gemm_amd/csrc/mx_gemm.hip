@@ -12,12 +12,13 @@
 //
 // Accuracy.  With two E2M1 operands every 32 products are summed exactly.
 // With an E4M3 operand the instruction adds products in groups of 8 and cuts
-// each at 2^-14 of the group's largest (measured: relative error of a whole
-// Gaussian product about 1e-5).  That is far below the rounding of a bf16
-// output (2^-9) and is left as it is there; where the output is fp32, the E4M3
-// operand is split by magnitude (below 2 and from 2 up, zeros in the places
-// of the other part) and multiplied twice: each part's products then span
-// fewer bits than the instruction keeps, and the sums are those of fp32.
+// each at 2^-14 of the group's largest: about 1e-5 of a Gaussian product, but
+// without limit where large products cancel.  So the E4M3 operand is split by
+// magnitude (below 2 and from 2 up, zeros in the places of the other part) and
+// multiplied twice: each part's products span 2^14 at most (2^-10 .. 11.25 and
+// 2^-3 .. 2688), nothing is cut, and the sums are those of fp32 whatever the
+// output's type.  The second product is free where the weights' way from HBM
+// bounds the kernel (up to 16 rows) and costs matrix time elsewhere.
 #include "launchers.h"
 #include "mx_tile.h"
 
@@ -47,13 +48,10 @@ __device__ __forceinline__ u32x4_t large_codes(u32x4_t v) {
 }
 
 // D += W (16 rows, E2M1, scale in byte J of ws) x A (16 rows, byte J of as).
-template <int FMT, bool EXACT, int J = 0>
+template <int FMT, int J = 0>
 __device__ __forceinline__ f32x4_t mma16(u32x4_t w, uint32_t ws, u32x4_t a0, u32x4_t a1, uint32_t as, f32x4_t d) {
   if constexpr (FMT == kMxFp4) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0), d, 4, 4, J, (int)ws, J, (int)as);
-  } else if constexpr (!EXACT) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0, a1), d, 4, 0, J, (int)ws, J,
-                                                            (int)as);
   } else {
     const u32x4_t h0 = large_codes(a0), h1 = large_codes(a1);
     d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(a0 ^ h0, a1 ^ h1), d, 4, 0, J, (int)ws, J,
@@ -97,7 +95,7 @@ __device__ __forceinline__ void store_rows(const f32x4_t* red, void* y, int m0, 
 constexpr int kRowWaves = 8;
 constexpr int kRowGroups = 256;  // workgroups: one per CU
 
-template <int FMT, bool EXACT, int C>
+template <int FMT, int C>
 __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __restrict__ a_codes,
                                                                const uint8_t* __restrict__ a_scales,
                                                                const uint8_t* __restrict__ w_codes,
@@ -167,7 +165,7 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
   auto multiply = [&](const Chunk& o) {
 #pragma unroll
     for (int j = 0; j < C; ++j)
-      acc = mma16<FMT, EXACT>(o.w[j], o.ws[j] >> (8 * q), o.a[j], o.a1[FMT == kMxFp8 ? j : 0], o.as[j] >> (8 * q), acc);
+      acc = mma16<FMT>(o.w[j], o.ws[j] >> (8 * q), o.a[j], o.a1[FMT == kMxFp8 ? j : 0], o.as[j] >> (8 * q), acc);
   };
   // the sums of tile t, the turn-th of this workgroup: one wave adds and stores
   auto finish = [&](int t, int turn) {
@@ -205,10 +203,10 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
 // lane can only load what its row of the product needs; the copies read whole
 // lines (rows of 256 bytes, or 512 of MXFP8 a), which brings the weights in
 // sooner and above all a, which every CU reads from L2.  Measured beside
-// k_mx_rows (us, weights from HBM, MXFP4 / MXFP8 a): 1 x 4096 x 4096 4.3 / 4.4
-// (4.4 / 4.6), 1 x 14336 x 4096 9.5 / 10.0 (10.4 / 10.8), 1 x 28672 x 4096 14.5
-// (16.0; 4.3 TB/s), 16 x 4096 x 14336 10.1 / 12.3 (12.3 / 15.1), 16 x 14336 x
-// 4096 9.8 / 10.6 (11.7 / 13.6).  Bound by the weights' way from HBM (31 MB more
+// k_mx_rows (us, weights from HBM, MXFP4 a): 1 x 4096 x 4096 4.3 (4.4), 1 x
+// 14336 x 4096 9.5 (10.4), 1 x 28672 x 4096 14.5 (16.0; 4.3 TB/s), 16 x 4096 x
+// 14336 10.1 (12.3), 16 x 14336 x 4096 9.8 (11.7); MXFP8 a, multiplied twice:
+// 4.8, 10.2, 15.4, 12.9, 10.6.  Bound by the weights' way from HBM (31 MB more
 // cost 5.2 us, 6.0 TB/s) behind a launch and the first copies' latency.
 //
 // Step j's block q is the chunk's block 4 q + j in both operands: a lane's four
@@ -216,10 +214,10 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
 // r lies at p ^ r of its LDS row (256 bytes, or 512), so that 16 rows' reads of
 // one piece meet all banks.  KEEP (one chunk per wave: K = 4096): a stays in
 // registers and the ring is the weights' alone.  RA: rows of a that are staged.
-template <int FMT_, bool EXACT_, bool KEEP_, int RA_, int NW_, int R_>
+template <int FMT_, bool KEEP_, int RA_, int NW_, int R_>
 struct Ring {
   static constexpr int FMT = FMT_, RA = RA_, NW = NW_, R = R_;
-  static constexpr bool EXACT = EXACT_, KEEP = KEEP_;
+  static constexpr bool KEEP = KEEP_;
   static constexpr int kRowA = FMT == kMxFp4 ? 256 : 512;  // bytes of a's row per chunk
   static constexpr int kW = 4096, kA = KEEP ? 0 : RA * kRowA, kS = KEEP ? 256 : 512, kSlot = kW + kA + kS;
   static constexpr int ND = 4 + kA / 1024 + 1;             // copies per chunk
@@ -308,7 +306,7 @@ __global__ __launch_bounds__(64 * T::NW, T::NW / 4) void k_mx_rows_dma(
       constexpr int j = decltype(jc)::value;
       const u32x4_t w = load16(p + 256 * r + 16 * ((4 * q + j) ^ r));
       const A a = T::KEEP ? kept[T::KEEP ? j : 0] : read_a(p + kW, j);
-      acc = mma16<FMT, T::EXACT, j>(w, ws, a.lo, a.hi, as, acc);
+      acc = mma16<FMT, j>(w, ws, a.lo, a.hi, as, acc);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
@@ -375,9 +373,9 @@ __global__ __launch_bounds__(64 * T::NW, T::NW / 4) void k_mx_rows_dma(
 // 3450 clocks per stage of 256 k, 2430 of them the products as fast as they
 // issue, 2810 with the copies left out, at the 1.85 GHz that the card then runs
 // at; a round has 5.7 us of first loads and stores beside its 30 us of stages at
-// k = 4096.  4096 x 14336 x 4096: 143 us, 3.36 PFLOP/s; MXFP8 208 us, 2.31;
-// MXFP8 with fp32 output, every product twice, 326 us.  4096 x 4096 x 14336
-// MXFP4: 114 us, 4.2 PFLOP/s.
+// k = 4096.  4096 x 14336 x 4096: 142 us, 3.39 PFLOP/s; MXFP8, every product
+// twice, 312 us (327 with fp32 output; 206 with each product once, which loses
+// the small ones).  4096 x 4096 x 14336 MXFP4: 114 us, 4.2 PFLOP/s.
 template <int FMT, int NT_, int MT_, int WN_, int S_, int B_, int G_>
 struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
@@ -396,7 +394,7 @@ struct Tile {
   static_assert(B >= 2 && (S == 2 || S == 4) && G >= 2 && SR % 16 == 0 && kLds <= 160 * 1024, "stages");
 };
 
-template <int FMT, bool EXACT, typename T>
+template <int FMT, typename T>
 __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
     const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_scales, const uint8_t* __restrict__ w_codes,
     const uint8_t* __restrict__ w_scales, void* __restrict__ y, float* __restrict__ planes, int M, int N, int K,
@@ -544,17 +542,15 @@ const int b = at + 4 * d, left = nb - b;
   };
   auto multiply = [&](const Operands& o, const Scales& c, auto jc) {
     constexpr int j = decltype(jc)::value;
-    i32x8_t af[MT], ah[EXACT ? MT : 1];
+    i32x8_t af[MT], ah[FMT == kMxFp8 ? MT : 1];  // below 2 and from 2 up
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       if constexpr (FMT == kMxFp4) {
         af[i] = operand(o.a[i]);
-      } else if constexpr (EXACT) {
+      } else {
         const u32x4_t lo = large_codes(o.a[i]), hi = large_codes(o.a1[i]);
         ah[i] = operand(lo, hi);
         af[i] = operand(o.a[i] ^ lo, o.a1[i] ^ hi);
-      } else {
-        af[i] = operand(o.a[i], o.a1[i]);
       }
     }
 #pragma unroll
@@ -563,12 +559,12 @@ const int b = at + 4 * d, left = nb - b;
       for (int m = 0; m < MT; ++m) {
         acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(o.w[i]), af[m], acc[i][m], 4, kCbsz<FMT>, j,
                                                                     (int)c.w[i], j, (int)c.a[m]);
-        if constexpr (EXACT)
+        if constexpr (FMT == kMxFp8)
           acc[i][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(o.w[i]), ah[m], acc[i][m], 4, kCbsz<FMT>,
                                                                       j, (int)c.w[i], j, (int)c.a[m]);
       }
   };
-  constexpr int kReads = NT + (FMT == kMxFp8 ? 2 : 1) * MT, kProducts = NT * MT * (EXACT ? 2 : 1);
+  constexpr int kReads = NT + (FMT == kMxFp8 ? 2 : 1) * MT, kProducts = NT * MT * (FMT == kMxFp8 ? 2 : 1);
   // The copies of stage s + B go into the buffer of stage s: one half during
   // the last step of stage s, the other during the first of the next stage.
   constexpr std::true_type kWhole;
@@ -655,15 +651,15 @@ int mx_tile_k(int fmt, int size) {
   return 64 * (size >= 224 ? Tile256<kMxFp8>::S : size == 128 ? Tile128<kMxFp8>::S : Tile64<kMxFp8>::S);
 }
 
-template <int FMT, bool EXACT, typename T>
+template <int FMT, typename T>
 hipError_t launch_tile(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        const MxPlan& plan, void* workspace, hipStream_t stream) {
   const int tiles_m = (int)((m + T::TM - 1) / T::TM), tiles_n = (int)((n + T::TN - 1) / T::TN);
   const dim3 grid((unsigned)(tiles_m * tiles_n), (unsigned)plan.splits);
-  hipError_t e = set_tile_lds<k_mx_tile<FMT, EXACT, T>, T::kLds>();
+  hipError_t e = set_tile_lds<k_mx_tile<FMT, T>, T::kLds>();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_mx_tile<FMT, EXACT, T>), grid, dim3(256), T::kLds, stream, a_codes, a_scales, w_codes,
+  hipLaunchKernelGGL((k_mx_tile<FMT, T>), grid, dim3(256), T::kLds, stream, a_codes, a_scales, w_codes,
                      w_scales, y, static_cast<float*>(workspace), (int)m, (int)n, (int)k, tiles_m, tiles_n,
                      plan.stages_per, out_f32);
   e = hipGetLastError();
@@ -693,7 +689,7 @@ __global__ __launch_bounds__(256) void k_plane_sum(const float* __restrict__ pla
   }
 }
 
-template <int FMT, bool EXACT>
+template <int FMT>
 hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                        const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                        hipStream_t stream) {
@@ -714,13 +710,13 @@ hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const ui
     };
     // a stays in registers where its way there is paid for by several tiles (one tile: 4.3 against 4.5 us at 1 x
     // 4096 x 4096; four: 9.8 against 11.0 at 16 x 14336 x 4096)
-    if (k == 4096 && tiles > kRowGroups) return ring(Ring<FMT, EXACT, true, 16, 8, 4>{});
-    if (m <= 4) return ring(Ring<FMT, EXACT, false, 4, 8, FMT == kMxFp4 ? 3 : 2>{});
-    return ring(Ring<FMT, EXACT, false, 16, FMT == kMxFp4 ? 8 : 4, FMT == kMxFp4 ? 2 : 3>{});
+    if (k == 4096 && tiles > kRowGroups) return ring(Ring<FMT, true, 16, 8, 4>{});
+    if (m <= 4) return ring(Ring<FMT, false, 4, 8, FMT == kMxFp4 ? 3 : 2>{});
+    return ring(Ring<FMT, false, 16, FMT == kMxFp4 ? 8 : 4, FMT == kMxFp4 ? 2 : 3>{});
   }
   // chunks of 512 once every wave has one
-  if (k >= 512 * kRowWaves) go(k_mx_rows<FMT, EXACT, 4>);
-  else go(k_mx_rows<FMT, EXACT, 1>);
+  if (k >= 512 * kRowWaves) go(k_mx_rows<FMT, 4>);
+  else go(k_mx_rows<FMT, 1>);
   return hipGetLastError();
 }
 
@@ -736,19 +732,19 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 // The kernel, tile and split with the least expected time, from times measured
 // on MI355X (microseconds, MXFP4 / MXFP8 activations).  A round of workgroups
 // over 256 of K takes
-//   64 x 64 tiles:   0.46 / 0.50 with at most one workgroup per CU, 0.60 / 0.75 with two
-//   128 x 128:       1.0 / 1.3, 1.5 with two (MXFP8: its LDS leaves room for one)
-//   256 x 256:       2.5 / 3.4
-//   256 x 224 (n):   2.27 / 3.0
+//   64 x 64 tiles:   0.46 / 0.80 with at most one workgroup per CU, 0.60 / 1.22 with two
+//   128 x 128:       1.0 / 2.15, 1.5 with two (MXFP8: its LDS leaves room for one)
+//   256 x 256:       2.5 / 5.4
+//   256 x 224 (n):   2.27 / 4.9
 // beside about 2 for a launch, and a split of K 3 for its second launch and the
-// planes' traffic.  So few outputs take small tiles, for more workgroups, and many
+// planes' traffic (written and read again at 3 / 5 TB/s).  So few outputs take small tiles, for more workgroups, and many
 // large ones, which read each operand less often: 1024 x 4096 x 4096 (m, n, k)
 // with MXFP4 took 21.5 / 17.6 / 32.0 with the three tiles, 512 x 4096 x 4096
 // 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
 // x 4096 281 / 175 / 158.  The 256 x 224 tile is for n = 7 2^i, whose rounds it
 // fills: 4096 x 14336 x 4096 in four rounds instead of three and a half of the
-// square tile took 143 / 208 (326 with fp32 output) against 149 / 226 (379), but
-// 2048 x 8192 x 4096 64 / 95 against 40 / 61.  64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
+// square tile took 142 / 316 against 144 / 350, but 2048 x 8192 x 4096 64 / 150
+// against 41 / 97.  64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
 // four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   MxPlan best{0, 1, 0, 0};
@@ -759,7 +755,8 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
     double alone, full;  // time of a round of at most 256 workgroups, of `slots`
   };
   static const Shape kFp4[4] = {{64, 512, 0.46, 0.60}, {128, 512, 1.0, 1.5}, {256, 256, 2.5, 2.5}, {224, 256, 2.27, 2.27}};
-  static const Shape kFp8[4] = {{64, 512, 0.50, 0.75}, {128, 256, 1.3, 1.3}, {256, 256, 3.4, 3.4}, {224, 256, 3.0, 3.0}};
+  static const Shape kFp8[4] = {{64, 512, 0.80, 1.22}, {128, 256, 2.15, 2.15}, {256, 256, 5.4, 5.4}, {224, 256, 4.9, 4.9}};
+  const double rate = a_fmt == kMxFp4 ? 3.0e6 : 5.0e6;  // bytes of planes per microsecond
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
     const Shape& t = a_fmt == kMxFp4 ? kFp4[i] : kFp8[i];
@@ -771,7 +768,7 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
       const int64_t rest = all % t.slots;
       const double rounds = (double)(all / t.slots) * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full);
       double time = 2.0 + rounds * (double)(per * bk) / 256.0;
-      if (z > 1) time += 3.0 + 8.0 * (double)z * (double)m * (double)n / 3.0e6;
+      if (z > 1) time += 3.0 + 8.0 * (double)z * (double)m * (double)n / rate;
       if (time < least) {
         least = time;
         best.tile = t.size;
@@ -785,16 +782,16 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
 }
 
 namespace {
-template <int FMT, bool EXACT>
+template <int FMT>
 hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
-  if (plan.tile == 256) return go(launch_tile<FMT, EXACT, Tile256<FMT>>);
-  if (plan.tile == 224) return go(launch_tile<FMT, EXACT, Tile224<FMT>>);
-  if (plan.tile == 128) return go(launch_tile<FMT, EXACT, Tile128<FMT>>);
-  if (plan.tile == 64) return go(launch_tile<FMT, EXACT, Tile64<FMT>>);
-  return launch_rows<FMT, EXACT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
+  if (plan.tile == 256) return go(launch_tile<FMT, Tile256<FMT>>);
+  if (plan.tile == 224) return go(launch_tile<FMT, Tile224<FMT>>);
+  if (plan.tile == 128) return go(launch_tile<FMT, Tile128<FMT>>);
+  if (plan.tile == 64) return go(launch_tile<FMT, Tile64<FMT>>);
+  return launch_rows<FMT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
 }
 }  // namespace
 
@@ -802,8 +799,7 @@ hipError_t launch_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a
                           const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
                           const MxPlan& plan, void* workspace, hipStream_t stream) {
   auto go = [&](auto f) { return f(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan, workspace, stream); };
-  if (a_fmt == kMxFp4) return go(launch_product<kMxFp4, false>);
-  return out_f32 ? go(launch_product<kMxFp8, true>) : go(launch_product<kMxFp8, false>);
+  return a_fmt == kMxFp4 ? go(launch_product<kMxFp4>) : go(launch_product<kMxFp8>);
 }
 
 }  // namespace nvfp4

@@ -512,3 +512,22 @@ def test_large_offsets():
     ref, _ = mx.add_rmsnorm_backward(z, z, np.ones(k), r)
     size = r[:, None] * (np.abs(z) + np.abs(z * r[:, None]) * np.mean(z * z, -1, keepdims=True) * r[:, None])
     assert np.all(np.abs(_np(dx[-3:]) - ref) <= (94 * U32 * size) * (1 + UBF16) + (UBF16 + 2 * U32) * np.abs(ref))
+
+
+# every kernel of few rows (k below 4096, at it with many weight rows, past it in whole chunks of 512 or not) and tiles
+@pytest.mark.parametrize("m,n,k", [(5, 40, 512), (5, 40, 4128), (3, 4200, 4096), (4, 70, 5120), (9, 45, 8192),
+                                   (150, 300, 512), (700, 2046, 1056)])
+def test_gemm_fp8_drops_nothing_in_either_output_type(m, n, k):
+    # every group of 8 is led by +-448 * 6, which cancels over two groups; the other seven codes lie anywhere between
+    # 2^-9 and 16.  All products are whole multiples of 2^-10 and the sums stay below 2^14: fp32 holds each of them
+    # exactly in any order, and a bf16 output is the exact sum rounded once
+    g = np.random.default_rng(160 + m)
+    c = (g.integers(1, 0x51, (m, k)) | g.integers(0, 2, (m, k)) << 7).astype(np.uint8)
+    c[:, 0::16], c[:, 8::16] = 0x7E, 0xFE
+    wc = (g.integers(0, 2, (n, k)) * 2 + 1 | g.integers(0, 2, (n, k)) << 3).astype(np.uint8)  # +-0.5, +-1.5
+    wc[:, 0::8] = 0x7
+    s, ws = np.full((m, k // 32), 127, dtype=np.uint8), np.full((n, k // 32), 127, dtype=np.uint8)
+    ref = mx.dequant_mx(c, s, mx.FP8) @ mx.dequant_mx(mx.pack(wc, mx.FP4), ws, mx.FP4).T
+    a, w = _mx(c, s, nv.MXFP8), _mx(mx.pack(wc, mx.FP4), ws, nv.MXFP4)
+    assert np.array_equal(_np(nv.mx_gemm(a, w, out_dtype=torch.float32)), ref)
+    assert np.array_equal(_np(nv.mx_gemm(a, w)), mx.round_bf16(ref.astype(np.float32)).astype(np.float64))
