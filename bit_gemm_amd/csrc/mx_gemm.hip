@@ -734,10 +734,13 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 // over 256 of K takes
 //   64 x 64 tiles:   0.46 / 0.80 with at most one workgroup per CU, 0.60 / 1.22 with two
 //   128 x 128:       1.0 / 2.15, 1.5 with two (MXFP8: its LDS leaves room for one)
-//   256 x 256:       2.5 / 5.4
-//   256 x 224 (n):   2.27 / 4.9
-// beside about 2 for a launch, and a split of K 3 for its second launch and the
-// planes' traffic (written and read again at 3 / 5 TB/s).  So few outputs take small tiles, for more workgroups, and many
+//   256 x 256:       2.5 / 5.2
+//   256 x 224 (n):   2.27 / 4.7
+// beside about 2 for a launch (MXFP8: 5 with 128 x 128, 9 with the larger tiles,
+// whose first loads and stores nothing else hides), and a split of K 3 for its
+// second launch and the planes' traffic (written and read again at 3 / 4 TB/s).
+// The choice these times give was within 12 % of the fastest tile and split at
+// each of 40 sizes with MXFP8 a.  So few outputs take small tiles, for more workgroups, and many
 // large ones, which read each operand less often: 1024 x 4096 x 4096 (m, n, k)
 // with MXFP4 took 21.5 / 17.6 / 32.0 with the three tiles, 512 x 4096 x 4096
 // 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
@@ -752,11 +755,13 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   if (m <= 16 || k > ((int64_t)1 << 22)) return best;
   struct Shape {
     int size, slots;
-    double alone, full;  // time of a round of at most 256 workgroups, of `slots`
+    double alone, full, start;  // time of a round of at most 256 workgroups, of `slots`, of a launch
   };
-  static const Shape kFp4[4] = {{64, 512, 0.46, 0.60}, {128, 512, 1.0, 1.5}, {256, 256, 2.5, 2.5}, {224, 256, 2.27, 2.27}};
-  static const Shape kFp8[4] = {{64, 512, 0.80, 1.22}, {128, 256, 2.15, 2.15}, {256, 256, 5.4, 5.4}, {224, 256, 4.9, 4.9}};
-  const double rate = a_fmt == kMxFp4 ? 3.0e6 : 5.0e6;  // bytes of planes per microsecond
+  static const Shape kFp4[4] = {
+      {64, 512, 0.46, 0.60, 2.0}, {128, 512, 1.0, 1.5, 2.0}, {256, 256, 2.5, 2.5, 2.0}, {224, 256, 2.27, 2.27, 2.0}};
+  static const Shape kFp8[4] = {
+      {64, 512, 0.80, 1.22, 2.0}, {128, 256, 2.15, 2.15, 5.0}, {256, 256, 5.2, 5.2, 9.0}, {224, 256, 4.7, 4.7, 9.0}};
+  const double rate = a_fmt == kMxFp4 ? 3.0e6 : 4.0e6;  // bytes of planes per microsecond
   double least = 1e300;
   for (int i = 0; i < 4; ++i) {
     const Shape& t = a_fmt == kMxFp4 ? kFp4[i] : kFp8[i];
@@ -767,7 +772,7 @@ MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
       const int64_t per = (stages + z - 1) / z, all = count * ((stages + per - 1) / per);
       const int64_t rest = all % t.slots;
       const double rounds = (double)(all / t.slots) * t.full + (rest == 0 ? 0.0 : rest <= 256 ? t.alone : t.full);
-      double time = 2.0 + rounds * (double)(per * bk) / 256.0;
+      double time = t.start + rounds * (double)(per * bk) / 256.0;
       if (z > 1) time += 3.0 + 8.0 * (double)z * (double)m * (double)n / rate;
       if (time < least) {
         least = time;
