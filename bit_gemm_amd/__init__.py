@@ -77,9 +77,11 @@ SIGNATURES = {
     "nvfp4_mx_quantize": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
     "nvfp4_mx_dequant": (_c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_int, _c_int, _c_p]),
     "nvfp4_mx_gemm_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "nvfp4_mx_gemm_path": (_c_int, [_c_i64, _c_i64, _c_i64, _c_int]),
     "nvfp4_mx_gemm": (_c_int, [_c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_size,
                                _c_p]),
     "nvfp4_mx_gemm_dx_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "nvfp4_mx_gemm_dx_path": (_c_int, [_c_i64, _c_i64, _c_i64]),
     "nvfp4_mx_gemm_dx": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_size, _c_p]),
     "nvfp4_add_rmsnorm_mx": (_c_int, [_c_p, _c_p, _c_p, _c_int, ctypes.c_float, _c_i64, _c_i64, _c_int, _c_p, _c_p,
                                       _c_p, _c_p, _c_p]),
@@ -736,6 +738,11 @@ def mx_gemm_workspace_size(m: int, n: int, k: int, a_fmt: int) -> int:
     return int(lib().nvfp4_mx_gemm_workspace_size(m, n, k, a_fmt))
 
 
+def mx_gemm_path(m: int, n: int, k: int, a_fmt: int) -> int:
+    """The kernel mx_gemm takes (see nvfp4_mx_gemm_path in include/nvfp4.h)."""
+    return int(lib().nvfp4_mx_gemm_path(m, n, k, a_fmt))
+
+
 def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[m, n] = a[m, k] @ w[n, k]^T for MXFP4 or MXFP8 a and MXFP4 w."""
@@ -761,6 +768,11 @@ def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, o
 
 def mx_gemm_dx_workspace_size(m: int, n: int, k: int) -> int:
     return int(lib().nvfp4_mx_gemm_dx_workspace_size(m, n, k))
+
+
+def mx_gemm_dx_path(m: int, n: int, k: int) -> int:
+    """The tile mx_gemm_dx takes (see nvfp4_mx_gemm_dx_path in include/nvfp4.h)."""
+    return int(lib().nvfp4_mx_gemm_dx_path(m, n, k))
 
 
 def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16,

@@ -167,9 +167,10 @@ hipError_t launch_mx_dequant(const uint8_t* codes, const uint8_t* scales, void* 
                              int out_f32, hipStream_t stream);
 
 // y[m, n] = a[m, k] . w[n, k]^T, a in MXFP4 or MXFP8, w in MXFP4.  tile: 0 =
-// the kernel for few rows of a, else 64, 128 or 256: that many squared outputs
-// per workgroup, or 224: 256 (m) x 224, with K split over `splits` of them, `stages_per` LDS stages
-// each (fp32 planes [splits, m, n] in the workspace, then launch_plane_sum).
+// the kernel for few rows of a, 16 = the one that stages them by DMA, else 64,
+// 128 or 256: that many squared outputs per workgroup, or 224: 256 (m) x 224,
+// with K split over `splits` of them, `stages_per` LDS stages each (fp32 planes
+// [splits, m, n] in the workspace, then launch_plane_sum).
 struct MxPlan {
   int tile;
   int splits;

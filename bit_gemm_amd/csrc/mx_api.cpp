@@ -127,6 +127,11 @@ NVFP4_API size_t nvfp4_mx_gemm_workspace_size(int64_t m, int64_t n, int64_t k, i
   return nvfp4::plan_mx_gemm(m, n, k, a_format).ws_bytes;
 }
 
+NVFP4_API int nvfp4_mx_gemm_path(int64_t m, int64_t n, int64_t k, int a_format) {
+  if (!product_sizes_ok(m, n, k) || (a_format != NVFP4_MXFP4 && a_format != NVFP4_MXFP8)) return -1;
+  return nvfp4::plan_mx_gemm(m, n, k, a_format).tile;
+}
+
 NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a_format, const uint8_t* w_codes,
                             const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_dtype,
                             void* workspace, size_t workspace_bytes, void* stream) {
@@ -149,6 +154,10 @@ NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
 
 NVFP4_API size_t nvfp4_mx_gemm_dx_workspace_size(int64_t m, int64_t n, int64_t k) {
   return product_sizes_ok(m, n, k) ? nvfp4::plan_mx_dx(m, n, k).ws_bytes : 0;
+}
+
+NVFP4_API int nvfp4_mx_gemm_dx_path(int64_t m, int64_t n, int64_t k) {
+  return product_sizes_ok(m, n, k) ? nvfp4::plan_mx_dx(m, n, k).tile : -1;
 }
 
 NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uint8_t* w_scales, void* dx, int64_t m,

@@ -691,7 +691,7 @@ __global__ __launch_bounds__(256) void k_plane_sum(const float* __restrict__ pla
 
 template <int FMT>
 hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
-                       const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32,
+                       const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_f32, bool dma,
                        hipStream_t stream) {
   const int64_t tiles = (n + 15) / 16;
   const dim3 grid((unsigned)(tiles < kRowGroups ? tiles : kRowGroups), (unsigned)((m + 15) / 16)), block(64 * kRowWaves);
@@ -699,7 +699,7 @@ hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const ui
     hipLaunchKernelGGL(kernel, grid, block, 0, stream, a_codes, a_scales, w_codes, w_scales, y, (int)m, (int)n, (int)k,
                        out_f32);
   };
-  if (m <= 16 && k >= 4096 && k % 512 == 0 && k <= ((int64_t)1 << 22)) {  // whole chunks, 32-bit offsets in a tile
+  if (dma) {
     auto ring = [&](auto tc) {
       using T = decltype(tc);
       hipError_t e = set_tile_lds<k_mx_rows_dma<T>, T::kLds>();
@@ -751,8 +751,9 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 // four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   MxPlan best{0, 1, 0, 0};
-  // up to 16 rows: the other kernel; also where a tile's rows pass 32-bit offsets
-  if (m <= 16 || k > ((int64_t)1 << 22)) return best;
+  const bool offsets = k <= ((int64_t)1 << 22);  // a tile's rows within 32-bit offsets
+  if (m <= 16 && k >= 4096 && k % 512 == 0 && offsets) best.tile = 16;  // whole chunks, one for every wave at least
+  if (m <= 16 || !offsets) return best;
   struct Shape {
     int size, slots;
     double alone, full, start;  // time of a round of at most 256 workgroups, of `slots`, of a launch
@@ -796,7 +797,7 @@ hipError_t launch_product(const uint8_t* a_codes, const uint8_t* a_scales, const
   if (plan.tile == 224) return go(launch_tile<FMT, Tile224<FMT>>);
   if (plan.tile == 128) return go(launch_tile<FMT, Tile128<FMT>>);
   if (plan.tile == 64) return go(launch_tile<FMT, Tile64<FMT>>);
-  return launch_rows<FMT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, stream);
+  return launch_rows<FMT>(a_codes, a_scales, w_codes, w_scales, y, m, n, k, out_f32, plan.tile == 16, stream);
 }
 }  // namespace
 

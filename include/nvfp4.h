@@ -459,6 +459,12 @@ NVFP4_API int nvfp4_mx_dequant(const uint8_t* codes, const uint8_t* scales, void
  * workspace  as nvfp4_w4a16_gemm, of nvfp4_mx_gemm_workspace_size bytes.
  */
 NVFP4_API size_t nvfp4_mx_gemm_workspace_size(int64_t m, int64_t n, int64_t k, int a_format);
+/* The kernel nvfp4_mx_gemm takes for these sizes: 0 or 16 (at most 16 rows of a
+ * or very long k; 16: staged by DMA), else its tile: 64, 128 or 256 (that many
+ * squared outputs per workgroup) or 224 (256 x 224).  K is split over workgroups
+ * where the workspace size is not 0.  -1 where no kernel runs (an empty product,
+ * or one that is refused). */
+NVFP4_API int nvfp4_mx_gemm_path(int64_t m, int64_t n, int64_t k, int a_format);
 NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int a_format, const uint8_t* w_codes,
                             const uint8_t* w_scales, void* y, int64_t m, int64_t n, int64_t k, int out_dtype,
                             void* workspace, size_t workspace_bytes, void* stream);
@@ -470,6 +476,8 @@ NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
  * Sizes as nvfp4_mx_gemm; n == 0 writes zeros; pointers 16-byte aligned.
  */
 NVFP4_API size_t nvfp4_mx_gemm_dx_workspace_size(int64_t m, int64_t n, int64_t k);
+/* The tile nvfp4_mx_gemm_dx takes (128 or 256), as nvfp4_mx_gemm_path. */
+NVFP4_API int nvfp4_mx_gemm_dx_path(int64_t m, int64_t n, int64_t k);
 NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uint8_t* w_scales, void* dx, int64_t m,
                                int64_t n, int64_t k, int out_dtype, void* workspace, size_t workspace_bytes,
                                void* stream);

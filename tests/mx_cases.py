@@ -68,3 +68,35 @@ def product_bound(a, w, fmt, out_dtype):
         bound = bound + 7 * 2.0 ** -14 * mag
     half = UBF16 if out_dtype == torch.bfloat16 else U32
     return ref, bound * (1 + half) + half * np.abs(ref)
+
+
+# (format of a, path, K split over workgroups, m, n, k): every kernel and tile of
+# mx_gemm, whole and split, with remainders in m, n and k; for the tiles rows of
+# n even, odd and a multiple of 8 (each stored its own way).  MXFP4 never splits
+# the 256 tile.  test_mx_host.py holds the paths to the library's plan.
+GEMM_PATHS = [
+    (mx.FP4, 0, False, 5, 83, 992), (mx.FP4, 0, False, 13, 4131, 4640), (mx.FP4, 16, False, 1, 4215, 4096),
+    (mx.FP4, 16, False, 15, 4200, 4096), (mx.FP4, 16, False, 16, 133, 4096), (mx.FP4, 16, False, 4, 4503, 4608),
+    (mx.FP4, 16, False, 3, 70, 7680), (mx.FP4, 16, False, 5, 4100, 5120), (mx.FP4, 16, False, 16, 97, 14336),
+    (mx.FP4, 64, False, 67, 131, 1056), (mx.FP4, 64, False, 142, 138, 96), (mx.FP4, 64, True, 50, 1715, 6592),
+    (mx.FP4, 64, True, 20, 16, 2368), (mx.FP4, 128, False, 388, 4739, 1056), (mx.FP4, 128, False, 342, 5632, 1056),
+    (mx.FP4, 128, False, 323, 5441, 32), (mx.FP4, 128, True, 17, 2103, 14880), (mx.FP4, 128, True, 66, 4104, 8320),
+    (mx.FP4, 224, False, 1046, 7244, 1088), (mx.FP4, 224, False, 1951, 4231, 1056), (mx.FP4, 224, False, 1542, 5136, 1184),
+    (mx.FP4, 224, True, 3345, 577, 15264), (mx.FP4, 224, True, 2421, 872, 16064), (mx.FP4, 256, False, 3862, 3659, 1056),
+    (mx.FP4, 256, False, 2172, 6632, 1088), (mx.FP4, 256, False, 2278, 6394, 288),
+    (mx.FP8, 0, False, 5, 83, 992), (mx.FP8, 0, False, 13, 4131, 4640), (mx.FP8, 16, False, 1, 4215, 4096),
+    (mx.FP8, 16, False, 15, 4200, 4096), (mx.FP8, 16, False, 16, 133, 4096), (mx.FP8, 16, False, 4, 4503, 4608),
+    (mx.FP8, 16, False, 3, 70, 7680), (mx.FP8, 16, False, 5, 4100, 5120), (mx.FP8, 16, False, 16, 97, 14336),
+    (mx.FP8, 64, False, 67, 131, 1056), (mx.FP8, 64, False, 142, 138, 96), (mx.FP8, 64, True, 50, 1715, 6592),
+    (mx.FP8, 64, True, 17, 16, 1888), (mx.FP8, 128, False, 1573, 1923, 1568), (mx.FP8, 128, False, 472, 6232, 1632),
+    (mx.FP8, 128, False, 650, 4484, 1664), (mx.FP8, 128, True, 70, 2077, 9440), (mx.FP8, 128, True, 2068, 72, 11424),
+    (mx.FP8, 224, False, 1860, 4474, 1056), (mx.FP8, 224, False, 1447, 5843, 1056), (mx.FP8, 224, False, 1215, 7176, 1088),
+    (mx.FP8, 224, True, 4197, 69, 13216), (mx.FP8, 224, True, 585, 784, 16032), (mx.FP8, 256, False, 3862, 3659, 1056),
+    (mx.FP8, 256, False, 2615, 5320, 1056), (mx.FP8, 256, True, 262, 3826, 11808), (mx.FP8, 256, True, 271, 4016, 13632),
+]
+# (tile, n split over workgroups, m, n, k) of mx_gemm_dx; rows of dy that are no whole 16-byte pieces have a kernel of their own
+DX_PATHS = [
+    (128, False, 129, 264, 96), (128, False, 300, 331, 2080), (128, False, 600, 72, 4128), (128, True, 131, 1001, 1056),
+    (128, True, 65, 4104, 4128), (128, True, 3, 2050, 64), (256, False, 1050, 776, 12192), (256, False, 2209, 904, 5472),
+    (256, False, 1000, 1000, 14304), (256, True, 149, 6432, 8800), (256, True, 1246, 6072, 1568),
+]

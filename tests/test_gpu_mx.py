@@ -8,7 +8,7 @@ import torch
 
 import bit_gemm_amd as nv
 import oracle.mx as mx
-from mx_cases import U32, UBF16, product_bound, rows, special_rows, weights
+from mx_cases import DX_PATHS, GEMM_PATHS, U32, UBF16, product_bound, rows, special_rows, weights
 
 pytestmark = pytest.mark.gpu
 
@@ -531,3 +531,69 @@ def test_gemm_fp8_drops_nothing_in_either_output_type(m, n, k):
     a, w = _mx(c, s, nv.MXFP8), _mx(mx.pack(wc, mx.FP4), ws, nv.MXFP4)
     assert np.array_equal(_np(nv.mx_gemm(a, w, out_dtype=torch.float32)), ref)
     assert np.array_equal(_np(nv.mx_gemm(a, w)), mx.round_bf16(ref.astype(np.float32)).astype(np.float64))
+
+
+def _exact_mx(rows_, k, fmt, gen):
+    """Random elements (all E2M1 codes; E4M3 codes of 1/8 up to 15) with scales 1/2 and 1: a product of two such
+    matrices has products of whole multiples of 2^-9, at most 90, and sums that stay far below 2^24 of those (random
+    walks of at most 16064 steps of 10 in the mean): fp32 holds every partial sum in any order."""
+    if fmt == nv.MXFP4:
+        codes = torch.randint(0, 256, (rows_, k // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    else:
+        codes = torch.randint(0x20, 0x58, (rows_, k), generator=gen, device="cuda", dtype=torch.uint8)
+        codes = codes | torch.randint(0, 2, (rows_, k), generator=gen, device="cuda", dtype=torch.uint8) << 7
+    return nv.MXTensor(codes, torch.randint(126, 128, (rows_, k // 32), generator=gen, device="cuda", dtype=torch.uint8), fmt)
+
+
+def _guarded(m, n, dtype):
+    big = torch.full((m * n + 4096,), 7.0, dtype=dtype, device="cuda")
+    return big, big[: m * n].view(m, n)
+
+
+@pytest.mark.parametrize("fmt,path,split,m,n,k", GEMM_PATHS)
+def test_every_gemm_kernel_to_the_last_bit(fmt, path, split, m, n, k):
+    print("mx gemm", fmt, path, split, m, n, k, flush=True)
+    assert nv.mx_gemm_path(m, n, k, fmt) == path and (nv.mx_gemm_workspace_size(m, n, k, fmt) > 0) == split
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    a, w = _exact_mx(m, k, fmt, gen), _exact_mx(n, k, nv.MXFP4, gen)
+    a.scales[m - 1, -1] = 255  # the last row and column are NaN, and nothing else
+    w.scales[n - 1, 0] = 255
+    ref = nv.dequant_mx(a).double() @ nv.dequant_mx(w).double().t()
+    for dt in (torch.float32, torch.bfloat16):
+        big, out = _guarded(m, n, dt)
+        y = nv.mx_gemm(a, w, out_dtype=dt, out=out)
+        assert bool((y == ref.float().to(dt))[:-1, :-1].all()), dt
+        assert bool(y[-1].isnan().all()) and bool(y[:, -1].isnan().all()) and bool((big[m * n:] == 7.0).all())
+
+
+@pytest.mark.parametrize("path,split,m,n,k", DX_PATHS)
+def test_every_gemm_dx_kernel_to_the_last_bit(path, split, m, n, k):
+    # quarters up to 1 times weights as above: every partial sum is exact in fp32
+    print("mx gemm_dx", path, split, m, n, k, flush=True)
+    assert nv.mx_gemm_dx_path(m, n, k) == path and (nv.mx_gemm_dx_workspace_size(m, n, k) > 0) == split
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    w = _exact_mx(n, k, nv.MXFP4, gen)
+    dy = (torch.randint(-4, 5, (m, n), generator=gen, device="cuda") / 4).bfloat16()
+    dy[m - 1, n - 1] = float("nan")  # one row of NaN
+    w.scales[n - 1, -1] = 255  # and one block of columns
+    ref = dy.double() @ nv.dequant_mx(w).double()
+    for dt in (torch.float32, torch.bfloat16):
+        big, out = _guarded(m, k, dt)
+        dx = nv.mx_gemm_dx(dy, w, out_dtype=dt, out=out)
+        assert bool((dx == ref.float().to(dt))[:-1, :-32].all()), dt
+        assert bool(dx[-1].isnan().all()) and bool(dx[:, -32:].isnan().all()) and bool((big[m * k:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fmt,path,split,m,n,k", [c for c in GEMM_PATHS if c[0] == nv.MXFP8 and c[1] >= 64])
+def test_gemm_fp8_drops_nothing_in_any_tile(fmt, path, split, m, n, k):
+    # the codes of test_gemm_fp8_drops_nothing_in_either_output_type, in every tile
+    print("mx gemm", fmt, path, split, m, n, k, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(m + n)
+    bits = lambda lo, hi, r: torch.randint(lo, hi, (r, k), generator=gen, device="cuda", dtype=torch.uint8)  # noqa: E731
+    c, wc = bits(1, 0x51, m) | bits(0, 2, m) << 7, bits(0, 2, n) * 2 + 1 | bits(0, 2, n) << 3
+    c[:, 0::16], c[:, 8::16], wc[:, 0::8] = 0x7E, 0xFE, 0x7
+    ones = lambda r: torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    a, w = nv.MXTensor(c, ones(m), nv.MXFP8), nv.MXTensor(wc[:, 0::2] | wc[:, 1::2] << 4, ones(n), nv.MXFP4)
+    ref = (nv.dequant_mx(a).double() @ nv.dequant_mx(w).double().t()).float()
+    assert torch.equal(nv.mx_gemm(a, w, out_dtype=torch.float32), ref)
+    assert torch.equal(nv.mx_gemm(a, w), ref.bfloat16())

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import bit_gemm_amd as nv
+from mx_cases import DX_PATHS, GEMM_PATHS
 
 FAKE, ODD = 0x10000, 0x10008  # never dereferenced
 
@@ -148,3 +149,20 @@ def test_binding_refuses():
         nv.add_rmsnorm_backward(x, x, w, torch.ones(3))
     with pytest.raises(ValueError, match="GPU"):
         nv.add_rmsnorm_backward(x, x, w, torch.ones(4))
+
+
+def test_paths(L):
+    """Every kernel and tile of the products is on the list that the GPU tests run, at a size that the plan gives it."""
+    for fmt, path, split, m, n, k in GEMM_PATHS:
+        assert nv.mx_gemm_path(m, n, k, fmt) == path, (fmt, m, n, k)
+        assert (nv.mx_gemm_workspace_size(m, n, k, fmt) > 0) == split, (fmt, m, n, k)
+    for path, split, m, n, k in DX_PATHS:
+        assert nv.mx_gemm_dx_path(m, n, k) == path and (nv.mx_gemm_dx_workspace_size(m, n, k) > 0) == split, (m, n, k)
+    forms = {(fmt, path, split) for fmt, path, split, *_ in GEMM_PATHS}
+    tiles = {(f, t, z) for f in (nv.MXFP4, nv.MXFP8) for t in (64, 128, 224, 256) for z in (False, True)}
+    assert forms == {(f, t, False) for f in (nv.MXFP4, nv.MXFP8) for t in (0, 16)} | tiles - {(nv.MXFP4, 256, True)}
+    assert {(t, z, n % 8 == 0) for t, z, _, n, _ in DX_PATHS} == \
+        {(128, z, w) for z in (False, True) for w in (False, True)} | {(256, False, True), (256, True, True)}
+    for bad in ((0, 8, 64), (4, 0, 64), (4, 8, 0), (4, 8, 48), (-1, 8, 64), (4, 1 << 27, 64)):
+        assert nv.mx_gemm_path(*bad, nv.MXFP4) == -1 and nv.mx_gemm_dx_path(*bad) == -1
+    assert nv.mx_gemm_path(4, 8, 64, 5) == -1
