@@ -597,3 +597,35 @@ def test_gemm_fp8_drops_nothing_in_any_tile(fmt, path, split, m, n, k):
     ref = (nv.dequant_mx(a).double() @ nv.dequant_mx(w).double().t()).float()
     assert torch.equal(nv.mx_gemm(a, w, out_dtype=torch.float32), ref)
     assert torch.equal(nv.mx_gemm(a, w), ref.bfloat16())
+
+
+# more than 512 rows: rows that divide neither a workgroup's group nor 256 workgroups, up to five turns per
+# workgroup, at widths of every number of threads and pieces per row
+@pytest.mark.parametrize("m,k", [(9001, 64), (4099, 512), (2501, 544), (1030, 2048), (1029, 2080), (4099, 4096), (1027, 4128),
+                                 (2051, 8192), (700, 11008), (1283, 16384), (515, 16416), (769, 32768), (515, 32800),
+                                 (513, 65536)])
+def test_norm_backward_many_rows(m, k):
+    print("norm backward", m, k, flush=True)
+    gen = torch.Generator(device="cuda").manual_seed(m + k)
+    R = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    for with_ds, wdtype in ((True, torch.bfloat16), (False, torch.float32)):
+        dh, s, ds = (R(m, k).bfloat16() for _ in range(3))
+        w, rstd = (1 + 0.2 * R(k)).to(wdtype), 0.5 + torch.rand(m, generator=gen, device="cuda")
+        big = torch.full(((m + 2) * k,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = big[: m * k].view(m, k)
+        if with_ds:
+            out.copy_(ds)  # in place
+        dx, dw = nv.add_rmsnorm_backward(dh, s, w, rstd, ds=out if with_ds else None, dx=out)
+        assert bool((big[m * k:] == 7.0).all())
+        r, g = rstd.double()[:, None], dh.double() * w.double()
+        xh = s.double() * r
+        ref = r * (g - xh * (g * xh).mean(-1, keepdim=True)) + (ds.double() if with_ds else 0)
+        # dx: as in test_norm_backward
+        size = r * (g.abs() + xh.abs() * (g * xh).abs().mean(-1, keepdim=True))
+        bound = (64 + 6 + 16 + 8) * U32 * size + 2 * U32 * ref.abs() + (U32 * ds.double().abs() if with_ds else 0)
+        assert bool(((dx.double() - ref).abs() <= bound * (1 + UBF16) + UBF16 * ref.abs()).all())
+        # dweight: a workgroup adds m / (256 groups) rows, at most 16 groups and 256 planes (8 + 6 steps deep);
+        # 2 roundings in a term
+        terms = dh.double() * xh
+        bound = (-(-m // 256) + 16 + 14 + 2) * U32 * terms.abs().sum(0)
+        assert bool(((dw.double() - terms.sum(0)).abs() <= bound).all())
