@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include "../../include/nvfp4.h"
 #include "launchers.h"
@@ -86,6 +87,34 @@ int check_norm(int64_t m, int64_t k, int weight_dtype) {
   // a row of more than 16384 elements has a workgroup of 1024 threads
   if (m >= kMaxTokens) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "m=%lld too large", (long long)m);
   return check_type(weight_dtype, "weight_dtype");
+}
+
+// A buffer of a call; NULL or no bytes: none.
+struct Buffer {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+
+bool overlap(const Buffer& a, const Buffer& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x && y && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+
+// An output that shares memory with an input or another output is written by one workgroup while another reads or
+// writes it: refused, but where the output is that whole buffer and every thread reads what it then writes (`in_place`).
+int check_outputs(std::initializer_list<Buffer> outputs, std::initializer_list<Buffer> inputs,
+                  std::initializer_list<Buffer> in_place) {
+  for (const Buffer* o = outputs.begin(); o != outputs.end(); ++o) {
+    for (const Buffer& i : inputs)
+      if (overlap(*o, i)) return fail(NVFP4_ERR_INVALID_VALUE, "%s overlaps %s", o->name, i.name);
+    for (const Buffer* q = outputs.begin(); q != o; ++q)
+      if (overlap(*o, *q)) return fail(NVFP4_ERR_INVALID_VALUE, "%s overlaps %s", o->name, q->name);
+    for (const Buffer& i : in_place)
+      if (overlap(*o, i) && !(o == outputs.begin() && o->p == i.p))
+        return fail(NVFP4_ERR_INVALID_VALUE, "%s overlaps %s", o->name, i.name);
+  }
+  return NVFP4_OK;
 }
 
 int done(hipError_t e, const char* where) { return e == hipSuccess ? NVFP4_OK : nvfp4::set_hip_error(e, where); }
@@ -195,6 +224,13 @@ NVFP4_API int nvfp4_add_rmsnorm_mx(const void* x, const void* residual, const vo
       !aligned(codes, 16) || !aligned(scales, 16))
     return fail(NVFP4_ERR_MISALIGNED, "x, residual, weight, residual_out, codes and scales must be 16-byte aligned");
   if (!aligned(rstd, 4)) return fail(NVFP4_ERR_MISALIGNED, "rstd must be 4-byte aligned");
+  const int64_t row = 2 * m * k, wide = weight_dtype == NVFP4_F32 ? 4 * k : 2 * k;
+  if ((st = check_outputs({{residual_out, row, "residual_out"},
+                           {rstd, 4 * m, "rstd"},
+                           {codes, format == NVFP4_MXFP4 ? m * k / 2 : m * k, "codes"},
+                           {scales, m * k / 32, "scales"}},
+                          {{weight, wide, "weight"}}, {{x, row, "x"}, {residual, row, "residual"}})))
+    return st;
   if ((st = device_ok())) return st;
   return done(nvfp4::launch_add_rmsnorm_mx(x, residual, weight, weight_dtype == NVFP4_F32, (double)eps, m, k, format,
                                            residual_out, rstd, codes, scales, hs(stream)),
@@ -215,15 +251,18 @@ NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const vo
   if (!dweight) return fail(NVFP4_ERR_INVALID_VALUE, "dweight is required");
   if (m > 0 && (!dh || !s || !weight || !rstd || !dx))
     return fail(NVFP4_ERR_INVALID_VALUE, "dh, s, weight, rstd and dx are required");
-  if (m > 0 && (dx == dh || dx == s))
-    return fail(NVFP4_ERR_INVALID_VALUE, "dx cannot be dh's or s's buffer: dweight reads them beside it");
   if (!aligned(dweight, 16) || (m > 0 && (!aligned(dh, 16) || !aligned(s, 16) || !aligned(weight, 16) ||
                                           !aligned(ds, 16) || !aligned(dx, 16))))
     return fail(NVFP4_ERR_MISALIGNED, "dh, s, weight, ds, dx and dweight must be 16-byte aligned");
   if (m > 0 && !aligned(rstd, 4)) return fail(NVFP4_ERR_MISALIGNED, "rstd must be 4-byte aligned");
-  if ((st = check_workspace(workspace, workspace_bytes, nvfp4_add_rmsnorm_backward_workspace_size(m, k))) ||
-      (st = device_ok()))
+  const int64_t need = (int64_t)nvfp4_add_rmsnorm_backward_workspace_size(m, k);
+  if ((st = check_workspace(workspace, workspace_bytes, (size_t)need))) return st;
+  const int64_t row = 2 * m * k, wide = weight_dtype == NVFP4_F32 ? 4 * k : 2 * k;
+  if (m > 0 && (st = check_outputs({{dx, row, "dx"}, {dweight, 4 * k, "dweight"}, {need > 0 ? workspace : nullptr, need, "workspace"}},
+                                   {{dh, row, "dh"}, {s, row, "s"}, {weight, wide, "weight"}, {rstd, 4 * m, "rstd"}},
+                                   {{ds, row, "ds"}})))
     return st;
+  if ((st = device_ok())) return st;
   return done(nvfp4::launch_rmsnorm_backward(dh, s, weight, weight_dtype == NVFP4_F32, rstd, ds, dx, dweight, m, k,
                                              workspace, hs(stream)),
               "add_rmsnorm_backward launch");

@@ -493,7 +493,8 @@ NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uin
  * weight     device [k], bf16 or fp32 (weight_dtype).
  * eps        finite, >= 0.
  * residual_out  device bf16 [m, k]: s (NULL exactly when residual is NULL);
- *            may be residual's or x's own buffer.
+ *            may be residual's or x's own buffer.  Any other overlap of an
+ *            output with an input or another output is refused.
  * rstd       device fp32 [m] or NULL (the gradient needs it).
  * m, k       m >= 0, m < 2^22; 32 <= k <= 65536, k % 32 == 0.
  * One launch.  A row with an infinity or NaN follows the formulas.
@@ -507,8 +508,10 @@ NVFP4_API int nvfp4_mx_gemm_dx(const void* dy, const uint8_t* w_codes, const uin
  * s, rstd    residual_out (x without a residual) and rstd of the forward.
  * ds         device bf16 [m, k] or NULL: the gradient that reaches s by the
  *            residual branch; may be dx's own buffer.
- * dx         device bf16 [m, k]; not dh's or s's buffer.
- * dweight    device fp32 [k], written whole (zeros when m == 0).
+ * dx         device bf16 [m, k].
+ * dweight    device fp32 [k], written whole (zeros when m == 0).  Any overlap
+ *            of dx, dweight and workspace with an input or one another, but for
+ *            dx in ds's buffer, is refused.
  * workspace  device, >= nvfp4_add_rmsnorm_backward_workspace_size(m, k)
  *            bytes, 16-byte aligned (0 for few rows: NULL allowed, one
  *            launch): fp32 partial sums of dweight, added in a fixed order by

@@ -96,6 +96,36 @@ def test_norm(L):
     assert L.nvfp4_add_rmsnorm_backward_workspace_size(0, 64) == 0
 
 
+def test_norm_refuses_overlaps(L):
+    """Outputs that share memory with what other workgroups read: at any offset, the largest included."""
+    m, k = 6, 96
+    row = 2 * m * k
+    at = {n: (1 << 24) + (1 << 16) * i for i, n in enumerate(["x", "r", "w", "ro", "rs", "c", "s", "dh", "ds", "dx", "dw"])}
+
+    def f(**o):
+        p = {**at, **o}
+        return L.nvfp4_add_rmsnorm_mx(p["x"], p["r"], p["w"], 1, 1e-6, m, k, 1, p["ro"], p["rs"], p["c"], p["s"], None)
+
+    def b(**o):
+        p = {**at, **o}
+        return L.nvfp4_add_rmsnorm_backward(p["dh"], p["s"], p["w"], 1, p["rs"], p["ds"], p["dx"], p["dw"], m, k, None,
+                                            0, None)
+
+    for call, out, inputs in ((f, "ro", ("x", "r")), (b, "dx", ("dh", "s", "ds"))):
+        for name in inputs:
+            for off in (-row + 16, -16, 16, row - 16):
+                assert call(**{out: at[name] + off}) == 1, (out, name, off)
+                assert f"{out.replace('ro', 'residual_out')} overlaps" in L.nvfp4_last_error().decode()
+    assert b(dx=at["dh"]) == 1 and b(dx=at["s"]) == 1 and b(dx=at["w"]) == 1 and b(dx=at["rs"] - 16) == 1
+    assert b(dw=at["w"]) == 1 and b(dw=at["dx"] + 32) == 1 and b(dw=at["dh"] + row - 16) == 1 and b(dw=at["ds"]) == 1
+    assert f(c=at["x"]) == 1 and f(c=at["ro"] + 16) == 1 and f(s=at["c"]) == 1 and f(rs=at["r"] + 4) == 1
+    assert f(ro=at["w"] + 16) == 1 and f(rs=at["ro"] + row - 4) == 1
+    if not torch.cuda.is_available():  # past every check, no device here: whole buffers in place, neighbours
+        for ok in (f(), f(ro=at["x"]), f(ro=at["r"]), f(r=at["x"], ro=at["x"]), f(ro=at["x"] + row), f(r=None, ro=None, rs=None),
+                   b(), b(dx=at["ds"]), b(ds=None), b(dx=at["dh"] - row), b(dx=at["s"] + row), b(dw=at["w"] + 4 * k)):
+            assert ok > 4
+
+
 def _mx(m, k, fmt):
     return nv.MXTensor.empty(m, k, fmt, "cpu")
 
