@@ -686,6 +686,13 @@ class MXTensor:
                         torch.empty((m, k // 32), dtype=_U8, device=device), fmt)
 
 
+def _mx_sizes(q, name):
+    """(m, k) of argument `name`, which must be an MXTensor."""
+    if not isinstance(q, MXTensor):
+        raise ValueError(f"{name} must be an MXTensor, got {type(q).__name__}")
+    return q.sizes(name + ".")
+
+
 def _mx_out(out, m, k, fmt, like):
     """out, checked to be an [m, k] matrix in format fmt beside tensor `like`, or a new one."""
     if out is None:
@@ -722,7 +729,7 @@ def quantize_mx(x: torch.Tensor, fmt: int = MXFP4, out: Optional[MXTensor] = Non
 
 def dequant_mx(q: MXTensor, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of an MX matrix, as float32 or bfloat16."""
-    m, k = q.sizes()
+    m, k = _mx_sizes(q, "q")
     code = _out_code(dtype, "dtype")
     codes = q.codes
     index = codes.get_device()
@@ -746,8 +753,8 @@ def mx_gemm_path(m: int, n: int, k: int, a_fmt: int) -> int:
 def mx_gemm(a: MXTensor, w: MXTensor, out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y[m, n] = a[m, k] @ w[n, k]^T for MXFP4 or MXFP8 a and MXFP4 w."""
-    m, k = a.sizes("a.")
-    n, kw = w.sizes("w.")
+    m, k = _mx_sizes(a, "a")
+    n, kw = _mx_sizes(w, "w")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if kw != k:
@@ -779,7 +786,7 @@ def mx_gemm_dx(dy: torch.Tensor, w: MXTensor, out_dtype: torch.dtype = torch.bfl
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dx = dy @ w for bf16 [m, n] dy and MXFP4 w [n, k]: mx_gemm's gradient
     with respect to its activations, straight through their quantization."""
-    n, k = w.sizes("w.")
+    n, k = _mx_sizes(w, "w")
     if w.fmt != MXFP4:
         raise ValueError("w must be in MXFP4")
     if not isinstance(dy, torch.Tensor) or dy.dim() != 2 or dy.shape[1] != n:

@@ -196,3 +196,12 @@ def test_paths(L):
     for bad in ((0, 8, 64), (4, 0, 64), (4, 8, 0), (4, 8, 48), (-1, 8, 64), (4, 1 << 27, 64)):
         assert nv.mx_gemm_path(*bad, nv.MXFP4) == -1 and nv.mx_gemm_dx_path(*bad) == -1
     assert nv.mx_gemm_path(4, 8, 64, 5) == -1
+
+
+def test_binding_refuses_what_is_no_mx_matrix():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), _mx(4, 64, nv.MXFP4)
+    for bad in (x, None, (w.codes, w.scales), 3):
+        for call, name in ((lambda: nv.dequant_mx(bad), "q"), (lambda: nv.mx_gemm(bad, w), "a"),
+                           (lambda: nv.mx_gemm(w, bad), "w"), (lambda: nv.mx_gemm_dx(x, bad), "w")):
+            with pytest.raises(ValueError, match=f"^{name} must be an MXTensor"):
+                call()
