@@ -33,15 +33,17 @@ __device__ __forceinline__ void wait_lds_all() {
 // from src, or from base + a 32-bit offset per lane.  As inline asm: the
 // compiler holds back transposing LDS reads until all copies it knows of have
 // landed, the ones into other buffers too, and counts them in its own waits.
-// They write no register, and the kernel waits for them itself.
+// They write no register, and the kernel waits for them itself.  The address is
+// an operand in M0, which the compiler's own copies set too; the s_nop is the
+// wait that a write of M0 needs before the copy.
 __device__ __forceinline__ void copy16_unseen(const uint8_t* src, uint32_t to) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(to), "v"(src) : "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "{m0}"(to), "v"(src));
 #endif
 }
 __device__ __forceinline__ void copy16_unseen(const uint8_t* base, uint32_t offset, uint32_t to) {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(to), "v"(offset), "s"(base) : "m0");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "{m0}"(to), "v"(offset), "s"(base));
 #endif
 }
 __device__ __forceinline__ uint32_t lds_address(const uint8_t* p) {
