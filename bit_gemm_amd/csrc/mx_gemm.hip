@@ -470,9 +470,8 @@ __global__ __launch_bounds__(256, T::NT * T::MT > 8 ? 1 : 2) void k_mx_tile(
       } else {  // the end of the rows, ones behind it: all loads under way at once (one after another 0.3-2 us more)
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          uint32_t v = 0;
-const int b = at + 4 * d, left = nb - b;
-          v = 0x7F7F7F7Fu;
+          const int b = at + 4 * d, left = nb - b;
+          uint32_t v = 0x7F7F7F7Fu;
           if (left >= 4) __builtin_memcpy(&v, p + b, 4);
           else if (left > 0) {
             v = p[b] | 0x7F7F7F00u;
