@@ -33,7 +33,7 @@ constexpr int64_t kMaxElems = ((int64_t)1 << 37) - (1 << 20);
 constexpr int64_t kMaxTokens = (int64_t)1 << 22;  // rows of a product's activations: 64 rows per grid row
 constexpr int64_t kMaxRows = (int64_t)1 << 27;    // weight rows: 512 threads per 16 of them
 constexpr int64_t kMaxK = (int64_t)1 << 30;
-constexpr int64_t kMaxNormK = 65536;  // a row lives in the registers of one workgroup
+constexpr int64_t kMaxNormK = 65536;  // 8 pieces of 8 elements for each of 1024 threads, one workgroup per row
 
 int check_mk(int64_t m, int64_t k, const char* rows) {
   if (m < 0 || k < 0)

@@ -18,14 +18,14 @@
 //
 // What bounds it: at 256 x 256 a step is 64 products of 32 clocks per SIMD
 // (2048) beside 192 KiB through LDS (about 1000) and the conversions; measured
-// 1.6 us per step with every CU at work, 3000 clocks at the 1.87 GHz that the
-// card then runs at, 1.34 PFLOP/s at 4096 x 14336 x 4096 (m, n, k; 357 us), where
-// a large bf16 library product of plain matrices reaches 1.38.  At 128 x 128 the
-// LDS needs longer than the products: 1.0 PFLOP/s, for where there are too few
-// outputs for the large tile.  A 256 x 224 tile (rounds that fill for k = 7 2^i)
-// was no faster: 118 against 115 us at 1024 x 4096 x 14336.  Operands are read a
-// step of 16 ahead (two ahead: no faster), and the waves meet before the last of
-// a buffer's four steps, as in mx_gemm.hip.
+// 1.6 to 1.7 us per step with every CU at work (3570 clocks under the counters,
+// which slow it by 4 %), 1.26 to 1.34 PFLOP/s at 4096 x 14336 x 4096 (m, n, k; 358
+// to 382 us, card by card), where a large bf16 library product of plain matrices
+// reaches 1.38.  At 128 x 128 the LDS needs longer than the products: 1.0 PFLOP/s,
+// for where there are too few outputs for the large tile.  A 256 x 224 tile (rounds
+// that fill for k = 7 2^i) was 2.5 % slower at 1024 x 4096 x 14336.  Operands are
+// read a step of 16 ahead (two ahead: no faster), and the waves meet before the
+// last of a buffer's four steps, as in mx_gemm.hip.
 #include "launchers.h"
 #include "mx_tile.h"
 
@@ -314,9 +314,9 @@ bool dma_rows(int64_t n) { return n % 8 == 0 && n <= ((int64_t)1 << 22); }
 // 128 x 128 tiles, 1.1 with two workgroups per CU, 1.75 with 256 x 256; a launch
 // about 2.5 (8 with the large tile, whose first loads and stores nothing else
 // hides), a split 3 for its second launch and the planes' traffic.  1024 x 4096 x
-// 14336 (m, n, k) took 115 with the large tile, 143 with the small one, 2048 x
-// 4096 x 4096 114 and 76, 512 x 4096 x 4096 with small tiles 43 whole, 33 split
-// in two or four, 44 in eight.
+// 14336 (m, n, k) took 103 to 111 with the large tile, 134 with the small one, 2048
+// x 4096 x 4096 92 and 72, 512 x 4096 x 4096 with small tiles 41 whole, 31 split in
+// two, 32 in four.
 MxPlan plan_mx_dx(int64_t m, int64_t n, int64_t k) {
   MxPlan best{128, 1, 0, 0};
   const int64_t steps = (n + 63) / 64;

@@ -90,8 +90,11 @@ __device__ __forceinline__ void store_rows(const f32x4_t* red, void* y, int m0, 
 // consecutive bytes of 16 rows; C steps' scales are one load per row, and a
 // lane shifts its block's byte to the bottom.  Three or four chunks ahead, or 16
 // waves: no faster; 64 consecutive bytes per lane (four loads of 16 separate
-// pieces per row): 13.7 / 17.7 us against 12.3 / 15.1 at 16 x 4096 x 14336 with
-// MXFP4 / MXFP8 a.  For every K that k_mx_rows_dma does not take.
+// pieces per row): 13.7 us against 12.3 at 16 x 4096 x 14336 with MXFP4 a.  For
+// every K that k_mx_rows_dma does not take: 1 x 4096 x 11008 8.4 / 10.4 us (MXFP4
+// / MXFP8 a), 16 x 4096 x 11008 9.9 / 12.9, 16 x 5120 x 5088 10.6 (7.4 with
+// k_mx_rows_dma at K = 5120), and 16 x 14336 x 4128, whose ninth chunk of 32 k takes
+// every wave a turn, 14.9 / 20.2 (9.6 / 10.7 at K = 4096).
 constexpr int kRowWaves = 8;
 constexpr int kRowGroups = 256;  // workgroups: one per CU
 
@@ -202,18 +205,21 @@ __global__ __launch_bounds__(64 * kRowWaves, 2) void k_mx_rows(const uint8_t* __
 // own LDS.  A load into registers reads 64 bytes of each of 16 rows, because a
 // lane can only load what its row of the product needs; the copies read whole
 // lines (rows of 256 bytes, or 512 of MXFP8 a), which brings the weights in
-// sooner and above all a, which every CU reads from L2.  Measured beside
-// k_mx_rows (us, weights from HBM, MXFP4 a): 1 x 4096 x 4096 4.3 (4.4), 1 x
-// 14336 x 4096 9.5 (10.4), 1 x 28672 x 4096 14.5 (16.0; 4.3 TB/s), 16 x 4096 x
-// 14336 10.1 (12.3), 16 x 14336 x 4096 9.8 (11.7); MXFP8 a, multiplied twice:
-// 4.8, 10.2, 15.4, 12.9, 10.6.  Bound by the weights' way from HBM (31 MB more
+// sooner and above all a, which every CU reads from L2.  K off the multiples of
+// 512 stays with k_mx_rows: a short chunk's scales are not whole 16-byte pieces,
+// nor are any row's behind the first.  Measured beside k_mx_rows (us, weights from
+// HBM, MXFP4 / MXFP8 a): 1 x 4096 x 4096 4.3 / 4.7 (4.4 / 4.9), 1 x 14336 x 4096
+// 9.3 / 10.1 (10.3 / 11.8), 1 x 28672 x 4096 14.4 / 15.1 (16.0 / 17.7; 4.3 TB/s),
+// 16 x 4096 x 14336 10.1 / 12.9 (12.3 / 15.6), 16 x 14336 x 4096 9.6 / 10.7 (11.7
+// / 14.1), 16 x 4096 x 11264 8.0 / 10.3 (9.5 / 12.3).  Bound by the weights' way from HBM (31 MB more
 // cost 5.2 us, 6.0 TB/s) behind a launch and the first copies' latency.
 //
 // Step j's block q is the chunk's block 4 q + j in both operands: a lane's four
 // scales are one word, byte j of it picked by the instruction.  Piece p of row
 // r lies at p ^ r of its LDS row (256 bytes, or 512), so that 16 rows' reads of
-// one piece meet all banks.  KEEP (one chunk per wave: K = 4096): a stays in
-// registers and the ring is the weights' alone.  RA: rows of a that are staged.
+// one piece meet all banks.  KEEP (exactly one chunk for each of 8 waves, which
+// with whole chunks is K = 4096): a stays in registers and the ring is the
+// weights' alone.  RA: rows of a that are staged.
 template <int FMT_, bool KEEP_, int RA_, int NW_, int R_>
 struct Ring {
   static constexpr int FMT = FMT_, RA = RA_, NW = NW_, R = R_;
@@ -369,13 +375,14 @@ __global__ __launch_bounds__(64 * T::NW, T::NW / 4) void k_mx_rows_dma(
 // stage's 8 bytes per row cost as much time as the stage's codes (a 256 x 256
 // tile's 512 rows: 0.5 us against 0.65 us for 64 KiB of codes in whole lines).
 //
-// What bounds it, 256 x 256 with MXFP4 (4096 x 4096 x 14336, every CU at work):
-// 3450 clocks per stage of 256 k, 2430 of them the products as fast as they
-// issue, 2810 with the copies left out, at the 1.85 GHz that the card then runs
-// at; a round has 5.7 us of first loads and stores beside its 30 us of stages at
-// k = 4096.  4096 x 14336 x 4096: 142 us, 3.39 PFLOP/s; MXFP8, every product
-// twice, 312 us (327 with fp32 output; 206 with each product once, which loses
-// the small ones).  4096 x 4096 x 14336 MXFP4: 114 us, 4.2 PFLOP/s.
+// What bounds it, 256 x 256 with MXFP4 (4096 x 4096 x 14336, every CU at work): 2.0
+// us per stage of 256 k, 4340 clocks under the counters, of which the matrix cores
+// work 2048; one wave per SIMD (460 registers), so that whatever a wave waits for,
+// a quarter of its time, is idle matrix time.  A fifth less without the copies (a
+// variant of the source, for timing).  A round has about 6 us of first loads and
+// stores beside its 32 us of stages at k = 4096.  4096 x 14336 x 4096: 144 us, 3.3
+// PFLOP/s; MXFP8, every product twice, 318 us (336 with fp32 output), the matrix
+// cores at work 0.61 of the time.  4096 x 4096 x 14336 MXFP4: 114 us, 4.2 PFLOP/s.
 template <int FMT, int NT_, int MT_, int WN_, int S_, int B_, int G_>
 struct Tile {
   static constexpr int NT = NT_, MT = MT_, WN = WN_, WM = 4 / WN_, S = S_, B = B_, G = G_;
@@ -709,7 +716,8 @@ hipError_t launch_rows(const uint8_t* a_codes, const uint8_t* a_scales, const ui
     };
     // a stays in registers where its way there is paid for by several tiles (one tile: 4.3 against 4.5 us at 1 x
     // 4096 x 4096; four: 9.8 against 11.0 at 16 x 14336 x 4096)
-    if (k == 4096 && tiles > kRowGroups) return ring(Ring<FMT, true, 16, 8, 4>{});
+    const int64_t chunks = k / 512;
+    if (chunks == kRowWaves && tiles > kRowGroups) return ring(Ring<FMT, true, 16, 8, 4>{});
     if (m <= 4) return ring(Ring<FMT, false, 4, 8, FMT == kMxFp4 ? 3 : 2>{});
     return ring(Ring<FMT, false, 16, FMT == kMxFp4 ? 8 : 4, FMT == kMxFp4 ? 2 : 3>{});
   }
@@ -743,10 +751,14 @@ hipError_t launch_plane_sum(const float* planes, void* y, int64_t mn, int splits
 // large ones, which read each operand less often: 1024 x 4096 x 4096 (m, n, k)
 // with MXFP4 took 21.5 / 17.6 / 32.0 with the three tiles, 512 x 4096 x 4096
 // 11.7 / 16.1 / above 20, 2048 x 4096 x 4096 40.7 / 25.9 / 33.0, 4096 x 14336
-// x 4096 281 / 175 / 158.  The 256 x 224 tile is for n = 7 2^i, whose rounds it
-// fills: 4096 x 14336 x 4096 in four rounds instead of three and a half of the
-// square tile took 142 / 316 against 144 / 350, but 2048 x 8192 x 4096 64 / 150
-// against 41 / 97.  64 x 4096 x 14336 with 64 x 64 tiles 17.6 split in
+// x 4096 281 / 175 / 158.  The 256 x 224 tile, whose round is shorter, is chosen
+// wherever it needs no more rounds than the square one, n = 7 2^i and others.  It
+// took, against the square tile (MXFP4 / MXFP8 a): 4096 x 14336 x 4096 142 / 317
+// against 144 / 350, 2048 x 6144 x 4096 33.4 / 77 against 33.5 / 88, 3500 x 3700 x
+// 544 19.4 / 25.8 against 19.0 / 26.6, 2300 x 5000 x 1024 16.0 / 27.6 against 16.4 /
+// 30.4, 1024 x 14336 x 4096 37.4 / 83.7 against 37.5 / 91.0; it lost at 2045 x 7159 x
+// 544, 31.1 / 37.3 against 26.5 / 34.1 (more tiles with stores of odd rows), and
+// with more rounds: 2048 x 8192 x 4096 64 / 150 against 41 / 97.  64 x 4096 x 14336 with 64 x 64 tiles 16.1 split in
 // four, above 20 in two or not at all.
 MxPlan plan_mx_gemm(int64_t m, int64_t n, int64_t k, int a_fmt) {
   MxPlan best{0, 1, 0, 0};

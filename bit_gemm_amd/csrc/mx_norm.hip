@@ -19,9 +19,11 @@
 //   dx_i = rstd (g_i - xhat_i mean(g xhat)) + ds_i
 //   dweight_i = sum over rows of dh_i xhat_i
 // in fp32; dx is the gradient of x and of the residual alike.  4096 x 4096 with
-// ds: 31.3 us (4.3 TB/s, 27.8 us in the first kernel, the rest the sum of
-// dweight's 256 planes), 4096 x 14336 95 us (4.9 TB/s), 333 x 11008 7.8 us, 16 x
-// 4096 2.8 us.
+// ds: 31.6 us (4.2 TB/s, 27.7 us in the first kernel, the rest the sum of
+// dweight's 256 planes), 4096 x 14336 93 us (5.0 TB/s), 1024 x 16384 36 us, 333 x
+// 11008 7.8 us, 16 x 4096 2.9 us.  Rows of more than 16384 elements do not fit the
+// registers of one workgroup: 1024 x 32768 107 us (2.5 TB/s), 1024 x 65536 476 us
+// (1.1 TB/s), 512 x 65536 151 us.
 #include "launchers.h"
 #include "mx_device.h"
 
@@ -156,8 +158,10 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void k_add_rmsnorm_mx(
 // + R gridDim.x, ...; every thread keeps its columns' share of dweight in
 // registers, the groups' shares meet in LDS at the end, and plane blockIdx.x of
 // `planes` receives the workgroup's.  Up to P = 2 pieces per thread the next
-// row is loaded before the current one's sum and the weight stays in registers;
-// wider rows have enough loads of their own under way.
+// row is loaded before the current one's sum and the weight stays in registers.
+// Wider rows load one row at a time, and yet their pieces and sums pass the 128
+// registers that a thread of 1024 has: with P = 4 120 bytes per thread go through
+// scratch memory, with P = 8 770, which is what bounds those widths.
 template <int T, int P, int R, bool WF32>
 __global__ __launch_bounds__(T* R) void k_rmsnorm_backward(const u32x4_t* __restrict__ dh,
                                                            const u32x4_t* __restrict__ s,
@@ -295,7 +299,8 @@ __global__ __launch_bounds__(T* R) void k_rmsnorm_backward(const u32x4_t* __rest
 // Few rows (up to kFewRows): one launch, the first m workgroups a row each, the
 // others 64 columns of dweight each, which they sum from dh and s themselves:
 // 4 bytes per element read a second time, from the caches, against 8 per
-// element of a plane per one or two rows, and no second launch.
+// element of a plane per one or two rows, and no second launch.  (P = 8, rows of
+// more than 32768: up to 400 bytes per thread through scratch memory.)
 template <int T, int P, bool WF32>
 __global__ __launch_bounds__(T) void k_rmsnorm_backward_few(const u32x4_t* __restrict__ dh,
                                                             const u32x4_t* __restrict__ s,

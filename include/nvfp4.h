@@ -473,7 +473,9 @@ NVFP4_API int nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, int
  * nvfp4_mx_gemm_dx - dx[m, k] = dy[m, n] . w[n, k] for bf16 dy and MXFP4
  * weights: nvfp4_mx_gemm's gradient with respect to the activations (straight
  * through their quantization), as nvfp4_w4a16_gemm_dx is for NVFP4 weights.
- * Sizes as nvfp4_mx_gemm; n == 0 writes zeros; pointers 16-byte aligned.
+ * Sizes as nvfp4_mx_gemm; n == 0 writes zeros; pointers 16-byte aligned.  A
+ * weight past bf16's range (magnitudes from 4 up at a scale byte of 253, from 2
+ * up at 254; nvfp4_mx_quantize writes neither byte) counts as infinite.
  */
 NVFP4_API size_t nvfp4_mx_gemm_dx_workspace_size(int64_t m, int64_t n, int64_t k);
 /* The tile nvfp4_mx_gemm_dx takes (128 or 256), as nvfp4_mx_gemm_path. */

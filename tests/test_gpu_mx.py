@@ -629,3 +629,24 @@ def test_norm_backward_many_rows(m, k):
         terms = dh.double() * xh
         bound = (-(-m // 256) + 16 + 14 + 2) * U32 * terms.abs().sum(0)
         assert bool(((dw.double() - terms.sum(0)).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("scale", [0, 1, 126, 252, 253, 254])
+def test_gemm_dx_of_one_weight_row(scale):
+    # dy = 1 and n = 1: the weights as bf16, infinite where they pass its range
+    w = nv.MXTensor(torch.arange(256, device="cuda").to(torch.uint8).view(1, 256),
+                    torch.full((1, 16), scale, dtype=torch.uint8, device="cuda"), nv.MXFP4)
+    want = nv.dequant_mx(w, torch.bfloat16)
+    assert bool(want.isinf().any()) == (scale >= 253)
+    for dt in (torch.bfloat16, torch.float32):
+        assert torch.equal(nv.mx_gemm_dx(torch.ones((1, 1), device="cuda").bfloat16(), w, out_dtype=dt), want.to(dt))
+
+
+@FMTS
+@DTYPES
+def test_quantize_special_rows_among_others(fmt, dtype):
+    # in the middle of a wave's run, so that neighbouring blocks' lanes hold ordinary values
+    x = torch.cat([rows(21, 64, 170, dtype), special_rows(dtype), rows(30, 64, 171, dtype)])
+    q = nv.quantize_mx(x.cuda(), fmt)
+    c, s = mx.quantize_mx(x.double().numpy(), fmt)
+    assert np.array_equal(q.scales.cpu().numpy(), s) and np.array_equal(q.codes.cpu().numpy(), mx.pack(c, fmt))
