@@ -650,3 +650,18 @@ def test_quantize_special_rows_among_others(fmt, dtype):
     q = nv.quantize_mx(x.cuda(), fmt)
     c, s = mx.quantize_mx(x.double().numpy(), fmt)
     assert np.array_equal(q.scales.cpu().numpy(), s) and np.array_equal(q.codes.cpu().numpy(), mx.pack(c, fmt))
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 83, 992), (13, 131, 4640), (15, 4200, 4096), (16, 97, 14336), (67, 131, 1056),
+                                   (1573, 1923, 1568), (1860, 4474, 1056), (2615, 5320, 1056)])
+def test_gemm_fp8_nan_codes_reach_their_row_only(m, n, k):
+    # both NaN codes, at the first and the last place of a row, in every kernel (each lies whole in one of the two
+    # parts that are multiplied)
+    gen = torch.Generator(device="cuda").manual_seed(m)
+    a, w = _exact_mx(m, k, nv.MXFP8, gen), _exact_mx(n, k, nv.MXFP4, gen)
+    a.codes[0, k - 1], a.codes[m - 2, 0] = 0x7F, 0xFF
+    bad = torch.zeros(m, dtype=torch.bool, device="cuda")
+    bad[0] = bad[m - 2] = True
+    for dt in (torch.bfloat16, torch.float32):
+        y = nv.mx_gemm(a, w, out_dtype=dt).isnan()
+        assert bool(y[bad].all()) and not bool(y[~bad].any())
