@@ -14,6 +14,8 @@ Entry points mirror the C ABI in ``include/nvfp4.h``:
 * ``quantize_mx(x, fmt=MXFP4)`` -> :class:`MXTensor`, ``dequant_mx(q)``
 * ``mx_gemm(a, w)``, ``mx_gemm_dx(dy, w)``
 * ``add_rmsnorm_mx(x, weight, residual=None)``, ``add_rmsnorm_backward(...)``
+* ``kv_append(cache, k, v, slots, ...)``, ``kv_read(cache, slots)`` on a
+  :class:`KVCache`, ``kv_attention(q, cache, page_table, kv_lens, ...)``
 * ``selftest_cvt()``
 """
 
@@ -88,6 +90,15 @@ SIGNATURES = {
     "nvfp4_add_rmsnorm_backward_workspace_size": (_c_size, [_c_i64, _c_i64]),
     "nvfp4_add_rmsnorm_backward": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p,
                                             _c_size, _c_p]),
+    "nvfp4_kv_page_bytes": (_c_size, [_c_i64, _c_i64, _c_i64]),
+    "nvfp4_kv_append": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64,
+                                 _c_i64, _c_int, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "nvfp4_kv_read": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_int,
+                               _c_p]),
+    "nvfp4_kv_attention_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "nvfp4_kv_attention": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p,
+                                    _c_p, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_int, _c_i64, _c_p, _c_p, _c_p,
+                                    _c_size, _c_p]),
     "nvfp4_selftest_cvt": (_c_int, [_c_p, _c_p]),
     "nvfp4_stream_read": (_c_int, [_c_p, _c_size, _c_int, _c_int, _c_int, _c_p, _c_p]),
     "nvfp4_w4a16_gemm_noalloc": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p]),
@@ -882,6 +893,224 @@ def add_rmsnorm_backward(dh: torch.Tensor, s: torch.Tensor, weight: torch.Tensor
     _run(index, L.nvfp4_add_rmsnorm_backward, dh.data_ptr(), s.data_ptr(), weight.data_ptr(), wcode, rstd.data_ptr(),
          _ptr(ds), dx.data_ptr(), dweight.data_ptr(), m, k, ws, ws_bytes)
     return dx, dweight
+
+
+_I32 = torch.int32
+
+
+@dataclass
+class KVCache:
+    """Paged key/value cache of one attention layer in NVFP4 (see
+    include/nvfp4.h): one E4M3 scale per 16 elements of a head, one float32
+    scale per head for keys and one for values (a calibrated largest magnitude
+    over 2688)."""
+
+    data: torch.Tensor  # uint8 [pages, page bytes]
+    k_scale: torch.Tensor  # float32 [heads]
+    v_scale: torch.Tensor  # float32 [heads]
+    head_dim: int  # 64, 128 or 256
+    page_size: int  # tokens of a page
+
+    @property
+    def heads(self) -> int:
+        return self.k_scale.numel()
+
+    @property
+    def pages(self) -> int:
+        return self.data.shape[0]
+
+    @staticmethod
+    def empty(pages: int, page_size: int, heads: int, head_dim: int, device="cuda", k_scale=None,
+              v_scale=None) -> "KVCache":
+        """An uninitialised cache.  k_scale, v_scale: a number, a float32 [heads] tensor, or None for 1 (magnitudes
+        from 2^-8 to 2688; below, blocks round to zero)."""
+        n = kv_page_bytes(heads, head_dim, page_size)
+        if n == 0:
+            raise ValueError(f"no cache of {heads} heads of {head_dim} in pages of {page_size} tokens")
+        if pages < 0:
+            raise ValueError(f"pages={pages}")
+        scales = []
+        for s in (k_scale, v_scale):
+            if not isinstance(s, torch.Tensor):
+                s = torch.full((heads,), 1.0 if s is None else float(s), dtype=_F32, device=device)
+            scales.append(s)
+        return KVCache(torch.empty((pages, n), dtype=_U8, device=device), *scales, head_dim, page_size)
+
+    def check(self):
+        """(pages, heads, GPU index); raises ValueError unless the fields are
+        those of one cache on a GPU."""
+        data, ks, vs = self.data, self.k_scale, self.v_scale
+        if (isinstance(data, torch.Tensor) and data.dim() == 2 and isinstance(ks, torch.Tensor) and ks.dim() == 1):
+            (pages, bytes_), heads, index = data.shape, ks.shape[0], data.get_device()
+            n = lib().nvfp4_kv_page_bytes(heads, self.head_dim, self.page_size)
+            if (n > 0 and n == bytes_ and _fits(data, _U8, (pages, n), index) and _fits(ks, _F32, (heads,), index)
+                    and _fits(vs, _F32, (heads,), index)):
+                return pages, heads, index
+        if not isinstance(data, torch.Tensor) or data.dim() != 2:
+            raise ValueError("cache.data must be a 2-D uint8 tensor [pages, page bytes]")
+        if not isinstance(ks, torch.Tensor) or ks.dim() != 1:
+            raise ValueError("cache.k_scale must be a float32 tensor [heads]")
+        heads = ks.shape[0]
+        n = kv_page_bytes(heads, self.head_dim, self.page_size)
+        if n == 0:
+            raise ValueError(f"no cache of {heads} heads of {self.head_dim} in pages of {self.page_size} tokens")
+        _need_all(data.device, [(data, "cache.data", _U8, (data.shape[0], n)), (ks, "cache.k_scale", _F32, (heads,)),
+                                (vs, "cache.v_scale", _F32, (heads,))])
+        raise ValueError("cache is not on a GPU")
+
+
+def kv_page_bytes(heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of a cache page; 0 for sizes that are not supported."""
+    return int(lib().nvfp4_kv_page_bytes(heads, head_dim, page_size))
+
+
+def _kv_cache(cache):
+    if not isinstance(cache, KVCache):
+        raise ValueError(f"cache must be a KVCache, got {type(cache).__name__}")
+    return cache.check()
+
+
+def _token_rows(t, name, head_dim, index, heads=None, tokens=None):
+    """(tokens, heads, stride) of a bf16 [tokens, heads, head_dim] GPU tensor whose heads lie beside one another."""
+    if (not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != head_dim
+            or (heads is not None and t.shape[1] != heads) or (tokens is not None and t.shape[0] != tokens)):
+        want = f"[{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, {head_dim}]"
+        raise ValueError(f"{name} must be a bfloat16 tensor {want}, got {tuple(getattr(t, 'shape', ()))}")
+    n, h, _ = t.shape
+    if t.dtype is not _BF16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    stride, of_head, of_element = t.stride()
+    if of_element != 1 or (h > 1 and of_head != head_dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on GPU {index}")
+    return n, h, stride if n > 1 else h * head_dim
+
+
+def _indices(t, name, shape, index):
+    if not _fits(t, _I32, shape, index):
+        _need(t, name, _I32, shape, torch.device("cuda", index))
+
+
+def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, q: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+              q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Write bf16 [tokens, heads, head_dim] keys and values into the cache's
+    slots (int32 [tokens], page * page_size + place in the page; a token whose
+    slot is negative or past the cache is left out).
+
+    With rope (float32 [max_positions, rope_dim]: cosines, then sines) keys
+    and q (bf16 [tokens, q_heads, head_dim]) are first rotated by their
+    positions (int32 [tokens]), in pairs (i, i + rope_dim / 2) or, if
+    interleaved, (2 i, 2 i + 1).  Returns the rotated queries (q_out, which
+    may be q; None without q).  The heads of a token must be contiguous;
+    tokens may be further apart, as columns of one projection's output are."""
+    pages, heads, index = _kv_cache(cache)
+    d = cache.head_dim
+    n, _, k_stride = _token_rows(k, "k", d, index, heads)
+    _, _, v_stride = _token_rows(v, "v", d, index, heads, n)
+    _indices(slots, "slots", (n,), index)
+    rope_dim = max_positions = 0
+    if (rope is None) != (positions is None):
+        raise ValueError("positions and rope go together")
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
+            raise ValueError("rope must be a float32 tensor [max_positions, rope_dim]")
+        max_positions, rope_dim = rope.shape
+        if not _fits(rope, _F32, rope.shape, index):
+            _need(rope, "rope", _F32, None, torch.device("cuda", index))
+        _indices(positions, "positions", (n,), index)
+    q_ptr = out_ptr = None
+    q_heads = q_stride = out_stride = 0
+    if q is not None:
+        _, q_heads, q_stride = _token_rows(q, "q", d, index, None, n)
+        if q_out is None:
+            q_out = q.new_empty(q.shape)
+        _, _, out_stride = _token_rows(q_out, "q_out", d, index, q_heads, n)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+        if q_heads == 0:  # nothing to rotate
+            q_ptr = out_ptr = None
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _run(index, lib().nvfp4_kv_append, k.data_ptr(), k_stride, v.data_ptr(), v_stride, q_ptr, q_stride, out_ptr,
+         out_stride, q_heads, _ptr(positions), _ptr(rope), max_positions, rope_dim, 1 if interleaved else 0,
+         slots.data_ptr(), n, cache.data.data_ptr(), pages, cache.page_size, heads, d, cache.k_scale.data_ptr(),
+         cache.v_scale.data_ptr())
+    return q_out
+
+
+def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
+    """(keys, values) of the cache's slots (int32 [tokens]), [tokens, heads,
+    head_dim] in bfloat16 or float32; zeros for slots that are not in it."""
+    pages, heads, index = _kv_cache(cache)
+    code = _out_code(dtype, "dtype")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be an int32 tensor [tokens]")
+    n = slots.shape[0]
+    _indices(slots, "slots", (n,), index)
+    k = cache.data.new_empty((n, heads, cache.head_dim), dtype=dtype)
+    v = cache.data.new_empty((n, heads, cache.head_dim), dtype=dtype)
+    _run(index, lib().nvfp4_kv_read, cache.data.data_ptr(), pages, cache.page_size, heads, cache.head_dim,
+         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), code)
+    return k, v
+
+
+def kv_attention_workspace_size(sequences: int, tokens: int, q_heads: int, heads: int, head_dim: int, page_size: int,
+                                table_pages: int, one_each: bool) -> int:
+    return int(lib().nvfp4_kv_attention_workspace_size(sequences, tokens, q_heads, heads, head_dim, page_size,
+                                                       table_pages, 1 if one_each else 0))
+
+
+def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                 q_starts: Optional[torch.Tensor] = None, scale: Optional[float] = None, causal: bool = True,
+                 window: int = 0, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Attention of new tokens over their sequences' contexts in the cache.
+
+    q: bf16 [tokens, q_heads, head_dim], q_heads a multiple of the cache's
+    heads; page_table: int32 [sequences, table_pages]; kv_lens: int32
+    [sequences], the contexts' lengths with the new tokens, which are in the
+    cache already; q_starts: int32 [sequences + 1], the rows of q of each
+    sequence, or None for one row each; scale: 1 / sqrt(head_dim) by default;
+    causal: a new token sees the context up to itself, and with window > 0
+    only its last `window` tokens.  Returns out, bf16 like q, or with
+    return_lse (or lse) also the float32 [tokens, q_heads] logarithms of the
+    softmax's sums.  Rows that see nothing are 0 and -inf; rows behind the
+    last sequence are left as they were in out and lse."""
+    pages, heads, index = _kv_cache(cache)
+    d = cache.head_dim
+    n, q_heads, q_stride = _token_rows(q, "q", d, index)
+    if q_heads == 0 or q_heads % heads != 0:
+        raise ValueError(f"q has {q_heads} heads, not a multiple of the cache's {heads}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor [sequences, table_pages]")
+    b, table_pages = page_table.shape
+    _indices(page_table, "page_table", (b, table_pages), index)
+    _indices(kv_lens, "kv_lens", (b,), index)
+    if q_starts is not None:
+        _indices(q_starts, "q_starts", (b + 1,), index)
+    elif b != n:
+        raise ValueError(f"without q_starts each sequence has one token: {n} tokens, {b} sequences")
+    shape = (n, q_heads, d)
+    if out is None:
+        out = q.new_empty(shape)
+    elif not _fits(out, _BF16, shape, index):
+        _need(out, "out", _BF16, shape, q.device)
+    if lse is None:
+        if return_lse:
+            lse = q.new_empty((n, q_heads), dtype=_F32)
+    elif not _fits(lse, _F32, (n, q_heads), index):
+        _need(lse, "lse", _F32, (n, q_heads), q.device)
+    L = lib()
+    one_each = 1 if q_starts is None else 0
+    ws, ws_bytes, keep = _mx_workspace(
+        workspace, L.nvfp4_kv_attention_workspace_size(b, n, q_heads, heads, d, cache.page_size, table_pages, one_each),
+        cache.data)
+    _run(index, L.nvfp4_kv_attention, q.data_ptr(), q_stride, cache.data.data_ptr(), pages, cache.page_size, heads, d,
+         cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), page_table.data_ptr(), table_pages, kv_lens.data_ptr(),
+         _ptr(q_starts), b, n, q_heads, d ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+         out.data_ptr(), _ptr(lse), ws, ws_bytes)
+    return out if lse is None else (out, lse)
 
 
 def selftest_cvt(device=None) -> list:

@@ -202,6 +202,58 @@ hipError_t launch_rmsnorm_backward(const void* dh, const void* s, const void* we
                                    const void* ds, void* dx, float* dweight, int64_t m, int64_t k, void* workspace,
                                    hipStream_t stream);
 
+// The NVFP4 key/value cache (layout: kv_device.h): `heads` heads of head_dim
+// (64, 128 or 256), pages of 1 << page_shift tokens, slot_limit = pages <<
+// page_shift.  Strides are in elements, from token to token.
+struct KvAppend {
+  const uint16_t *k, *v, *q;  // q NULL: no queries
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;
+  const int* slots;
+  const int* positions;  // with rot > 0
+  const float* rope;     // [max_positions, rot]
+  uint8_t* cache;
+  const float *k_scale, *v_scale;  // [heads]
+  int tokens, q_heads, heads, rot, max_positions, interleaved, page_shift, slot_limit;
+  uint32_t kv_groups;  // set by the launcher
+};
+int64_t kv_append_workgroups(int64_t tokens, int64_t q_heads, int64_t heads, int head_dim);
+hipError_t launch_kv_append(KvAppend a, int head_dim, hipStream_t stream);
+
+struct KvRead {
+  const uint8_t* cache;
+  const float *k_scale, *v_scale;
+  const int* slots;
+  void *k, *v;  // [tokens, heads, head_dim]
+  int tokens, heads, page_shift, slot_limit;
+};
+int64_t kv_read_workgroups(int64_t tokens, int64_t heads, int head_dim);
+hipError_t launch_kv_read(const KvRead& a, int head_dim, int out_f32, hipStream_t stream);
+
+struct KvAttend {
+  const uint16_t* q;
+  int64_t q_stride;
+  const uint8_t* cache;
+  const float *k_scale, *v_scale;
+  const int *table, *lens, *starts;  // starts NULL: one token per sequence
+  uint16_t* out;
+  float* lse;  // or NULL
+  int table_pages, sequences, tokens, heads, group, pages, page_shift, causal, window;
+  float scale;
+};
+// How a call is laid out: row blocks of 16 * tiles rows (a row: a token and a
+// query head), at most `blocks` of them for each head, and up to `parts` more
+// work items for each head from splitting long contexts (0: none is split).
+struct KvPlan {
+  int tiles, parts;
+  int64_t blocks;
+  size_t ws_bytes;
+};
+KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
+                         int64_t capacity, bool one_each);
+hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& plan, void* workspace,
+                               hipStream_t stream);
+
 // Thread-local error text and status codes of the C ABI (api.cpp), for
 // entry points defined in other sources.
 void clear_error();

@@ -528,6 +528,112 @@ NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const vo
                                          int64_t k, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The NVFP4 key/value cache: keys and values of one attention layer in pages,
+ * in the weights' format with one block of 16 along head_dim,
+ *   k_hat = val(code) * sigma * k_scale[head]
+ * (sigma the block's E4M3 scale, k_scale and v_scale device fp32 [heads], the
+ * caller's: a calibrated largest magnitude / 2688; positive and finite), 0.5625
+ * bytes per element.  What [Recap] section 1 does for the weights that decode
+ * reads, done for the context that it reads beside them.
+ *
+ * cache      device, 16-byte aligned: `pages` pages of nvfp4_kv_page_bytes
+ *            bytes, each page_size tokens of all heads.  The order of a page's
+ *            bytes is that of the matrix instructions' operands, fixed for a
+ *            head_dim (csrc/kv_device.h) and independent of page_size but for
+ *            the number of 32-token units in a page; pages can be copied
+ *            whole.  Pages need no initialisation.
+ * page_size  a power of two, 32 .. 65536; pages * page_size < 2^31.
+ * heads      key/value heads, 1 .. 65536; head_dim 64, 128 or 256.
+ * slots      device int32: page * page_size + place in the page of each token.
+ *            pages * page_size is the number of slots.
+ *
+ * nvfp4_kv_page_bytes - bytes of a page; 0 for sizes that are not supported.
+ *
+ * nvfp4_kv_append - rotates queries and keys by their positions and writes
+ * keys and values into their slots; one launch.  Per element pair (a, b) with
+ * the position's cosine c and sine s, in fp32 with one rounding per operation:
+ *   a' = a c - b s,  b' = b c + a s
+ * for the pairs (i, i + rope_dim / 2), or (2 i, 2 i + 1) if interleaved, of a
+ * head's first rope_dim elements.  Keys are quantized from the fp32 a', b' and
+ * values from their own, per block as nvfp4_quantize_act with s_t = the head's
+ * scale; queries are rounded to bf16.
+ * k, v       device bf16 [tokens, heads, head_dim], tokens k_stride (v_stride)
+ *            elements apart (a multiple of 8; they may be columns of one
+ *            matrix), 16-byte aligned.
+ * q, q_out   device bf16 [tokens, q_heads, head_dim] likewise, or both NULL;
+ *            q_out may be q with the same stride.
+ * positions  device int32 [tokens]; with rope_dim > 0.
+ * rope       device fp32 [max_positions, rope_dim], 16-byte aligned: rope_dim
+ *            / 2 cosines, then the sines.  A position outside the table gives
+ *            NaN.
+ * rope_dim   0 (no rotation) .. head_dim, a multiple of 32.
+ * slots      a token whose slot is not in the cache (a negative one, say) is
+ *            left out: neither the cache nor its row of q_out is written.
+ *            Two tokens of one call must not have the same slot (it would hold
+ *            parts of both).
+ * A token whose key or value of a head holds an infinity or a NaN is NaN there
+ * as a whole: it reads back as NaN, and so is every row of attention that sees
+ * it.  Overlap of cache or q_out with another argument is refused, but for
+ * q_out in q's place.
+ *
+ * nvfp4_kv_read - the values of given slots, k_hat and v_hat, as fp32 or
+ * rounded to bf16 [tokens, heads, head_dim]; zeros for a slot that is not in
+ * the cache.  One launch.
+ */
+NVFP4_API size_t nvfp4_kv_page_bytes(int64_t heads, int64_t head_dim, int64_t page_size);
+NVFP4_API int nvfp4_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                              int64_t q_stride, void* q_out, int64_t q_out_stride, int64_t q_heads,
+                              const int32_t* positions, const float* rope, int64_t max_positions, int64_t rope_dim,
+                              int interleaved, const int32_t* slots, int64_t tokens, uint8_t* cache, int64_t pages,
+                              int64_t page_size, int64_t heads, int64_t head_dim, const float* k_scale,
+                              const float* v_scale, void* stream);
+NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_size, int64_t heads, int64_t head_dim,
+                            const float* k_scale, const float* v_scale, const int32_t* slots, int64_t tokens, void* k,
+                            void* v, int out_dtype, void* stream);
+
+/*
+ * nvfp4_kv_attention - attention of the last tokens of each sequence over its
+ * pages of the cache, whose keys and values were appended before (their own
+ * included): for new token i of a sequence with n new tokens and a context of
+ * kv_len, and query head h with its key head h / (q_heads / heads),
+ *   p_j = exp(scale * q . k_hat_j),  out = sum_j p_j v_hat_j / sum_j p_j,
+ *   lse = log sum_j p_j
+ * over the visible tokens j: all of the context; with causal j <= kv_len - n +
+ * i; with window > 0 also j > kv_len - n + i - window.  Rows that see nothing
+ * (kv_len 0, or fewer than the new tokens): out = 0, lse = -infinity.
+ *
+ * q          device bf16 [tokens, q_heads, head_dim], tokens q_stride elements
+ *            apart (a multiple of 8), 16-byte aligned.
+ * page_table device int32 [sequences, table_pages]: the pages of each context
+ *            in order.  Only the ones that kv_len reaches are used; the tokens
+ *            of a page number that is not in the cache are left out.
+ * kv_lens    device int32 [sequences]; a length past the table's is cut to it.
+ * q_starts   device int32 [sequences + 1]: the new tokens of sequence b are
+ *            rows q_starts[b] .. q_starts[b + 1] - 1 of q, out and lse; a
+ *            sequence may have none.  Rows behind the last sequence's are left
+ *            as they were.  NULL: one token each (tokens == sequences).
+ * q_heads    a multiple of heads.
+ * scale      finite.  window: >= 0; 0 (none) without causal.
+ * out        device bf16 [tokens, q_heads, head_dim] (contiguous); lse device
+ *            fp32 [tokens, q_heads] or NULL.
+ * workspace  >= nvfp4_kv_attention_workspace_size bytes, 16-byte aligned (0
+ *            bytes for short contexts: NULL allowed, one launch); one_each: q_starts is NULL.
+ * Logits and the softmax's sums are fp32; the products are exact in their fp16
+ * operands but for p, rounded to fp16 (11 bits).  Lengths are read on the
+ * device alone: a captured call follows them.  The order of the sums is fixed
+ * for given sizes and lengths.
+ */
+NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
+                                                   int64_t head_dim, int64_t page_size, int64_t table_pages,
+                                                   int one_each);
+NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t* cache, int64_t pages,
+                                 int64_t page_size, int64_t heads, int64_t head_dim, const float* k_scale,
+                                 const float* v_scale, const int32_t* page_table, int64_t table_pages,
+                                 const int32_t* kv_lens, const int32_t* q_starts, int64_t sequences, int64_t tokens,
+                                 int64_t q_heads, float scale, int causal, int64_t window, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * nvfp4_selftest_cvt - validation of the gfx950 FP4 and FP8 (E4M3)
  * conversion instructions against the library's portable ALU rounding and
  * decoding.

@@ -39,6 +39,8 @@ qat     Quantization-aware training of a linear layer: forward on the FP4
         gradient.
 mx      Microscaled formats (power-of-two scale per 32), and the residual +
         RMS norm with its gradient that feeds the product on them.
+kv      Key/value cache in NVFP4 with the position rotation, and attention over
+        it in float64.
 
 Parity status: every function here is pinned by ``-m "not gpu"`` tests against
 something other than itself (the pages' printed value set, torch's
@@ -60,4 +62,4 @@ from .gemm import dequant, dequant_f64, gemm_ref  # noqa: F401
 from .gptq import gptq_fos, gptq_fos_obs, hessian, hessian_factor  # noqa: F401
 from .w4a4 import ActResult, act_blockscaled, quantize_act, w4a4_gemm_ref  # noqa: F401
 from .qat import qat_forward, qat_input_grad, qat_weight_grad  # noqa: F401
-from . import mx  # noqa: F401
+from . import kv, mx  # noqa: F401
