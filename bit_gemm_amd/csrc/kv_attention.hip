@@ -27,10 +27,27 @@ namespace {
 
 constexpr float kLow = -1e37f;  // the bound before a row has seen a token
 
+// Inclusive sums over the lanes of a wave (all active), in six cross-lane adds.
+template <int CTRL, int ROWS_>
+__device__ __forceinline__ int moved(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS_, 0xF, false);
+}
+__device__ __forceinline__ int plus(int a, int b) { return a + b; }
+__device__ __forceinline__ int plus_f32(int a, int b) {
+  return __float_as_int(__int_as_float(a) + __int_as_float(b));
+}
+template <int (*ADD)(int, int)>
+__device__ __forceinline__ int wave_scan(int v) {
+  v = ADD(v, moved<0x111, 0xF>(v));  // from 1, 2, 4, 8 lanes down within rows of 16
+  v = ADD(v, moved<0x112, 0xF>(v));
+  v = ADD(v, moved<0x114, 0xF>(v));
+  v = ADD(v, moved<0x118, 0xF>(v));
+  v = ADD(v, moved<0x142, 0xA>(v));  // the last lane of row 0 and 2 to rows 1 and 3
+  return ADD(v, moved<0x143, 0xC>(v));  // lane 31 to rows 2 and 3
+}
+__device__ __forceinline__ int wave_scan(int v) { return wave_scan<plus>(v); }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  return v;
+  return __int_as_float(__builtin_amdgcn_readlane(wave_scan<plus_f32>(__float_as_int(v)), 63));
 }
 
 // ------------------------------------------------------------ the work list
@@ -90,9 +107,21 @@ template <int ROWS, bool BLOCK>
 __device__ bool find(const KvAttend& a, int parts, int least, int number, Item& w) {
   const int lane = threadIdx.x & 63;
   w.part_units = 1 << 28;
+  if (a.sequences == 1) {
+    w.index = w.base = 0;
+    w.local = number;
+    w.seq = sequence(a, 0);
+    const Extent e = extent<ROWS>(a, w.seq);
+    w.blocks = e.blocks;
+    if (parts > 0) w.part_units = max(least, (int)ceilf((float)e.blocks * (float)e.units * (1.0f + 1e-4f) / (float)parts));
+    return number < (BLOCK ? e.blocks : e.blocks * max(1, (e.units + w.part_units - 1) / w.part_units));
+  }
+  // the first 64 sequences' stay in registers
+  Extent mine = {0, 0};
+  if (lane < a.sequences) mine = extent<ROWS>(a, sequence(a, lane));
   if (parts > 0) {
-    float units = 0.0f;
-    for (int b = lane; b < a.sequences; b += 64) {
+    float units = (float)mine.blocks * (float)mine.units;
+    for (int b = lane + 64; b < a.sequences; b += 64) {
       const Extent e = extent<ROWS>(a, sequence(a, b));
       units += (float)e.blocks * (float)e.units;
     }
@@ -104,33 +133,23 @@ __device__ bool find(const KvAttend& a, int parts, int least, int number, Item& 
   for (int b0 = 0; b0 < a.sequences; b0 += 64) {
     int items = 0, key = 0;
     if (b0 + lane < a.sequences) {
-      const Extent e = extent<ROWS>(a, sequence(a, b0 + lane));
+      const Extent e = b0 == 0 ? mine : extent<ROWS>(a, sequence(a, b0 + lane));
       items = e.blocks * max(1, (e.units + w.part_units - 1) / w.part_units);
       key = BLOCK ? e.blocks : items;
     }
-    int sum_items = items, sum_key = key;  // inclusive
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int x = __shfl_up(sum_items, o, 64);
-      if (lane >= o) sum_items += x;
-      if constexpr (BLOCK) {
-        const int y = __shfl_up(sum_key, o, 64);
-        if (lane >= o) sum_key += y;
-      }
-    }
-    if constexpr (!BLOCK) sum_key = sum_items;
+    const int sum_items = wave_scan(items), sum_key = BLOCK ? wave_scan(key) : sum_items;
     const uint64_t past = __ballot(before + sum_key > number);
     if (past) {
       const int at = __builtin_ctzll(past);
       w.index = b0 + at;
       w.seq = sequence(a, w.index);
-      w.local = number - before - (__shfl(sum_key, at, 64) - __shfl(key, at, 64));
-      w.base = base + __shfl(sum_items, at, 64) - __shfl(items, at, 64);
+      w.local = number - before - __builtin_amdgcn_readlane(sum_key - key, at);
+      w.base = base + __builtin_amdgcn_readlane(sum_items - items, at);
       w.blocks = extent<ROWS>(a, w.seq).blocks;
       return true;
     }
-    base += __shfl(sum_items, 63, 64);
-    before += __shfl(sum_key, 63, 64);
+    base += __builtin_amdgcn_readlane(sum_items, 63);
+    before += __builtin_amdgcn_readlane(sum_key, 63);
   }
   return false;
 }
@@ -152,9 +171,86 @@ __device__ __forceinline__ void block_units(const KvAttend& a, const Sequence& s
   end = max(first, (hi + 31) >> 5);
 }
 
+// The row block and units [first, end) of an item; false: it has none.
+template <int ROWS>
+__device__ __forceinline__ bool find_part(const KvAttend& a, int parts, int least, int number, Item& w, int& block,
+                                          int& block_parts, int& first, int& end) {
+  if (!find<ROWS, false>(a, parts, least, number, w)) return false;
+  const int part = w.local / w.blocks;
+  block = w.blocks - 1 - (w.local - part * w.blocks);
+  block_units<ROWS>(a, w.seq, block * ROWS, first, end);
+  block_parts = max(1, (end - first + w.part_units - 1) / w.part_units);
+  if (part >= block_parts) return false;
+  const int units = (end - first + block_parts - 1) / block_parts;  // equal parts
+  first += part * units;
+  end = min(end, first + units);
+  return true;
+}
+
 // ------------------------------------------------------------- the operands
 
-// One unit's bytes for a lane.
+__device__ __forceinline__ f16x8_t join(f16x2_t a, f16x2_t b, f16x2_t c, f16x2_t d) {
+  return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// The two codes of byte j of a word (j constant after unrolling) times a power of two.
+__device__ __forceinline__ f16x2_t codes(uint32_t w, int j, float f) {
+  switch (j) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, f, 3);
+  }
+}
+
+// Operand j from a lane's words and the scales that belong to them: byte j of
+// each of four words, or bytes j and j + 2 of two where D is 64.  Keys and
+// values alike: the elements of a key may come in any order that the query's
+// follow (key_element).
+template <int D>
+__device__ __forceinline__ f16x8_t operand(const uint32_t (&w)[4], const f16x2_t (&g)[4], int j, float f) {
+  if constexpr (D == 64)
+    return join(codes(w[0], j, f) * g[0], codes(w[0], j + 2, f) * g[1], codes(w[1], j, f) * g[2], codes(w[1], j + 2, f) * g[3]);
+  else
+    return join(codes(w[0], j, f) * g[0], codes(w[1], j, f) * g[1], codes(w[2], j, f) * g[2], codes(w[3], j, f) * g[3]);
+}
+
+// Element of a lane's share of a key at place i of operand n.
+template <int D>
+__device__ constexpr int key_element(int n, int i) {
+  return D == 64 ? 8 * (i >> 2) + 2 * (n + 2 * ((i >> 1) & 1)) + (i & 1) : 8 * (i >> 1) + 2 * n + (i & 1);
+}
+
+// Words whose bytes hold the codes of two neighbouring tokens for one element:
+// from a lane's words of both tokens, the even and the odd elements.
+__device__ __forceinline__ uint32_t even(uint32_t a, uint32_t b) { return (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u); }
+__device__ __forceinline__ uint32_t odd(uint32_t a, uint32_t b) { return ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u); }
+
+// E4M3 bytes 0, 2 and 1, 3 of a word as fp16 times 2^-8: the byte's bits in
+// fp16's exponent and fraction (the exponents' biases differ by 8).  Every
+// byte gives a finite number, also 0x7F and what an unwritten page holds; the
+// codes are decoded with the factor 256.
+__device__ __forceinline__ f16x2_t scales02(uint32_t w) { return __builtin_bit_cast(f16x2_t, (w << 7) & 0x3F803F80u); }
+__device__ __forceinline__ f16x2_t scales13(uint32_t w) { return __builtin_bit_cast(f16x2_t, (w >> 1) & 0x3F803F80u); }
+
+// The scales of a lane's keys in half h of a unit, from its word of four bytes
+// (two where D is 64).
+template <int D>
+__device__ __forceinline__ void key_scales(uint32_t w, int h, f16x2_t (&g)[4]) {
+  const f16x2_t z = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)(w >> (D == 64 ? 8 * h : 16 * h)), 1.0f, false);
+  g[0] = g[1] = f16x2_t{z[0], z[0]};
+  g[2] = g[3] = D == 64 ? g[0] : f16x2_t{z[1], z[1]};
+}
+
+// The scales of a lane's values: halves 0 and 1, places (0, 1) and (2, 3) each.
+__device__ __forceinline__ void value_scales(uint2 w, f16x2_t (&g)[4]) {
+  g[0] = scales02(w.x);
+  g[1] = scales13(w.x);
+  g[2] = scales02(w.y);
+  g[3] = scales13(w.y);
+}
+
+// One unit's bytes for a lane, and the operands made of them.
 template <int D>
 struct Unit {
   static constexpr int P = KvUnit<D>::kPanels, H = D == 64 ? 1 : 2;  // 16-byte pieces per panel
@@ -179,36 +275,248 @@ struct Unit {
       }
     }
   }
+  __device__ __forceinline__ f16x8_t key(int p, int h, int n) const {
+    f16x2_t g[4];
+    key_scales<D>(ks[p], h, g);
+    const u32x4_t& x = k[p][D == 64 ? 0 : h];
+    const uint32_t w[4] = {D == 64 ? x[2 * h] : x[0], D == 64 ? x[2 * h + 1] : x[1], x[2], x[3]};
+    return operand<D>(w, g, n, 1.0f);
+  }
+  // Tile t of V^T: elements 8 c + t of lane c's 8 (4 c + t of 4).
+  __device__ __forceinline__ f16x8_t value(int p, int t) const {
+    f16x2_t g[4];
+    value_scales(vs[p], g);
+    const u32x4_t &x = v[p][0], &y = v[p][H - 1];
+    const uint32_t e[4] = {even(x[0], x[1]), even(x[2], x[3]), even(y[0], y[1]), even(y[2], y[3])};
+    const uint32_t o[4] = {odd(x[0], x[1]), odd(x[2], x[3]), odd(y[0], y[1]), odd(y[2], y[3])};
+    return t & 1 ? operand<D>(o, g, t >> 1, 256.0f) : operand<D>(e, g, t >> 1, 256.0f);
+  }
 };
 
-__device__ __forceinline__ f16x8_t join(f16x2_t a, f16x2_t b, f16x2_t c, f16x2_t d) {
-  return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
+// Where a sequence's units lie: a wave holds the offsets in the cache of 64
+// units of the head at a time, one per lane.
+template <int D>
+struct Units {
+  const KvAttend& a;
+  const int* table;
+  int head, shift, first;
+  uint32_t lo, hi;  // the lane's offset; that of page 0 if the page is not in the cache
+  uint64_t in;      // lanes whose page is in the cache
 
-// The 8 codes of a word times a scale (in both halves of sg).
-__device__ __forceinline__ f16x8_t key_operand(uint32_t w, f16x2_t sg) {
-  return join(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * sg,
-              __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * sg,
-              __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * sg,
-              __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * sg);
-}
+  __device__ __forceinline__ Units(const KvAttend& a_, int index, int head_)
+      : a(a_), table(a_.table + (int64_t)index * a_.table_pages), head(head_), shift(a_.page_shift - 5), first(-(1 << 30)) {}
 
-template <int J>
-__device__ __forceinline__ f16x2_t pair_of(uint32_t w) {
-  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 256.0f, J);
-}
+  // The lane of unit u, which no earlier unit is asked for after.
+  __device__ __forceinline__ int lane_of(int u) {
+    if (u - first >= 64) {
+      const int unit = u + (threadIdx.x & 63), page = unit >> shift, id = page < a.table_pages ? table[page] : -1;
+      const bool held = id >= 0 && id < a.pages;
+      first = u;
+      in = __ballot(held);
+      const uint64_t offset =
+          (((uint64_t)((int64_t)(held ? id : 0) * a.heads + head) << shift) + (unit & ((1 << shift) - 1))) * KvUnit<D>::kBytes;
+      lo = (uint32_t)offset;
+      hi = (uint32_t)(offset >> 32);
+    }
+    return u - first;
+  }
+  __device__ __forceinline__ const uint8_t* at(int u) {
+    const int lane = lane_of(u);
+    return a.cache + ((uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, lane) << 32 |
+                      (uint32_t)__builtin_amdgcn_readlane(lo, lane));
+  }
+  __device__ __forceinline__ bool held(int u) {
+    const int lane = lane_of(u);
+    return in >> lane & 1;
+  }
+};
 
-// Words whose bytes hold the codes of two neighbouring tokens for one element:
-// from a lane's words of both tokens, the even and the odd elements.
-__device__ __forceinline__ uint32_t even(uint32_t a, uint32_t b) { return (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u); }
-__device__ __forceinline__ uint32_t odd(uint32_t a, uint32_t b) { return ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u); }
+// The state of 16 R rows in a wave: row c of tile r in the lanes c, c + 16, ..
+template <int D, int R>
+struct Rows {
+  static constexpr int P = Unit<D>::P, N = D == 64 ? 2 : 4, T = 2 * N;  // K steps and tiles of V per panel
+  f16x8_t q[R][P][N];  // operands of Q^T: of elements 128 p + 8 N g ..
+  f32x4_t acc[R][P][T];
+  float factor[R], m[R], l[R];
+  int lo[R], hi[R];
+  int lo_all, hi_all;  // tokens that every row sees
 
-// E4M3 bytes 0, 2 and 1, 3 of a word as fp16 times 2^-8: the byte's bits in
-// fp16's exponent and fraction (the exponents' biases differ by 8).  Every
-// byte gives a finite number, also 0x7F and what an unwritten page holds; the
-// codes are decoded with the factor 256.
-__device__ __forceinline__ f16x2_t scales02(uint32_t w) { return __builtin_bit_cast(f16x2_t, (w << 7) & 0x3F803F80u); }
-__device__ __forceinline__ f16x2_t scales13(uint32_t w) { return __builtin_bit_cast(f16x2_t, (w >> 1) & 0x3F803F80u); }
+  // rows [first, first + 16 R) of a sequence
+  __device__ __forceinline__ void start(const KvAttend& a, const Sequence& seq, int first, int head) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int rows = seq.count * a.group;
+    const float base = a.scale * 1.44269504088896340736f * a.k_scale[head];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = min(first + r * 16 + c, rows - 1);  // rows past the last: computed, not stored
+      const int t = row / a.group;
+      visible(a, seq, t, lo[r], hi[r]);
+      const uint16_t* src = a.q + (int64_t)(seq.first + t) * a.q_stride + (head * a.group + row - t * a.group) * D;
+      // read twice, the second time from the cache: fewer registers than held meanwhile
+      auto raw = [&](int p, int n) { return *reinterpret_cast<const u32x4_t*>(src + p * 128 + g * (8 * N) + n * 8); };
+      float top = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const u32x4_t x = raw(p, n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
+        }
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64));
+      // 2^e, e = 14 - floor(log2(top)); rows of zeros, subnormals or infinities keep theirs
+      const int exponent = (int)(__float_as_uint(top) >> 23);
+      const int e = exponent == 0 || exponent == 255 ? 0 : min(14 + 127 - exponent, 126);
+      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+      factor[r] = base * __uint_as_float((uint32_t)(127 - e) << 23);
+      const float sign = factor[r] < 0.0f ? -up : up;
+      factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        float x[8 * N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const u32x4_t y = raw(p, n);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[8 * n + 2 * i] = __uint_as_float(y[i] << 16) * sign;
+            x[8 * n + 2 * i + 1] = __uint_as_float(y[i] & 0xFFFF0000u) * sign;
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[r][p][n][i] = (_Float16)x[key_element<D>(n, i)];
+      }
+      m[r] = kLow;
+      l[r] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int t_ = 0; t_ < T; ++t_) acc[r][p][t_] = f32x4_t{};
+    }
+    int skip;
+    visible(a, seq, min(first, rows - 1) / a.group, skip, hi_all);
+    visible(a, seq, (min(first + 16 * R, rows) - 1) / a.group, lo_all, skip);
+  }
+
+  template <class Operands>
+  __device__ __forceinline__ void logits(const Operands& x, f32x4_t (&s)[R][2]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{};
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+          const f16x8_t k = x.key(p, h, n);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+            s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][p][n], s[r][h], 0, 0, 0);
+        }
+  }
+
+  // Whether every row sees all of the unit at token t0.
+  __device__ __forceinline__ bool whole(int t0, bool held) const { return held && t0 >= lo_all && t0 + 32 <= hi_all; }
+
+  // Result i of half h: token t0 + 16 h + 4 g + i.
+  __device__ __forceinline__ void mask(f32x4_t (&s)[R][2], int t0, bool held) {
+    const int g = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = t0 + 16 * h + 4 * g + i;
+          s[r][h][i] = held && j >= lo[r] && j < hi[r] ? s[r][h][i] : -__builtin_inff();
+        }
+  }
+
+  // Logits in powers of two over the rows' bounds; true: some passed 15 and the bounds must be raised.
+  __device__ __forceinline__ bool exponents(const f32x4_t (&s)[R][2], f32x4_t (&y)[R][2]) const {
+    float top = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[r][h][i] = __builtin_fmaf(s[r][h][i], factor[r], -m[r]);
+        top = fmaxf(fmaxf(top, y[r][h][0]), y[r][h][1]);
+        top = fmaxf(fmaxf(top, y[r][h][2]), y[r][h][3]);
+      }
+    return __any(top > 15.0f);
+  }
+
+  // Raises the bounds of rows with a logit 15 above to 7 below their largest.
+  __device__ __forceinline__ void raise(const f32x4_t (&s)[R][2], f32x4_t (&y)[R][2]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
+                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
+      top = fmaxf(top, __shfl_xor(top, 16, 64));
+      top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor[r];
+      const float to = top - m[r] > 15.0f ? top - 7.0f : m[r];
+      const float shrink = __builtin_amdgcn_exp2f(m[r] - to);
+      m[r] = to;
+      l[r] *= shrink;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[r][p][t] *= shrink;
+    }
+    exponents(s, y);
+  }
+
+  __device__ __forceinline__ void probabilities(const f32x4_t (&y)[R][2], f16x8_t (&pr)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = __builtin_amdgcn_exp2f(y[r][h][i]);
+          l[r] += e;
+          pr[r][4 * h + i] = (_Float16)e;
+        }
+  }
+
+  template <class Operands>
+  __device__ __forceinline__ void add(const Operands& x, const f16x8_t (&pr)[R]) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const f16x8_t v = x.value(p, t);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          acc[r][p][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pr[r], acc[r][p][t], 0, 0, 0);
+      }
+  }
+
+  template <class Operands>
+  __device__ __forceinline__ void attend(const Operands& x, int t0, bool held) {
+    f32x4_t s[R][2], y[R][2];
+    f16x8_t pr[R];
+    logits(x, s);
+    if (!whole(t0, held)) mask(s, t0, held);
+    if (exponents(s, y)) raise(s, y);
+    probabilities(y, pr);
+    add(x, pr);
+  }
+
+  // The sums over a row's four lanes.
+  __device__ __forceinline__ void finish() {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      l[r] += __shfl_xor(l[r], 16, 64);
+      l[r] += __shfl_xor(l[r], 32, 64);
+    }
+  }
+};
 
 // Elements [d, d + E) of a row of the output, and its log sum (natural) at d = 0.
 template <int D, int E>
@@ -228,8 +536,10 @@ __device__ __forceinline__ void store_row(const KvAttend& a, const Sequence& s, 
   uint16_t* to = a.out + at * D + d;
   if constexpr (E == 8)
     *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-  else
+  else if constexpr (E == 4)
     *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(to) = w[0];
   if (a.lse && d == 0)
     a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994530942f;
 }
@@ -237,358 +547,425 @@ __device__ __forceinline__ void store_row(const KvAttend& a, const Sequence& s, 
 // -------------------------------------------------------------- the kernels
 
 template <int D, int R>
-__global__ __launch_bounds__(256) void k_kv_rows(KvAttend a, int parts, int least, float* __restrict__ partial,
-                                                 float2* __restrict__ stats) {
-  using U = Unit<D>;
-  constexpr int P = U::P, N = D == 64 ? 2 : 4, T = 2 * N;  // K steps and tiles of V per panel
-  constexpr int W = D == 64 ? 64 : 128, ROWS = 16 * R;
-  __shared__ float s_o[4][16][W + 4];
-  __shared__ float2 s_ml[4][ROWS];
+__global__ __launch_bounds__(256, 2) void k_kv_rows(KvAttend a, int parts, int least, float* __restrict__ partial,
+                                                    float2* __restrict__ stats) {
+  using X = Rows<D, R>;
+  constexpr int P = X::P, T = X::T, ROWS = 16 * R, WAVES = 4, DEPTH = 2;
+  __shared__ float s_o[WAVES][16][68];
+  __shared__ float2 s_ml[WAVES][ROWS];
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, c = lane & 15;
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int number = blockIdx.x / a.heads, head = blockIdx.x - number * a.heads;
   Item w;
-  if (!find<ROWS, false>(a, parts, least, number, w)) return;
+  int block, block_parts, u, end;
+  if (!find_part<ROWS>(a, parts, least, number, w, block, block_parts, u, end)) return;
   const Sequence seq = w.seq;
-  const int part = w.local / w.blocks, block = w.blocks - 1 - (w.local - part * w.blocks);
-  int first, end;
-  block_units<ROWS>(a, seq, block * ROWS, first, end);
-  const int block_parts = max(1, (end - first + w.part_units - 1) / w.part_units);
-  if (part >= block_parts) return;
-  first += part * w.part_units;
-  end = min(end, first + w.part_units);
-
-  // queries, as operands of Q^T: row c of a tile, elements 128 p + 32 g + 8 n ..
-  f16x8_t q[R][P][N];
-  float factor[R], m[R], l[R];
-  int lo[R], hi[R];
   const int rows = seq.count * a.group;
-  const float base = a.scale * 1.44269504088896340736f * a.k_scale[head];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = block * ROWS + r * 16 + c;
-    const int t = min(row, rows - 1) / a.group;
-    const int at = min(row, rows - 1) - t * a.group;
-    visible(a, seq, t, lo[r], hi[r]);
-    const uint16_t* src = a.q + (int64_t)(seq.first + t) * a.q_stride + (head * a.group + at) * D;
-    u32x4_t raw[P][N];
-    float top = 0.0f;
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int n = 0; n < N; ++n) {
-        raw[p][n] = *reinterpret_cast<const u32x4_t*>(src + p * 128 + g * (8 * N) + n * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[p][n][i] << 16)),
-                                 fabsf(__uint_as_float(raw[p][n][i] & 0xFFFF0000u))));
-      }
-    top = fmaxf(top, __shfl_xor(top, 16, 64));
-    top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // 2^e, e = 14 - floor(log2(top)); rows of zeros, infinities or subnormals keep a factor in range
-    const int exponent = (int)(__float_as_uint(top) >> 23);
-    const int e = exponent == 0 || exponent == 255 ? 0 : min(14 + 127 - exponent, 126);
-    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    factor[r] = base * __uint_as_float((uint32_t)(127 - e) << 23);
-    const float sign = factor[r] < 0.0f ? -up : up;
-    factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q[r][p][n][2 * i] = (_Float16)(__uint_as_float(raw[p][n][i] << 16) * sign);
-          q[r][p][n][2 * i + 1] = (_Float16)(__uint_as_float(raw[p][n][i] & 0xFFFF0000u) * sign);
-        }
-    m[r] = kLow;
-    l[r] = 0.0f;
-  }
-  // units that every row sees whole
-  int lo_all, hi_all, skip;
-  visible(a, seq, block * ROWS / a.group, skip, hi_all);
-  visible(a, seq, (min((block + 1) * ROWS, rows) - 1) / a.group, lo_all, skip);
 
-  f32x4_t acc[R][P][T] = {};
-
-  const int unit_shift = a.page_shift - 5;
-  const int* table = a.table + (int64_t)w.index * a.table_pages;
-  // page ids, one per lane: of the 64 pages from page0 on
-  int page0 = 0, ids = -1;
-  bool fresh = false;
-  auto locate = [&](int u, bool& held) -> const uint8_t* {
-    const int page = u >> unit_shift;
-    if (!fresh || page - page0 >= 64) {
-      page0 = page;
-      ids = page + lane < a.table_pages ? table[page + lane] : -1;
-      fresh = true;
-    }
-    const int id = __builtin_amdgcn_readlane(ids, page - page0);
-    held = id >= 0 && id < a.pages;
-    return a.cache + (((int64_t)(held ? id : 0) * a.heads + head) * (1 << unit_shift) + (u & ((1 << unit_shift) - 1))) *
-                         KvUnit<D>::kBytes;
+  // DEPTH units under way, from here on
+  Units<D> units(a, w.index, head);
+  Unit<D> x[DEPTH];
+  bool held[DEPTH];
+  u += wave;
+  auto load = [&](int n, int at) {
+    if (at >= end) return;
+    x[n].load(units.at(at), lane);
+    held[n] = units.held(at);
   };
-
-  auto attend = [&](const U& x, int u, bool held) {
-    f32x4_t s[R][2] = {};
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
+  for (int n = 0; n < DEPTH; ++n) load(n, u + n * WAVES);
+  X z;
+  z.start(a, seq, block * ROWS, head);
+  for (; u < end; u += DEPTH * WAVES) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f16x2_t s0, s1;  // the scales of the lane's elements
-        if constexpr (D == 64) {
-          const f16x2_t z = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)x.ks[p], 1.0f, false);
-          s0 = s1 = f16x2_t{z[h], z[h]};
-        } else {
-          const f16x2_t z = h ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)x.ks[p], 1.0f, true)
-                              : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)x.ks[p], 1.0f, false);
-          s0 = f16x2_t{z[0], z[0]};
-          s1 = f16x2_t{z[1], z[1]};
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const uint32_t word = D == 64 ? x.k[p][0][2 * h + n] : x.k[p][D == 64 ? 0 : h][n];
-          const f16x8_t k = key_operand(word, n < 2 ? s0 : s1);
-#pragma unroll
-          for (int r = 0; r < R; ++r)
-            s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][p][n], s[r][h], 0, 0, 0);
-        }
-      }
+    for (int n = 0; n < DEPTH; ++n) {
+      const int at = u + n * WAVES;
+      if (at >= end) break;
+      z.attend(x[n], at * 32, held[n]);
+      load(n, at + DEPTH * WAVES);
     }
-    // logits: token 32 u + 16 h + 4 g + i, row c of tile r
-    const int t0 = u * 32;
-    const bool whole = held && t0 >= lo_all && t0 + 32 <= hi_all;
-    f16x8_t pr[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (!whole) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = t0 + 16 * h + 4 * g + i;
-            s[r][h][i] = held && j >= lo[r] && j < hi[r] ? s[r][h][i] : -__builtin_inff();
-          }
-      }
-      float top = fmaxf(fmaxf(fmaxf(s[r][0][0], s[r][0][1]), fmaxf(s[r][0][2], s[r][0][3])),
-                        fmaxf(fmaxf(s[r][1][0], s[r][1][1]), fmaxf(s[r][1][2], s[r][1][3])));
-      if (__any(__builtin_fmaf(top, factor[r], -m[r]) > 15.0f)) {
-        top = fmaxf(top, __shfl_xor(top, 16, 64));
-        top = fmaxf(top, __shfl_xor(top, 32, 64)) * factor[r];
-        const float to = top - m[r] > 15.0f ? top - 7.0f : m[r];
-        const float shrink = __builtin_amdgcn_exp2f(m[r] - to);
-        m[r] = to;
-        l[r] *= shrink;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int t = 0; t < T; ++t) acc[r][p][t] *= shrink;
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][h][i], factor[r], -m[r]));
-          l[r] += e;
-          pr[r][4 * h + i] = (_Float16)e;
-        }
-    }
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const f16x2_t g0 = scales02(x.vs[p].x), g1 = scales13(x.vs[p].x);  // half 0: places (0, 1), (2, 3)
-      const f16x2_t g2 = scales02(x.vs[p].y), g3 = scales13(x.vs[p].y);
-      uint32_t e[4], o[4];  // even and odd elements of the four pairs of tokens
-      if constexpr (D == 64) {
-        e[0] = even(x.v[p][0][0], x.v[p][0][1]);
-        o[0] = odd(x.v[p][0][0], x.v[p][0][1]);
-        e[1] = even(x.v[p][0][2], x.v[p][0][3]);
-        o[1] = odd(x.v[p][0][2], x.v[p][0][3]);
-        f16x8_t v;
-#define NVFP4_TILE(t, w, j)                                                                               \
-  v = join(pair_of<j>(w[0]) * g0, pair_of<j + 2>(w[0]) * g1, pair_of<j>(w[1]) * g2, pair_of<j + 2>(w[1]) * g3); \
-  _Pragma("unroll") for (int r = 0; r < R; ++r) acc[r][p][t] =                                           \
-      __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pr[r], acc[r][p][t], 0, 0, 0);
-        NVFP4_TILE(0, e, 0)
-        NVFP4_TILE(1, o, 0)
-        NVFP4_TILE(2, e, 1)
-        NVFP4_TILE(3, o, 1)
-#undef NVFP4_TILE
-      } else {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4_t& v = x.v[p][D == 64 ? 0 : h];
-          e[2 * h] = even(v[0], v[1]);
-          o[2 * h] = odd(v[0], v[1]);
-          e[2 * h + 1] = even(v[2], v[3]);
-          o[2 * h + 1] = odd(v[2], v[3]);
-        }
-        f16x8_t v;
-#define NVFP4_TILE(t, w, j)                                                                           \
-  v = join(pair_of<j>(w[0]) * g0, pair_of<j>(w[1]) * g1, pair_of<j>(w[2]) * g2, pair_of<j>(w[3]) * g3); \
-  _Pragma("unroll") for (int r = 0; r < R; ++r) acc[r][p][t] =                                        \
-      __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pr[r], acc[r][p][t], 0, 0, 0);
-        NVFP4_TILE(0, e, 0)
-        NVFP4_TILE(1, o, 0)
-        NVFP4_TILE(2, e, 1)
-        NVFP4_TILE(3, o, 1)
-        NVFP4_TILE(4, e, 2)
-        NVFP4_TILE(5, o, 2)
-        NVFP4_TILE(6, e, 3)
-        NVFP4_TILE(7, o, 3)
-#undef NVFP4_TILE
-      }
-    }
-  };
-
-  // two units under way
-  U x, y;
-  bool held_x = false, held_y = false;
-  int u = first + wave;
-  if (u < end) x.load(locate(u, held_x), lane);
-  if (u + 4 < end) y.load(locate(u + 4, held_y), lane);
-  while (u < end) {
-    attend(x, u, held_x);
-    if (u + 8 < end) x.load(locate(u + 8, held_x), lane);
-    u += 4;
-    if (u >= end) break;
-    attend(y, u, held_y);
-    if (u + 8 < end) y.load(locate(u + 8, held_y), lane);
-    u += 4;
   }
 
-  // the four waves' parts brought to one bound and added
+  // the waves' parts brought to one bound and added, 64 elements of 16 rows at a time
+  z.finish();
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    l[r] += __shfl_xor(l[r], 16, 64);
-    l[r] += __shfl_xor(l[r], 32, 64);
-    if (g == 0) s_ml[wave][r * 16 + c] = make_float2(m[r], l[r]);
-  }
+  for (int r = 0; r < R; ++r)
+    if (g == 0) s_ml[wave][r * 16 + c] = make_float2(z.m[r], z.l[r]);
   __syncthreads();
   const float vs = a.v_scale[head];
   const int64_t slot = (int64_t)blockIdx.x * ROWS;  // of the workspace
+  const int tr = threadIdx.x >> 4, td = (threadIdx.x & 15) * 4;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float2 z0 = s_ml[0][r * 16 + c], z1 = s_ml[1][r * 16 + c], z2 = s_ml[2][r * 16 + c], z3 = s_ml[3][r * 16 + c];
-    const float top = fmaxf(fmaxf(z0.x, z1.x), fmaxf(z2.x, z3.x));
-    const float shrink = __builtin_amdgcn_exp2f(m[r] - top);
+    float top = kLow, m_row = kLow, l_row = 0.0f;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      if (r + p > 0) __syncthreads();
-      // the lane's elements of its row: tile t, result i is element 8 i + t (4 i + t) after W / 4 * g
+    for (int v = 0; v < WAVES; ++v) {
+      top = fmaxf(top, s_ml[v][r * 16 + c].x);
+      m_row = fmaxf(m_row, s_ml[v][r * 16 + tr].x);
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+    for (int v = 0; v < WAVES; ++v)
+      l_row += s_ml[v][r * 16 + tr].y * __builtin_amdgcn_exp2f(s_ml[v][r * 16 + tr].x - m_row);
+    const float shrink = __builtin_amdgcn_exp2f(z.m[r] - top);
+    const int row = block * ROWS + r * 16 + tr;
+    // element 128 p + 32 g + 8 i + t of row c is result i of tile t (D = 64: 16 g + 4 i + t); a
+    // pass takes the results 2 k and 2 k + 1 (D = 64: all)
+    constexpr int PASSES = D == 64 ? 1 : 2;
+#pragma unroll
+    for (int pass = 0; pass < P * PASSES; ++pass) {
+      const int p = pass / PASSES, k = pass % PASSES;
+      if (r + pass > 0) __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4 / PASSES; ++i)
 #pragma unroll
         for (int t = 0; t < T; t += 4) {
           float4 o;
-          o.x = acc[r][p][t][i] * shrink;
-          o.y = acc[r][p][t + 1][i] * shrink;
-          o.z = acc[r][p][t + 2][i] * shrink;
-          o.w = acc[r][p][t + 3][i] * shrink;
-          *reinterpret_cast<float4*>(&s_o[wave][c][g * (W / 4) + i * T + t]) = o;
+          o.x = z.acc[r][p][t][2 * k + i] * shrink;
+          o.y = z.acc[r][p][t + 1][2 * k + i] * shrink;
+          o.z = z.acc[r][p][t + 2][2 * k + i] * shrink;
+          o.w = z.acc[r][p][t + 3][2 * k + i] * shrink;
+          *reinterpret_cast<float4*>(&s_o[wave][c][g * 16 + i * T + t]) = o;
         }
       __syncthreads();
-      constexpr int E = W / 16;  // elements of a thread
-      const int tr = threadIdx.x >> 4, d = (threadIdx.x & 15) * E;
-      float o[E];
+      float o[4] = {};
 #pragma unroll
-      for (int i = 0; i < E; i += 4) {
-        float4 z = *reinterpret_cast<const float4*>(&s_o[0][tr][d + i]);
+      for (int v = 0; v < WAVES; ++v)
 #pragma unroll
-        for (int v = 1; v < 4; ++v) {
-          const float4 n = *reinterpret_cast<const float4*>(&s_o[v][tr][d + i]);
-          z.x += n.x;
-          z.y += n.y;
-          z.z += n.z;
-          z.w += n.w;
-        }
-        o[i] = z.x;
-        o[i + 1] = z.y;
-        o[i + 2] = z.z;
-        o[i + 3] = z.w;
-      }
-      float m_row = kLow, l_row = 0.0f;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) m_row = fmaxf(m_row, s_ml[v][r * 16 + tr].x);
-#pragma unroll
-      for (int v = 0; v < 4; ++v)
-        l_row += s_ml[v][r * 16 + tr].y * __builtin_amdgcn_exp2f(s_ml[v][r * 16 + tr].x - m_row);
-      const int row = block * ROWS + r * 16 + tr;
+        for (int i = 0; i < 4; ++i) o[i] += s_o[v][tr][td + i];
       if (row >= rows) continue;
+      const int d = D == 64 ? td : p * 128 + (td >> 4) * 32 + k * 16 + (td & 15);
       if (block_parts > 1) {
-        float* to = partial + (slot + r * 16 + tr) * D + p * 128 + d;
-#pragma unroll
-        for (int i = 0; i < E; i += 4) *reinterpret_cast<float4*>(to + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        if (p == 0 && d == 0) stats[slot + r * 16 + tr] = make_float2(m_row, l_row);
+        *reinterpret_cast<float4*>(partial + (slot + r * 16 + tr) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+        if (d == 0) stats[slot + r * 16 + tr] = make_float2(m_row, l_row);
       } else {
-        store_row<D, E>(a, seq, row, head, p * 128 + d, o, m_row, l_row, vs);
+        store_row<D, 4>(a, seq, row, head, d, o, m_row, l_row, vs);
       }
     }
   }
 }
 
-// A row of a split block: its parts brought to one bound and added in order.
-template <int D, int R>
-__global__ __launch_bounds__(256) void k_kv_join(KvAttend a, int parts, int least, const float* __restrict__ partial,
-                                                 const float2* __restrict__ stats) {
-  constexpr int ROWS = 16 * R, E = 8, LANES = D / E;  // threads of a row
+// Operands in LDS, 1 KiB each in the lanes' order; a panel's are the keys of
+// half 0 and 1, the even and the odd tiles of its values, N of each.
+template <int D>
+struct Staged {
+  static constexpr int P = Unit<D>::P, N = D == 64 ? 2 : 4;
+  static constexpr int kBytes = P * 4 * N * 1024;  // of a unit
+  const uint8_t* at;  // the lane's 16 bytes of the unit's first operand
+  __device__ __forceinline__ f16x8_t key(int p, int h, int n) const {
+    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + h) * N + n) * 1024);
+  }
+  __device__ __forceinline__ f16x8_t value(int p, int t) const {
+    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + 2 + (t & 1)) * N + (t >> 1)) * 1024);
+  }
+};
+
+// A wave's share of a unit's way into LDS: 4 p + 0, 1 the keys of half 0, 1 of
+// panel p, 4 p + 2, 3 the even, odd tiles of its values; N operands.
+template <int D>
+struct Share {
+  static constexpr int N = D == 64 ? 2 : 4, kCount = 4 * Unit<D>::P;
+  u32x4_t a, b;
+  uint2 s;
+
+  __device__ __forceinline__ void load(const uint8_t* u, int share, int lane) {
+    const int p = share >> 2, kind = share & 3;
+    const bool key = kind < 2;
+    if constexpr (D == 64) {
+      a = *reinterpret_cast<const u32x4_t*>(u + (key ? 0 : KvUnit<D>::kValues) + lane * 16);
+      if (key)
+        s.x = *reinterpret_cast<const uint16_t*>(u + KvUnit<D>::kKeyScales + lane * 2);
+      else
+        s = *reinterpret_cast<const uint2*>(u + KvUnit<D>::kValueScales + (lane >> 4) * 32 + ((lane & 15) >> 2) * 8);
+    } else {  // keys: 16 bytes and one word of scales, the rest read for nothing instead of a branch
+      a = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues)) + lane * 16);
+      b = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues + 1024)) + lane * 16);
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(
+          u + (p * 256 + (key ? KvUnit<D>::kKeyScales : KvUnit<D>::kValueScales)) + (key ? lane * 4 : (lane >> 1) * 8));
+      s.x = w[0];
+      s.y = w[1];
+    }
+  }
+  // Operands [from, until), without branches, to be scheduled among matrix instructions.
+  __device__ __forceinline__ void store(uint8_t* to, int share, int from, int until) const {
+    const int kind = share & 3;
+    const bool key = kind < 2;
+    const uint32_t low = key ? 0xFFFFFFFFu : 0x0F0F0F0Fu;  // bits that come from the first of two words
+    const int right = kind == 3 ? 4 : 0, left = kind == 2 ? 4 : 0;
+    uint32_t w[4] = {};
+    if constexpr (D == 64) {
+      w[0] = ((kind == 1 ? a[2] : a[0]) >> right & low) | (a[1] << left & ~low);
+      w[1] = ((key ? (kind ? a[3] : a[1]) : a[2]) >> right & low) | (a[3] << left & ~low);
+    } else {
+      w[0] = (a[0] >> right & low) | (a[1] << left & ~low);
+      w[1] = ((key ? a[1] : a[2]) >> right & low) | (a[3] << left & ~low);
+      w[2] = ((key ? a[2] : b[0]) >> right & low) | (b[1] << left & ~low);
+      w[3] = ((key ? a[3] : b[2]) >> right & low) | (b[3] << left & ~low);
+    }
+    f16x2_t gk[4], gv[4], g[4];
+    key_scales<D>(kind & 1 ? s.x >> (D == 64 ? 8 : 16) : s.x, 0, gk);
+    value_scales(s, gv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      g[i] = __builtin_bit_cast(f16x2_t, key ? __builtin_bit_cast(uint32_t, gk[i]) : __builtin_bit_cast(uint32_t, gv[i]));
+    const float f = key ? 1.0f : 256.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      if (n >= from && n < until) *reinterpret_cast<f16x8_t*>(to + (share * N + n) * 1024) = operand<D>(w, g, n, f);
+  }
+};
+
+// Many rows: 16 R for each of 8 waves, which decode tiles of kUnits units
+// together into LDS operands.
+template <int D>
+struct Tiles {
+  static constexpr int kWaves = 8, R = D == 256 ? 1 : 2, kRows = kWaves * 16 * R;
+  static constexpr int kUnits = D == 64 ? 4 : D == 128 ? 2 : 1;
+  static constexpr int kShares = kUnits * Share<D>::kCount / kWaves;  // of a wave
+  static_assert(kShares > 0 && kShares * kWaves == kUnits * Share<D>::kCount, "every operand has a wave");
+  static constexpr int kTileBytes = kUnits * Staged<D>::kBytes;
+};
+
+template <int D>
+__global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend a, int parts, int least, float* __restrict__ partial,
+                                                     float2* __restrict__ stats) {
+  using C = Tiles<D>;
+  using X = Rows<D, C::R>;
+  constexpr int P = X::P, N = X::N, T = X::T, ROWS = C::kRows;
+  extern __shared__ __align__(16) uint8_t s_kv[];  // three tiles
+
+  const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int number = blockIdx.x / a.heads, head = blockIdx.x - number * a.heads;
+  Item w;
+  int block, block_parts, first, end;
+  if (!find_part<ROWS>(a, parts, least, number, w, block, block_parts, first, end)) return;
+  const Sequence seq = w.seq;
+  const int rows = seq.count * a.group;
+  const int row0 = block * ROWS + wave * 16 * C::R;
+  const bool active = row0 < rows;
+
+  Units<D> ahead(a, w.index, head), mine(a, w.index, head);
+  Share<D> x[C::kShares];
+  auto load = [&](int tile) {
+#pragma unroll
+    for (int n = 0; n < C::kShares; ++n) {
+      const int at = wave * C::kShares + n;
+      x[n].load(ahead.at(min(tile + at / Share<D>::kCount, end - 1)), at % Share<D>::kCount, lane);
+    }
+  };
+  // Piece n of the wave's operands, of as many as there are units before the
+  // last; past the end: of what the registers hold, never used.
+  auto store = [&](uint8_t* to, int n) {
+    constexpr int all = C::kShares * N, pieces = C::kUnits > 1 ? C::kUnits - 1 : 1, each = (all + pieces - 1) / pieces;
+#pragma unroll
+    for (int i = 0; i < C::kShares; ++i) {
+      const int at = wave * C::kShares + i;
+      x[i].store(to + at / Share<D>::kCount * Staged<D>::kBytes + lane * 16, at % Share<D>::kCount, n * each - i * N,
+                 (n + 1) * each - i * N);
+    }
+  };
+  // While tile i is multiplied, tile i + 1 is decoded into the next of three
+  // buffers and tile i + 2 is on its way from memory.  The one barrier of a
+  // turn stands before the first use of tile i + 1; the buffer that a turn
+  // writes was last read before the barrier of the turn before.
+  uint8_t *now = s_kv, *next = s_kv + C::kTileBytes, *spare = s_kv + 2 * C::kTileBytes;
+  if (first < end) load(first);
+  X z;
+  z.start(a, seq, min(row0, rows - 1), head);
+#pragma unroll
+  for (int n = 0; n < C::kUnits; ++n) store(now, n);
+  if (first < end) load(first + C::kUnits);
+  __syncthreads();
+  // The logits of a unit are made while the one before is added up.
+  f32x4_t y[C::R][2];
+  if (active && first < end) {
+    f32x4_t s[C::R][2];
+    const bool held = mine.held(first);
+    z.logits(Staged<D>{now + lane * 16}, s);
+    if (!z.whole(first * 32, held)) z.mask(s, first * 32, held);
+    if (z.exponents(s, y)) z.raise(s, y);
+  }
+  for (int tile = first; tile < end; tile += C::kUnits) {
+#pragma unroll
+    for (int n = 0; n < C::kUnits; ++n) {
+      const bool last = n == C::kUnits - 1;
+      if (last) {
+        if (C::kUnits == 1) store(next, 0);
+        load(tile + 2 * C::kUnits);
+        __syncthreads();
+      }
+      const int u = tile + n;
+      if (active && u < end) {
+        const Staged<D> at = {now + n * Staged<D>::kBytes + lane * 16};
+        const Staged<D> after = {(last ? next : now + (n + 1) * Staged<D>::kBytes) + lane * 16};
+        const bool held = u + 1 < end && mine.held(u + 1);  // past the end: what lies there is masked
+        f16x8_t pr[C::R];
+        f32x4_t s[C::R][2];
+        z.probabilities(y, pr);
+        z.logits(after, s);
+        z.add(at, pr);
+        if (!last) store(next, n);
+        if (!z.whole(u * 32 + 32, held)) z.mask(s, u * 32 + 32, held);
+        if (z.exponents(s, y)) z.raise(s, y);
+      } else if (!last) {
+        store(next, n);
+      }
+    }
+    uint8_t* const done = now;
+    now = next;
+    next = spare;
+    spare = done;
+  }
+
+  z.finish();
+  const float vs = a.v_scale[head];
+  const int64_t slot = (int64_t)blockIdx.x * ROWS + wave * 16 * C::R;
+#pragma unroll
+  for (int r = 0; r < C::R; ++r) {
+    const int row = row0 + r * 16 + c;
+    if (row >= rows) continue;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < T; t += 4) {
+          const float o[4] = {z.acc[r][p][t][i], z.acc[r][p][t + 1][i], z.acc[r][p][t + 2][i], z.acc[r][p][t + 3][i]};
+          const int d = p * 128 + g * (4 * T) + i * T + t;
+          if (block_parts > 1)
+            *reinterpret_cast<float4*>(partial + (slot + r * 16 + c) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+          else
+            store_row<D, 4>(a, seq, row, head, d, o, z.m[r], z.l[r], vs);
+        }
+    if (block_parts > 1 && g == 0) stats[slot + r * 16 + c] = make_float2(z.m[r], z.l[r]);
+  }
+}
+
+// The rows of a split block, a wave each: its parts brought to one bound and
+// added, LANES lanes to a part, which reads 4 LANES elements of it (the lanes'
+// sums of 64 / LANES parts at once are added at the end).  A workgroup has D /
+// (4 LANES) neighbours that take the other elements: eight lanes to a part read
+// 64 parts in one round of loads where few blocks leave the GPU empty.
+template <int D, int ROWS, int LANES>
+__global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int least, const float* __restrict__ partial,
+                                                  const float2* __restrict__ stats) {
+  constexpr int AT_ONCE = 64 / LANES, SLICES = D / (4 * LANES);
+  const int slice = blockIdx.x % SLICES, sixteen = blockIdx.x / SLICES % (ROWS / 16), at_ = blockIdx.x / (SLICES * (ROWS / 16));
+  const int number = at_ / a.heads, head = at_ - number * a.heads;
   Item w;
   if (!find<ROWS, true>(a, parts, least, number, w)) return;
   int first, end;
   block_units<ROWS>(a, w.seq, w.local * ROWS, first, end);
   const int block_parts = (end - first + w.part_units - 1) / w.part_units;
   if (block_parts <= 1) return;
+  const int lane = threadIdx.x & 63, sub = lane / LANES, d = (slice * LANES + lane % LANES) * 4;
   const float vs = a.v_scale[head];
   const int rows = w.seq.count * a.group;
   const int64_t step = (int64_t)w.blocks * a.heads * ROWS;  // from part to part
   const int64_t slot0 = ((int64_t)(w.base + w.blocks - 1 - w.local) * a.heads + head) * ROWS;
-  for (int i = threadIdx.x / LANES; i < ROWS; i += 256 / LANES) {
-    const int row = w.local * ROWS + i, d = (threadIdx.x % LANES) * E;
+  for (int i = sixteen * 16 + (threadIdx.x >> 6); i < sixteen * 16 + 16; i += blockDim.x >> 6) {
+    const int row = w.local * ROWS + i;
     if (row >= rows) break;
-    float m = kLow, l = 0.0f, o[E] = {};
-    for (int n = 0; n < block_parts; ++n) m = fmaxf(m, stats[slot0 + n * step + i].x);
-    for (int n = 0; n < block_parts; ++n) {
-      const float2 z = stats[slot0 + n * step + i];
-      const float f = __builtin_amdgcn_exp2f(z.x - m);
-      const float4* src = reinterpret_cast<const float4*>(partial + (slot0 + n * step + i) * D + d);
-      const float4 x = src[0], y = src[1];
-      l = __builtin_fmaf(z.y, f, l);
-      o[0] = __builtin_fmaf(x.x, f, o[0]);
-      o[1] = __builtin_fmaf(x.y, f, o[1]);
-      o[2] = __builtin_fmaf(x.z, f, o[2]);
-      o[3] = __builtin_fmaf(x.w, f, o[3]);
-      o[4] = __builtin_fmaf(y.x, f, o[4]);
-      o[5] = __builtin_fmaf(y.y, f, o[5]);
-      o[6] = __builtin_fmaf(y.z, f, o[6]);
-      o[7] = __builtin_fmaf(y.w, f, o[7]);
+    const float2* st = stats + slot0 + i;
+    const float* src = partial + (slot0 + i) * D + d;
+    float m = kLow;
+    for (int n = lane; n < block_parts; n += 64) m = fmaxf(m, st[n * step].x);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
+    float l = 0.0f, o[4] = {};
+    for (int n0 = 0; n0 < block_parts; n0 += 64) {
+      const int count = min(64, block_parts - n0);
+      float f = 0.0f;
+      if (lane < count) {
+        const float2 z = st[(n0 + lane) * step];
+        f = __builtin_amdgcn_exp2f(z.x - m);
+        l = __builtin_fmaf(z.y, f, l);
+      }
+      for (int n = sub; n - sub < count; n += 8 * AT_ONCE) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // past the last part: that one again, with a weight of 0
+          const float weight = __shfl(f, (n + k * AT_ONCE) & 63, 64);
+          const float used = n + k * AT_ONCE < count ? weight : 0.0f;
+          const float4 x = *reinterpret_cast<const float4*>(src + (n0 + min(n + k * AT_ONCE, count - 1)) * step * D);
+          o[0] = __builtin_fmaf(x.x, used, o[0]);
+          o[1] = __builtin_fmaf(x.y, used, o[1]);
+          o[2] = __builtin_fmaf(x.z, used, o[2]);
+          o[3] = __builtin_fmaf(x.w, used, o[3]);
+        }
+      }
     }
-    store_row<D, E>(a, w.seq, row, head, d, o, m, l, vs);
+    l = wave_sum(l);
+#pragma unroll
+    for (int k = 32; k >= LANES; k >>= 1)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[x] += __shfl_xor(o[x], k, 64);
+    if (sub == 0) store_row<D, 4>(a, w.seq, row, head, d, o, m, l, vs);
   }
 }
 
-constexpr int kLeastUnits = 8;  // units of a part at least: two for each wave
+#ifndef KV_GOAL
+#define KV_GOAL 512
+#endif
+#ifndef KV_LEAST
+#define KV_LEAST 16
+#endif
+#ifndef KV_TGOAL
+#define KV_TGOAL 512
+#endif
+#ifndef KV_TLEAST
+#define KV_TLEAST 16
+#endif
+#ifndef KV_JW
+#define KV_JW 16
+#endif
+constexpr int kLeastUnits = KV_LEAST;
+
+int plan_rows(const KvPlan& p, int head_dim) {
+  return p.tiles ? 16 * p.tiles : head_dim == 256 ? Tiles<256>::kRows : head_dim == 128 ? Tiles<128>::kRows : Tiles<64>::kRows;
+}
 
 int64_t rows_blocks(int64_t sequences, int64_t tokens, int64_t group, int rows, bool one_each) {
   if (one_each) return sequences * ((group + rows - 1) / rows);
   return (tokens * group + sequences * (rows - 1)) / rows;  // at most so many partly filled ones
 }
 
+template <int D, int ROWS>
+void join_parts(const KvAttend& a, const KvPlan& p, int least, const float* partial, const float2* stats,
+                hipStream_t stream) {
+  if (p.parts == 0) return;
+  const unsigned blocks = (unsigned)(p.blocks * a.heads) * (ROWS / 16);
+  const unsigned waves = a.starts ? KV_JW : (unsigned)(a.group < 16 ? a.group : 16);
+  if (blocks <= 128)
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, 8>), dim3(blocks * (D / 32)), dim3(64 * waves), 0, stream, a, p.parts, least,
+                       partial, stats);
+  else
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, D / 4>), dim3(blocks), dim3(64 * waves), 0, stream, a, p.parts, least, partial,
+                       stats);
+}
+
 template <int D, int R>
-hipError_t run(const KvAttend& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  const int64_t items = p.blocks + p.parts;
-  float* partial = static_cast<float*>(workspace);
-  float2* stats = reinterpret_cast<float2*>(partial + items * a.heads * 16 * R * D);
-  hipLaunchKernelGGL((k_kv_rows<D, R>), dim3((unsigned)(items * a.heads)), dim3(256), 0, stream, a, p.parts, kLeastUnits,
-                     partial, stats);
-  if (p.parts > 0)
-    hipLaunchKernelGGL((k_kv_join<D, R>), dim3((unsigned)(p.blocks * a.heads)), dim3(256), 0, stream, a, p.parts,
-                       kLeastUnits, partial, stats);
+hipError_t run(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
+  hipLaunchKernelGGL((k_kv_rows<D, R>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(256), 0, stream, a,
+                     p.parts, kLeastUnits, partial, stats);
+  join_parts<D, 16 * R>(a, p, kLeastUnits, partial, stats, stream);
   return hipGetLastError();
 }
 
 template <int D>
 hipError_t pick(const KvAttend& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  return run<D, 1>(a, p, workspace, stream);
+  const int64_t slots = (p.blocks + p.parts) * a.heads * plan_rows(p, D);
+  float* partial = static_cast<float*>(workspace);
+  float2* stats = reinterpret_cast<float2*>(partial + slots * D);
+  if (p.tiles == 1) return run<D, 1>(a, p, partial, stats, stream);
+  constexpr size_t lds = 3 * Tiles<D>::kTileBytes;
+  const hipError_t e = set_lds_limit<k_kv_tiles<D>>(lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((k_kv_tiles<D>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(64 * Tiles<D>::kWaves), lds, stream, a,
+                     p.parts, KV_TLEAST, partial, stats);
+  join_parts<D, Tiles<D>::kRows>(a, p, KV_TLEAST, partial, stats, stream);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -596,10 +973,15 @@ hipError_t pick(const KvAttend& a, const KvPlan& p, void* workspace, hipStream_t
 KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
                          int64_t capacity, bool one_each) {
   KvPlan p;
-  p.tiles = 1;
-  p.blocks = rows_blocks(sequences, tokens, q_heads / heads, 16 * p.tiles, one_each);
-  p.parts = capacity > kLeastUnits * 32 ? (int)((1024 + heads - 1) / heads) : 0;
-  p.ws_bytes = p.parts ? (size_t)(p.blocks + p.parts) * heads * 16 * p.tiles * (head_dim + 2) * sizeof(float) : 0;
+  const int64_t group = q_heads / heads, mean = (tokens * group + sequences - 1) / sequences;  // rows of a sequence
+  p.tiles = mean <= 32 ? 1 : 0;
+#ifdef KV_TILES
+  p.tiles = KV_TILES;
+#endif
+  const int rows = plan_rows(p, head_dim);
+  p.blocks = rows_blocks(sequences, tokens, group, rows, one_each);
+  p.parts = capacity > kLeastUnits * 32 && p.blocks * heads < (p.tiles ? 1024 : 256) ? (int)(((p.tiles ? KV_GOAL : KV_TGOAL) + heads - 1) / heads) : 0;
+  p.ws_bytes = p.parts ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
   return p;
 }
 
