@@ -95,7 +95,8 @@ SIGNATURES = {
                                  _c_i64, _c_int, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
     "nvfp4_kv_read": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p, _c_int,
                                _c_p]),
-    "nvfp4_kv_attention_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "nvfp4_kv_attention_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                                    _c_int]),
     "nvfp4_kv_attention": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p,
                                     _c_p, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_int, _c_i64, _c_p, _c_p, _c_p,
                                     _c_size, _c_p]),
@@ -940,12 +941,13 @@ class KVCache:
         """(pages, heads, GPU index); raises ValueError unless the fields are
         those of one cache on a GPU."""
         data, ks, vs = self.data, self.k_scale, self.v_scale
-        if (isinstance(data, torch.Tensor) and data.dim() == 2 and isinstance(ks, torch.Tensor) and ks.dim() == 1):
-            (pages, bytes_), heads, index = data.shape, ks.shape[0], data.get_device()
-            n = lib().nvfp4_kv_page_bytes(heads, self.head_dim, self.page_size)
-            if (n > 0 and n == bytes_ and _fits(data, _U8, (pages, n), index) and _fits(ks, _F32, (heads,), index)
-                    and _fits(vs, _F32, (heads,), index)):
-                return pages, heads, index
+        if isinstance(data, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(vs, torch.Tensor):
+            index, shape, heads = data.get_device(), data.shape, ks.shape
+            if (index >= 0 and data.dtype is _U8 and data.is_contiguous() and ks.dtype is _F32 and vs.dtype is _F32
+                    and len(shape) == 2 and len(heads) == 1 and vs.shape == heads and ks.get_device() == index
+                    and vs.get_device() == index and ks.is_contiguous() and vs.is_contiguous()
+                    and shape[1] == heads[0] * self.page_size * (self.head_dim + self.head_dim // 8)):
+                return shape[0], heads[0], index  # the sizes themselves: checked by the library
         if not isinstance(data, torch.Tensor) or data.dim() != 2:
             raise ValueError("cache.data must be a 2-D uint8 tensor [pages, page bytes]")
         if not isinstance(ks, torch.Tensor) or ks.dim() != 1:
@@ -972,11 +974,12 @@ def _kv_cache(cache):
 
 def _token_rows(t, name, head_dim, index, heads=None, tokens=None):
     """(tokens, heads, stride) of a bf16 [tokens, heads, head_dim] GPU tensor whose heads lie beside one another."""
-    if (not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != head_dim
-            or (heads is not None and t.shape[1] != heads) or (tokens is not None and t.shape[0] != tokens)):
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if (len(shape) != 3 or shape[2] != head_dim or (heads is not None and shape[1] != heads)
+            or (tokens is not None and shape[0] != tokens)):
         want = f"[{'tokens' if tokens is None else tokens}, {'heads' if heads is None else heads}, {head_dim}]"
-        raise ValueError(f"{name} must be a bfloat16 tensor {want}, got {tuple(getattr(t, 'shape', ()))}")
-    n, h, _ = t.shape
+        raise ValueError(f"{name} must be a bfloat16 tensor {want}, got {tuple(shape)}")
+    n, h, _ = shape
     if t.dtype is not _BF16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     stride, of_head, of_element = t.stride()
@@ -988,7 +991,8 @@ def _token_rows(t, name, head_dim, index, heads=None, tokens=None):
 
 
 def _indices(t, name, shape, index):
-    if not _fits(t, _I32, shape, index):
+    if not (isinstance(t, torch.Tensor) and t.dtype is _I32 and t.shape == shape and t.get_device() == index
+            and t.is_contiguous()):
         _need(t, name, _I32, shape, torch.device("cuda", index))
 
 
@@ -1056,9 +1060,9 @@ def kv_read(cache: KVCache, slots: torch.Tensor, dtype: torch.dtype = torch.bflo
 
 
 def kv_attention_workspace_size(sequences: int, tokens: int, q_heads: int, heads: int, head_dim: int, page_size: int,
-                                table_pages: int, one_each: bool) -> int:
+                                table_pages: int, window: int, one_each: bool) -> int:
     return int(lib().nvfp4_kv_attention_workspace_size(sequences, tokens, q_heads, heads, head_dim, page_size,
-                                                       table_pages, 1 if one_each else 0))
+                                                       table_pages, window, 1 if one_each else 0))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -1104,8 +1108,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_l
     L = lib()
     one_each = 1 if q_starts is None else 0
     ws, ws_bytes, keep = _mx_workspace(
-        workspace, L.nvfp4_kv_attention_workspace_size(b, n, q_heads, heads, d, cache.page_size, table_pages, one_each),
-        cache.data)
+        workspace, L.nvfp4_kv_attention_workspace_size(b, n, q_heads, heads, d, cache.page_size, table_pages, window,
+                                                       one_each), cache.data)
     _run(index, L.nvfp4_kv_attention, q.data_ptr(), q_stride, cache.data.data_ptr(), pages, cache.page_size, heads, d,
          cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), page_table.data_ptr(), table_pages, kv_lens.data_ptr(),
          _ptr(q_starts), b, n, q_heads, d ** -0.5 if scale is None else scale, 1 if causal else 0, window,

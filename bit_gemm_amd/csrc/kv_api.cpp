@@ -34,6 +34,7 @@ constexpr int64_t kMaxSlots = ((int64_t)1 << 31) - 1;  // slots are int32
 constexpr int64_t kMaxStride = (int64_t)1 << 40;
 constexpr int64_t kMaxTokens = (int64_t)1 << 27;
 constexpr int64_t kMaxSequences = 65536;
+constexpr int64_t kMaxRows = (int64_t)1 << 30;  // of a call of attention: numbered by int32
 constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of 256 threads: a launch stays below 2^32 work-items
 
 int page_shift(int64_t page_size) {
@@ -140,9 +141,9 @@ NVFP4_API int nvfp4_kv_append(const void* k, int64_t k_stride, const void* v, in
     return fail(NVFP4_ERR_INVALID_VALUE, "q_heads=%lld: 1 .. %lld", (long long)q_heads, (long long)kMaxHeads);
   if (rope_dim < 0 || rope_dim > head_dim || rope_dim % 32 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "rope_dim=%lld: a multiple of 32 up to head_dim", (long long)rope_dim);
-  if (rope_dim > 0 && (max_positions < 0 || max_positions > kMaxSlots))
-    return fail(NVFP4_ERR_INVALID_VALUE, "max_positions=%lld", (long long)max_positions);
   if (tokens == 0) return NVFP4_OK;
+  if (rope_dim > 0 && (max_positions <= 0 || max_positions > kMaxSlots))
+    return fail(NVFP4_ERR_INVALID_VALUE, "max_positions=%lld: 1 .. 2^31 - 1", (long long)max_positions);
   const int64_t kw = heads * head_dim, qw = q ? q_heads * head_dim : 0;
   if ((st = check_rows(k, k_stride, kw, "k")) || (st = check_rows(v, v_stride, kw, "v"))) return st;
   if (q && ((st = check_rows(q, q_stride, qw, "q")) || (st = check_rows(q_out, q_out_stride, qw, "q_out")))) return st;
@@ -205,7 +206,7 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
   if (!slots || !k || !v) return fail(NVFP4_ERR_INVALID_VALUE, "slots, k and v are required");
   if (!aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16))
     return fail(NVFP4_ERR_MISALIGNED, "k and v must be 16-byte aligned, slots 4-byte aligned");
-  if (nvfp4::kv_read_workgroups(tokens, heads, (int)head_dim) >= kMaxGroups)
+  if (nvfp4::kv_read_workgroups(tokens, heads, (int)head_dim, out_dtype == NVFP4_F32) >= kMaxGroups)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld heads in one call", (long long)tokens, (long long)heads);
   const int64_t bytes = tokens * heads * head_dim * (out_dtype == NVFP4_F32 ? 4 : 2);
   if ((st = check_outputs({whole(k, bytes, "k"), whole(v, bytes, "v")},
@@ -221,12 +222,14 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
 
 NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
                                                    int64_t head_dim, int64_t page_size, int64_t table_pages,
-                                                   int one_each) {
+                                                   int64_t window, int one_each) {
   if (sequences <= 0 || sequences > kMaxSequences || tokens <= 0 || tokens > kMaxTokens || table_pages <= 0 ||
       !cache_sizes_ok(heads, head_dim, page_size) || table_pages > kMaxSlots / page_size || q_heads <= 0 ||
-      q_heads > kMaxHeads || q_heads % heads != 0 || (one_each && sequences != tokens))
+      q_heads > kMaxHeads || q_heads % heads != 0 || window < 0 ||
+      tokens * q_heads > kMaxRows || (one_each && sequences != tokens))
     return 0;
-  return nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim, table_pages * page_size, one_each != 0)
+  return nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim, table_pages * page_size, window,
+                                  one_each != 0)
       .ws_bytes;
 }
 
@@ -252,6 +255,9 @@ NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t*
   if (!q_starts && tokens != sequences)
     return fail(NVFP4_ERR_INVALID_VALUE, "without q_starts each sequence has one token: %lld tokens, %lld sequences",
                 (long long)tokens, (long long)sequences);
+  if (tokens * q_heads > kMaxRows)
+    return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld query heads in one call", (long long)tokens,
+                (long long)q_heads);
   if (tokens == 0 || sequences == 0) return NVFP4_OK;
   if ((st = check_rows(q, q_stride, q_heads * head_dim, "q"))) return st;
   if (!kv_lens || !out || (table_pages > 0 && !page_table))
@@ -260,7 +266,7 @@ NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t*
     return fail(NVFP4_ERR_MISALIGNED, "out must be 16-byte aligned, page_table, kv_lens, q_starts and lse 4-byte aligned");
   if (pages == 0 && table_pages > 0) return fail(NVFP4_ERR_INVALID_VALUE, "a page table without pages");
   const nvfp4::KvPlan plan = nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim,
-                                                      table_pages * page_size, q_starts == nullptr);
+                                                      table_pages * page_size, window, q_starts == nullptr);
   if ((plan.blocks + plan.parts) * heads >= kMaxGroups)
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld heads in one call", (long long)tokens,
                 (long long)q_heads);

@@ -20,6 +20,8 @@
 //  k_kv_rows  a workgroup of 4 waves per row block, head and part of the
 //             context; a wave takes every fourth unit of 32 tokens
 //  k_kv_join  adds the parts of the rows whose context was split
+#include <algorithm>
+
 #include "kv_device.h"
 
 namespace nvfp4 {
@@ -646,83 +648,67 @@ __global__ __launch_bounds__(256, 2) void k_kv_rows(KvAttend a, int parts, int l
 }
 
 // Operands in LDS, 1 KiB each in the lanes' order; a panel's are the keys of
-// half 0 and 1, the even and the odd tiles of its values, N of each.
+// half 0 and 1, the even and the odd tiles of its values, four of each.
 template <int D>
 struct Staged {
-  static constexpr int P = Unit<D>::P, N = D == 64 ? 2 : 4;
-  static constexpr int kBytes = P * 4 * N * 1024;  // of a unit
+  static constexpr int kBytes = Unit<D>::P * 16 * 1024;  // of a unit
   const uint8_t* at;  // the lane's 16 bytes of the unit's first operand
   __device__ __forceinline__ f16x8_t key(int p, int h, int n) const {
-    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + h) * N + n) * 1024);
+    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + h) * 4 + n) * 1024);
   }
   __device__ __forceinline__ f16x8_t value(int p, int t) const {
-    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + 2 + (t & 1)) * N + (t >> 1)) * 1024);
+    return *reinterpret_cast<const f16x8_t*>(at + ((p * 4 + 2 + (t & 1)) * 4 + (t >> 1)) * 1024);
   }
 };
 
 // A wave's share of a unit's way into LDS: 4 p + 0, 1 the keys of half 0, 1 of
-// panel p, 4 p + 2, 3 the even, odd tiles of its values; N operands.
+// panel p, 4 p + 2, 3 the even, odd tiles of its values; four operands.
 template <int D>
 struct Share {
-  static constexpr int N = D == 64 ? 2 : 4, kCount = 4 * Unit<D>::P;
+  static constexpr int kCount = 4 * Unit<D>::P;
   u32x4_t a, b;
   uint2 s;
 
+  // Keys take 16 bytes and one word of scales: the rest is read for nothing instead of a branch.
   __device__ __forceinline__ void load(const uint8_t* u, int share, int lane) {
     const int p = share >> 2, kind = share & 3;
     const bool key = kind < 2;
-    if constexpr (D == 64) {
-      a = *reinterpret_cast<const u32x4_t*>(u + (key ? 0 : KvUnit<D>::kValues) + lane * 16);
-      if (key)
-        s.x = *reinterpret_cast<const uint16_t*>(u + KvUnit<D>::kKeyScales + lane * 2);
-      else
-        s = *reinterpret_cast<const uint2*>(u + KvUnit<D>::kValueScales + (lane >> 4) * 32 + ((lane & 15) >> 2) * 8);
-    } else {  // keys: 16 bytes and one word of scales, the rest read for nothing instead of a branch
-      a = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues)) + lane * 16);
-      b = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues + 1024)) + lane * 16);
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(
-          u + (p * 256 + (key ? KvUnit<D>::kKeyScales : KvUnit<D>::kValueScales)) + (key ? lane * 4 : (lane >> 1) * 8));
-      s.x = w[0];
-      s.y = w[1];
-    }
+    a = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues)) + lane * 16);
+    b = *reinterpret_cast<const u32x4_t*>(u + (p * 2048 + (key ? kind * 1024 : KvUnit<D>::kValues + 1024)) + lane * 16);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(
+        u + (p * 256 + (key ? KvUnit<D>::kKeyScales : KvUnit<D>::kValueScales)) + (key ? lane * 4 : (lane >> 1) * 8));
+    s.x = w[0];
+    s.y = w[1];
   }
-  // Operands [from, until), without branches, to be scheduled among matrix instructions.
-  __device__ __forceinline__ void store(uint8_t* to, int share, int from, int until) const {
+  // Without branches, to be scheduled among matrix instructions.
+  __device__ __forceinline__ void store(uint8_t* to, int share) const {
     const int kind = share & 3;
     const bool key = kind < 2;
     const uint32_t low = key ? 0xFFFFFFFFu : 0x0F0F0F0Fu;  // bits that come from the first of two words
     const int right = kind == 3 ? 4 : 0, left = kind == 2 ? 4 : 0;
-    uint32_t w[4] = {};
-    if constexpr (D == 64) {
-      w[0] = ((kind == 1 ? a[2] : a[0]) >> right & low) | (a[1] << left & ~low);
-      w[1] = ((key ? (kind ? a[3] : a[1]) : a[2]) >> right & low) | (a[3] << left & ~low);
-    } else {
-      w[0] = (a[0] >> right & low) | (a[1] << left & ~low);
-      w[1] = ((key ? a[1] : a[2]) >> right & low) | (a[3] << left & ~low);
-      w[2] = ((key ? a[2] : b[0]) >> right & low) | (b[1] << left & ~low);
-      w[3] = ((key ? a[3] : b[2]) >> right & low) | (b[3] << left & ~low);
-    }
+    const uint32_t w[4] = {(a[0] >> right & low) | (a[1] << left & ~low),
+                           ((key ? a[1] : a[2]) >> right & low) | (a[3] << left & ~low),
+                           ((key ? a[2] : b[0]) >> right & low) | (b[1] << left & ~low),
+                           ((key ? a[3] : b[2]) >> right & low) | (b[3] << left & ~low)};
     f16x2_t gk[4], gv[4], g[4];
-    key_scales<D>(kind & 1 ? s.x >> (D == 64 ? 8 : 16) : s.x, 0, gk);
+    key_scales<D>(kind & 1 ? s.x >> 16 : s.x, 0, gk);
     value_scales(s, gv);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       g[i] = __builtin_bit_cast(f16x2_t, key ? __builtin_bit_cast(uint32_t, gk[i]) : __builtin_bit_cast(uint32_t, gv[i]));
     const float f = key ? 1.0f : 256.0f;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
-      if (n >= from && n < until) *reinterpret_cast<f16x8_t*>(to + (share * N + n) * 1024) = operand<D>(w, g, n, f);
+    for (int n = 0; n < 4; ++n) *reinterpret_cast<f16x8_t*>(to + (share * 4 + n) * 1024) = operand<D>(w, g, n, f);
   }
 };
 
 // Many rows: 16 R for each of 8 waves, which decode tiles of kUnits units
-// together into LDS operands.
+// together into LDS operands, a share of a unit each.
 template <int D>
 struct Tiles {
   static constexpr int kWaves = 8, R = D == 256 ? 1 : 2, kRows = kWaves * 16 * R;
-  static constexpr int kUnits = D == 64 ? 4 : D == 128 ? 2 : 1;
-  static constexpr int kShares = kUnits * Share<D>::kCount / kWaves;  // of a wave
-  static_assert(kShares > 0 && kShares * kWaves == kUnits * Share<D>::kCount, "every operand has a wave");
+  static constexpr int kUnits = D == 256 ? 1 : 2;
+  static_assert(kUnits * Share<D>::kCount == kWaves, "a share for each wave");
   static constexpr int kTileBytes = kUnits * Staged<D>::kBytes;
 };
 
@@ -731,7 +717,7 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
                                                      float2* __restrict__ stats) {
   using C = Tiles<D>;
   using X = Rows<D, C::R>;
-  constexpr int P = X::P, N = X::N, T = X::T, ROWS = C::kRows;
+  constexpr int P = X::P, T = X::T, ROWS = C::kRows;
   extern __shared__ __align__(16) uint8_t s_kv[];  // three tiles
 
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
@@ -746,25 +732,10 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   const bool active = row0 < rows;
 
   Units<D> ahead(a, w.index, head), mine(a, w.index, head);
-  Share<D> x[C::kShares];
-  auto load = [&](int tile) {
-#pragma unroll
-    for (int n = 0; n < C::kShares; ++n) {
-      const int at = wave * C::kShares + n;
-      x[n].load(ahead.at(min(tile + at / Share<D>::kCount, end - 1)), at % Share<D>::kCount, lane);
-    }
-  };
-  // Piece n of the wave's operands, of as many as there are units before the
-  // last; past the end: of what the registers hold, never used.
-  auto store = [&](uint8_t* to, int n) {
-    constexpr int all = C::kShares * N, pieces = C::kUnits > 1 ? C::kUnits - 1 : 1, each = (all + pieces - 1) / pieces;
-#pragma unroll
-    for (int i = 0; i < C::kShares; ++i) {
-      const int at = wave * C::kShares + i;
-      x[i].store(to + at / Share<D>::kCount * Staged<D>::kBytes + lane * 16, at % Share<D>::kCount, n * each - i * N,
-                 (n + 1) * each - i * N);
-    }
-  };
+  Share<D> x;
+  const int share = wave % Share<D>::kCount, share_of = wave / Share<D>::kCount;  // of unit share_of of a tile
+  auto load = [&](int tile) { x.load(ahead.at(min(tile + share_of, end - 1)), share, lane); };
+  auto store = [&](uint8_t* to) { x.store(to + share_of * Staged<D>::kBytes + lane * 16, share); };
   // While tile i is multiplied, tile i + 1 is decoded into the next of three
   // buffers and tile i + 2 is on its way from memory.  The one barrier of a
   // turn stands before the first use of tile i + 1; the buffer that a turn
@@ -773,8 +744,7 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   if (first < end) load(first);
   X z;
   z.start(a, seq, min(row0, rows - 1), head);
-#pragma unroll
-  for (int n = 0; n < C::kUnits; ++n) store(now, n);
+  store(now);
   if (first < end) load(first + C::kUnits);
   __syncthreads();
   // The logits of a unit are made while the one before is added up.
@@ -791,7 +761,7 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
     for (int n = 0; n < C::kUnits; ++n) {
       const bool last = n == C::kUnits - 1;
       if (last) {
-        if (C::kUnits == 1) store(next, 0);
+        if (C::kUnits == 1) store(next);
         load(tile + 2 * C::kUnits);
         __syncthreads();
       }
@@ -805,11 +775,11 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
         z.probabilities(y, pr);
         z.logits(after, s);
         z.add(at, pr);
-        if (!last) store(next, n);
+        if (!last) store(next);
         if (!z.whole(u * 32 + 32, held)) z.mask(s, u * 32 + 32, held);
         if (z.exponents(s, y)) z.raise(s, y);
       } else if (!last) {
-        store(next, n);
+        store(next);
       }
     }
     uint8_t* const done = now;
@@ -905,91 +875,95 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
   }
 }
 
-#ifndef KV_GOAL
-#define KV_GOAL 512
-#endif
-#ifndef KV_LEAST
-#define KV_LEAST 16
-#endif
-#ifndef KV_TGOAL
-#define KV_TGOAL 512
-#endif
-#ifndef KV_TLEAST
-#define KV_TLEAST 16
-#endif
-#ifndef KV_JW
-#define KV_JW 16
-#endif
-constexpr int kLeastUnits = KV_LEAST;
+// Parts: two work items for each CU beside the blocks, none of fewer than 16
+// units (four for each wave).  One token on 131072 of 8 heads takes 46 us with
+// one item for each CU, 41 with two, 41 with three, whose parts take longer to
+// join; 16 ragged contexts 25.5, 24.5, 25.
+constexpr int kItems = 512, kLeastUnits = 16;
 
-int plan_rows(const KvPlan& p, int head_dim) {
-  return p.tiles ? 16 * p.tiles : head_dim == 256 ? Tiles<256>::kRows : head_dim == 128 ? Tiles<128>::kRows : Tiles<64>::kRows;
-}
+int block_rows(int tiles, int head_dim) { return tiles ? 16 * tiles : head_dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows; }
 
-int64_t rows_blocks(int64_t sequences, int64_t tokens, int64_t group, int rows, bool one_each) {
+int64_t block_count(int64_t sequences, int64_t tokens, int64_t group, int rows, bool one_each) {
   if (one_each) return sequences * ((group + rows - 1) / rows);
   return (tokens * group + sequences * (rows - 1)) / rows;  // at most so many partly filled ones
 }
 
 template <int D, int ROWS>
-void join_parts(const KvAttend& a, const KvPlan& p, int least, const float* partial, const float2* stats,
-                hipStream_t stream) {
+void join_parts(const KvAttend& a, const KvPlan& p, const float* partial, const float2* stats, hipStream_t stream) {
   if (p.parts == 0) return;
   const unsigned blocks = (unsigned)(p.blocks * a.heads) * (ROWS / 16);
-  const unsigned waves = a.starts ? KV_JW : (unsigned)(a.group < 16 ? a.group : 16);
+  const unsigned waves = a.starts ? 16 : (unsigned)(a.group < 16 ? a.group : 16);
   if (blocks <= 128)
-    hipLaunchKernelGGL((k_kv_join<D, ROWS, 8>), dim3(blocks * (D / 32)), dim3(64 * waves), 0, stream, a, p.parts, least,
-                       partial, stats);
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, 8>), dim3(blocks * (D / 32)), dim3(64 * waves), 0, stream, a, p.parts,
+                       kLeastUnits, partial, stats);
   else
-    hipLaunchKernelGGL((k_kv_join<D, ROWS, D / 4>), dim3(blocks), dim3(64 * waves), 0, stream, a, p.parts, least, partial,
-                       stats);
+    hipLaunchKernelGGL((k_kv_join<D, ROWS, D / 4>), dim3(blocks), dim3(64 * waves), 0, stream, a, p.parts, kLeastUnits,
+                       partial, stats);
 }
 
 template <int D, int R>
-hipError_t run(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
+hipError_t run_rows(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
   hipLaunchKernelGGL((k_kv_rows<D, R>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(256), 0, stream, a,
                      p.parts, kLeastUnits, partial, stats);
-  join_parts<D, 16 * R>(a, p, kLeastUnits, partial, stats, stream);
+  join_parts<D, 16 * R>(a, p, partial, stats, stream);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t pick(const KvAttend& a, const KvPlan& p, void* workspace, hipStream_t stream) {
-  const int64_t slots = (p.blocks + p.parts) * a.heads * plan_rows(p, D);
-  float* partial = static_cast<float*>(workspace);
-  float2* stats = reinterpret_cast<float2*>(partial + slots * D);
-  if (p.tiles == 1) return run<D, 1>(a, p, partial, stats, stream);
+hipError_t run_tiles(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
   constexpr size_t lds = 3 * Tiles<D>::kTileBytes;
   const hipError_t e = set_lds_limit<k_kv_tiles<D>>(lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_kv_tiles<D>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(64 * Tiles<D>::kWaves), lds, stream, a,
-                     p.parts, KV_TLEAST, partial, stats);
-  join_parts<D, Tiles<D>::kRows>(a, p, KV_TLEAST, partial, stats, stream);
+  hipLaunchKernelGGL((k_kv_tiles<D>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(512), lds, stream, a,
+                     p.parts, kLeastUnits, partial, stats);
+  join_parts<D, Tiles<D>::kRows>(a, p, partial, stats, stream);
   return hipGetLastError();
 }
 
 }  // namespace
 
 KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
-                         int64_t capacity, bool one_each) {
+                         int64_t capacity, int64_t window, bool one_each) {
   KvPlan p;
-  const int64_t group = q_heads / heads, mean = (tokens * group + sequences - 1) / sequences;  // rows of a sequence
-  p.tiles = mean <= 32 ? 1 : 0;
-#ifdef KV_TILES
-  p.tiles = KV_TILES;
-#endif
-  const int rows = plan_rows(p, head_dim);
-  p.blocks = rows_blocks(sequences, tokens, group, rows, one_each);
-  p.parts = capacity > kLeastUnits * 32 && p.blocks * heads < (p.tiles ? 1024 : 256) ? (int)(((p.tiles ? KV_GOAL : KV_TGOAL) + heads - 1) / heads) : 0;
-  p.ws_bytes = p.parts ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
+  const int64_t group = q_heads / heads;
+  int64_t units = (capacity + 31) / 32;  // of a context, at most
+  if (window > 0) units = std::min(units, (window + 31) / 32 + 2);
+  // Blocks of 32 rows times the units that each may see.  Work enough to fill
+  // the GPU with fewer, larger workgroups takes them.  1000 tokens of 32 heads
+  // in groups of 4, head_dim 128: 29 us with blocks of 16 rows, 35 with 32, 52
+  // in tiles; 2000: 75, 62, 73; 4096: 252, 192, 160.  Head_dim 64 has no
+  // tiles: 4000 tokens of 16 heads 78, 59, 106 us, 16000 of 32 1017, 723, 809.
+  // Head_dim 256 has no room for 32 rows: 1500 tokens of 16 heads in groups of
+  // 4 take 48 us with 16 rows, 73 in tiles, 4096 tokens 242 and 177.
+  const double work = (double)block_count(sequences, tokens, group, 32, one_each) * (double)heads * (double)units;
+  const bool few = tokens * group <= 32 * sequences;
+  if (!few && ((head_dim == 256 && work >= 65536.0) || (head_dim == 128 && work >= 262144.0)))
+    p.tiles = 0;
+  else
+    p.tiles = !few && head_dim < 256 && work >= 32768.0 ? 2 : 1;
+  const int rows = block_rows(p.tiles, head_dim);
+  p.blocks = block_count(sequences, tokens, group, rows, one_each);
+  // The second launch takes 4 to 6 us, what a workgroup needs for 32 units.  One
+  // sequence of 1024 tokens of 8 heads: 9.2 us whole, 9.6 split; of 2048 14.4,
+  // 10.9; 32 of 1024 12.6, 17; 32 of 2048 21.9, 24.6.
+  const int64_t items = p.blocks * heads;
+  const bool split = units > (items < 192 ? 32 : 64) && items < (p.tiles ? 1024 : 256);
+  p.parts = split ? (int)((kItems + heads - 1) / heads) : 0;
+  p.ws_bytes = split ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
   return p;
 }
 
-hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& plan, void* workspace,
-                               hipStream_t stream) {
-  if (head_dim == 64) return pick<64>(a, plan, workspace, stream);
-  if (head_dim == 128) return pick<128>(a, plan, workspace, stream);
-  return pick<256>(a, plan, workspace, stream);
+hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& p, void* workspace, hipStream_t stream) {
+  const int64_t slots = (p.blocks + p.parts) * a.heads * block_rows(p.tiles, head_dim);
+  float* partial = static_cast<float*>(workspace);
+  float2* stats = reinterpret_cast<float2*>(partial + slots * head_dim);
+  if (head_dim == 64)
+    return p.tiles == 1 ? run_rows<64, 1>(a, p, partial, stats, stream) : run_rows<64, 2>(a, p, partial, stats, stream);
+  if (head_dim == 128)
+    return p.tiles == 1   ? run_rows<128, 1>(a, p, partial, stats, stream)
+           : p.tiles == 2 ? run_rows<128, 2>(a, p, partial, stats, stream)
+                          : run_tiles<128>(a, p, partial, stats, stream);
+  return p.tiles == 1 ? run_rows<256, 1>(a, p, partial, stats, stream) : run_tiles<256>(a, p, partial, stats, stream);
 }
 
 }  // namespace nvfp4

@@ -40,8 +40,8 @@ __device__ __forceinline__ void store16(uint16_t* p, const float* v) {
   uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  store_u4_stream(p, w[0], w[1], w[2], w[3]);
+  store_u4_stream(p + 8, w[4], w[5], w[6], w[7]);
 }
 
 // The elements of a thread: two blocks of 16.  A rotation of half the rotated
@@ -58,46 +58,44 @@ __device__ __forceinline__ Blocks blocks_of(int pair, int rot, bool halves) {
   return {2 * pair, 2 * pair + 1, false};
 }
 
-// Rotates the blocks x, y of one head by the angles at cs (rot / 2 cosines,
-// then as many sines); NULL: a position outside the table, every angle NaN.
+// The 16 angles that a thread's blocks x, y of any head turn by.
+struct Angles {
+  float c[16], s[16];
+};
+
 template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate(float* x, float* y, const Blocks& at, const float* cs, int rot) {
-  const float nan = __builtin_nanf("");
-  if constexpr (INTERLEAVED) {
+__device__ __forceinline__ bool turns(const Blocks& at, int rot) {
+  return INTERLEAVED ? at.b0 < rot >> 4 : at.split;
+}
+
+// From the position's row of the table: rot / 2 cosines, then as many sines;
+// a position outside the table turns by NaN.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void load_angles(const KvAppend& a, const Blocks& at, int pos, Angles& t) {
+  const bool known = pos >= 0 && pos < a.max_positions;
+  // interleaved: 8 pairs of each block, neighbouring ones; a rotated b0 has a rotated b1 (rot is a multiple of 32)
+  const float* p = a.rope + (int64_t)(known ? pos : 0) * a.rot + (INTERLEAVED ? at.b0 * 8 : at.b0 * 16);
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int b = n ? at.b1 : at.b0;
-      float* z = n ? y : x;
-      if (b >= rot >> 4) continue;
+  for (int i = 0; i < 16; i += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(p + i);
+    const float4 s = *reinterpret_cast<const float4*>(p + (a.rot >> 1) + i);
+    t.c[i] = c.x, t.c[i + 1] = c.y, t.c[i + 2] = c.z, t.c[i + 3] = c.w;
+    t.s[i] = s.x, t.s[i + 1] = s.y, t.s[i + 2] = s.z, t.s[i + 3] = s.w;
+  }
+  if (!known) {  // both products of a pair hold the cosine
 #pragma unroll
-      for (int i = 0; i < 8; i += 4) {
-        const float4 c = cs ? *reinterpret_cast<const float4*>(cs + b * 8 + i) : make_float4(nan, nan, nan, nan);
-        const float4 s =
-            cs ? *reinterpret_cast<const float4*>(cs + (rot >> 1) + b * 8 + i) : make_float4(nan, nan, nan, nan);
-        const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+    for (int i = 0; i < 16; ++i) t.c[i] = __builtin_nanf("");
+  }
+}
+
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate(float* x, float* y, const Angles& t) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = z[2 * (i + j)], e = z[2 * (i + j) + 1];
-          z[2 * (i + j)] = a * cv[j] - e * sv[j];
-          z[2 * (i + j) + 1] = e * cv[j] + a * sv[j];
-        }
-      }
-    }
-  } else {
-    if (!at.split) return;
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      const float4 c = cs ? *reinterpret_cast<const float4*>(cs + at.b0 * 16 + i) : make_float4(nan, nan, nan, nan);
-      const float4 s =
-          cs ? *reinterpret_cast<const float4*>(cs + (rot >> 1) + at.b0 * 16 + i) : make_float4(nan, nan, nan, nan);
-      const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = x[i + j], e = y[i + j];
-        x[i + j] = a * cv[j] - e * sv[j];
-        y[i + j] = e * cv[j] + a * sv[j];
-      }
-    }
+  for (int i = 0; i < 16; ++i) {
+    float &a = INTERLEAVED ? (i < 8 ? x : y)[2 * (i & 7)] : x[i], &b = INTERLEAVED ? (i < 8 ? x : y)[2 * (i & 7) + 1] : y[i];
+    const float a0 = a, b0 = b;
+    a = a0 * t.c[i] - b0 * t.s[i];
+    b = b0 * t.c[i] + a0 * t.s[i];
   }
 }
 
@@ -149,7 +147,11 @@ __device__ __forceinline__ void store_value(uint8_t* unit, int t, int b, uint2 c
 // Workgroups [0, kv_groups) write the cache: D / 16 neighbouring lanes hold
 // one token's key and value of one head, tokens of a head beside one another
 // (their bytes of a unit share cache lines).  The other workgroups rotate
-// queries.
+// queries.  A token that is left out is computed and not stored, so that its
+// inputs are asked for beside its slot and not after it.  Bound by bandwidth:
+// 4096 tokens of 32 heads each of q, k and v take 35 us (153 MB, 4.4 TB/s), one
+// token 3.5.  Threads that turn two or four heads by the angles they read once
+// take 34 us for the 4096 tokens, and 4.2 and 6 for one.
 template <int D, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
   constexpr int kPairs = D / 32;
@@ -158,17 +160,18 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
     const uint32_t row = i / kPairs;  // token, query head
     const uint32_t token = row / (uint32_t)a.q_heads, head = row - token * (uint32_t)a.q_heads;
     if (token >= (uint32_t)a.tokens) return;
-    const int slot = a.slots[token];
-    if (slot < 0 || slot >= a.slot_limit) return;
+    const int slot = a.slots[token], pos = a.rot ? a.positions[token] : 0;
     const Blocks at = blocks_of(i % kPairs, a.rot, !INTERLEAVED);
     const uint16_t* q = a.q + (int64_t)token * a.q_stride + head * D;
     float x[16], y[16];
     load16(q + at.b0 * 16, x);
     load16(q + at.b1 * 16, y);
-    if (a.rot) {
-      const int pos = a.positions[token];
-      rotate<INTERLEAVED>(x, y, at, pos >= 0 && pos < a.max_positions ? a.rope + (int64_t)pos * a.rot : nullptr, a.rot);
+    if (turns<INTERLEAVED>(at, a.rot)) {
+      Angles t;
+      load_angles<INTERLEAVED>(a, at, pos, t);
+      rotate<INTERLEAVED>(x, y, t);
     }
+    if (slot < 0 || slot >= a.slot_limit) return;
     uint16_t* o = a.q_out + (int64_t)token * a.q_out_stride + head * D;
     store16(o + at.b0 * 16, x);
     store16(o + at.b1 * 16, y);
@@ -178,8 +181,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
   const uint32_t row = i / (2 * kPairs), part = i % (2 * kPairs);
   const uint32_t head = row / (uint32_t)a.tokens, token = row - head * (uint32_t)a.tokens;
   if (head >= (uint32_t)a.heads) return;
-  const int slot = a.slots[token];
-  if (slot < 0 || slot >= a.slot_limit) return;
+  const int slot = a.slots[token], pos = a.rot ? a.positions[token] : 0;
   const bool value = part >= kPairs;
   const Blocks at = blocks_of(part % kPairs, value ? 0 : a.rot, !INTERLEAVED);
   const uint16_t* p =
@@ -187,9 +189,11 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
   float x[16], y[16];
   load16(p + at.b0 * 16, x);
   load16(p + at.b1 * 16, y);
-  if (!value && a.rot) {
-    const int pos = a.positions[token];
-    rotate<INTERLEAVED>(x, y, at, pos >= 0 && pos < a.max_positions ? a.rope + (int64_t)pos * a.rot : nullptr, a.rot);
+  const float s = (value ? a.v_scale : a.k_scale)[head];
+  if (!value && turns<INTERLEAVED>(at, a.rot)) {
+    Angles t;
+    load_angles<INTERLEAVED>(a, at, pos, t);
+    rotate<INTERLEAVED>(x, y, t);
   }
   // A token whose key or value holds an infinity or a NaN is NaN as a whole:
   // NaN key scales, zero values.  Values in the cache are always finite, so a
@@ -197,13 +201,13 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
   const uint64_t lanes = __ballot(!(finite16(x) && finite16(y)));
   const int first = (threadIdx.x & 63) & ~(2 * kPairs - 1);
   const bool poisoned = ((lanes >> first) & ((1ull << (2 * kPairs)) - 1)) != 0;
-  const float s = value ? a.v_scale[head] : a.k_scale[head];
   uint32_t s0, s1;
   uint2 c0 = quantize16(x, s, &s0), c1 = quantize16(y, s, &s1);
   if (poisoned) {
     c0 = c1 = make_uint2(0, 0);
     s0 = s1 = value ? 0u : 0x7Fu;
   }
+  if (slot < 0 || slot >= a.slot_limit) return;
   uint8_t* unit = a.cache + kv_unit_offset<D>(slot, (int)head, a.heads, a.page_shift);
   const int t = slot & 31;
   if (value) {
@@ -215,53 +219,50 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
   }
 }
 
-// A thread per block of 16 of a token's key or value of one head.
+// A thread per 16 bytes of output: 8 elements in bf16, 4 in fp32 (neighbouring
+// lanes then store whole lines: 32768 tokens of 8 heads of 128 take 34 us, 5.1
+// TB/s; with a thread for each block of 16 they took 48).
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_read(KvRead a) {
-  constexpr int kBlocks = D / 16;
+  constexpr int E = F32 ? 4 : 8, kPieces = D / E;
   const uint32_t i = blockIdx.x * 256u + threadIdx.x;
-  const uint32_t row = i / (2 * kBlocks), part = i % (2 * kBlocks);
+  const uint32_t row = i / (2 * kPieces), part = i % (2 * kPieces);
   const uint32_t head = row / (uint32_t)a.tokens, token = row - head * (uint32_t)a.tokens;
   if (head >= (uint32_t)a.heads) return;
-  const bool value = part >= kBlocks;
-  const int b = (int)(part % kBlocks);
+  const bool value = part >= kPieces;
+  const int d = (int)(part % kPieces) * E, b = d >> 4;
   const int slot = a.slots[token];
-  float v[16] = {};
+  const float s = (value ? a.v_scale : a.k_scale)[head];
+  float v[8] = {};
   if (slot >= 0 && slot < a.slot_limit) {
     const uint8_t* unit = a.cache + kv_unit_offset<D>(slot, (int)head, a.heads, a.page_shift);
     const int t = slot & 31;
-    uint2 c;
-    uint32_t sb;
-    if (value) {
-      const uint8_t* p = unit + KvUnit<D>::value(t, b);
-      if constexpr (D == 64) {
-        c.x = *reinterpret_cast<const uint16_t*>(p) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 16) << 16;
-        c.y = *reinterpret_cast<const uint16_t*>(p + 32) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 48) << 16;
-      } else {
-        c.x = *reinterpret_cast<const uint32_t*>(p);
-        c.y = *reinterpret_cast<const uint32_t*>(p + 16);
-      }
-      sb = unit[KvUnit<D>::value_scale(t, b)];
-      if (unit[KvUnit<D>::key_scale(t, 0)] == 0x7F) sb = 0x7F;
+    // the piece's bytes: a value's lie in 4 bytes per 8 elements (2 per 4 where D is 64), 16 bytes apart
+    const uint8_t* p = value ? unit + KvUnit<D>::value(t, b) : unit + KvUnit<D>::key(t, b);
+    uint32_t c;
+    if constexpr (F32) {
+      const int step = D == 64 ? 16 * ((d >> 2) & 3) : 16 * ((d >> 3) & 1) + ((d >> 1) & 2);
+      c = *reinterpret_cast<const uint16_t*>(p + (value ? step : (d & 15) >> 1));
+    } else if (value && D == 64) {
+      p += 32 * ((d >> 3) & 1);
+      c = *reinterpret_cast<const uint16_t*>(p) | (uint32_t)*reinterpret_cast<const uint16_t*>(p + 16) << 16;
     } else {
-      c = *reinterpret_cast<const uint2*>(unit + KvUnit<D>::key(t, b));
-      sb = unit[KvUnit<D>::key_scale(t, b)];
+      c = *reinterpret_cast<const uint32_t*>(p + (value ? 16 : 4) * ((d >> 3) & 1));
     }
-    const float sigma = scale_at<kConvHw, 0>(sb), s = (value ? a.v_scale : a.k_scale)[head];
-    dequant8_f32<kConvHw>(c.x, sigma, v);
-    dequant8_f32<kConvHw>(c.y, sigma, v + 8);
+    uint32_t sb = value ? unit[KvUnit<D>::value_scale(t, b)] : unit[KvUnit<D>::key_scale(t, b)];
+    if (value && unit[KvUnit<D>::key_scale(t, 0)] == 0x7F) sb = 0x7F;
+    dequant8_f32<kConvHw>(c, scale_at<kConvHw, 0>(sb), v);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) v[j] = v[j] * s;
+    for (int j = 0; j < E; ++j) v[j] = v[j] * s;
   }
-  const int64_t at = ((int64_t)token * a.heads + head) * D + b * 16;
+  const int64_t at = ((int64_t)token * a.heads + head) * D + d;
   void* out = value ? a.v : a.k;
-  if constexpr (F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-    store16(static_cast<uint16_t*>(out) + at, v);
-  }
+  if constexpr (F32)
+    store_u4_stream(static_cast<float*>(out) + at, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                    __float_as_uint(v[3]));
+  else
+    store_u4_stream(static_cast<uint16_t*>(out) + at, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                    pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
 template <int D>
@@ -290,20 +291,20 @@ int64_t kv_append_workgroups(int64_t tokens, int64_t q_heads, int64_t heads, int
   return groups(tokens * heads * (head_dim / 16)) + groups(tokens * q_heads * (head_dim / 32));
 }
 
-int64_t kv_read_workgroups(int64_t tokens, int64_t heads, int head_dim) {
-  return groups(tokens * heads * (head_dim / 8));
+int64_t kv_read_workgroups(int64_t tokens, int64_t heads, int head_dim, int out_f32) {
+  return groups(tokens * heads * (head_dim / (out_f32 ? 2 : 4)));
 }
 
 hipError_t launch_kv_append(KvAppend a, int head_dim, hipStream_t stream) {
   a.kv_groups = (uint32_t)groups((int64_t)a.tokens * a.heads * (head_dim / 16));
-  const unsigned grid = (unsigned)kv_append_workgroups(a.tokens, a.q ? a.q_heads : 0, a.heads, head_dim);
+  const unsigned grid = (unsigned)kv_append_workgroups(a.tokens, a.q_heads, a.heads, head_dim);
   if (head_dim == 64) return append<64>(a, grid, stream);
   if (head_dim == 128) return append<128>(a, grid, stream);
   return append<256>(a, grid, stream);
 }
 
 hipError_t launch_kv_read(const KvRead& a, int head_dim, int out_f32, hipStream_t stream) {
-  const unsigned grid = (unsigned)kv_read_workgroups(a.tokens, a.heads, head_dim);
+  const unsigned grid = (unsigned)kv_read_workgroups(a.tokens, a.heads, head_dim, out_f32);
   if (head_dim == 64) return read<64>(a, out_f32, grid, stream);
   if (head_dim == 128) return read<128>(a, out_f32, grid, stream);
   return read<256>(a, out_f32, grid, stream);

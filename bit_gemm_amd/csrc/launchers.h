@@ -227,7 +227,7 @@ struct KvRead {
   void *k, *v;  // [tokens, heads, head_dim]
   int tokens, heads, page_shift, slot_limit;
 };
-int64_t kv_read_workgroups(int64_t tokens, int64_t heads, int head_dim);
+int64_t kv_read_workgroups(int64_t tokens, int64_t heads, int head_dim, int out_f32);
 hipError_t launch_kv_read(const KvRead& a, int head_dim, int out_f32, hipStream_t stream);
 
 struct KvAttend {
@@ -242,15 +242,16 @@ struct KvAttend {
   float scale;
 };
 // How a call is laid out: row blocks of 16 * tiles rows (a row: a token and a
-// query head), at most `blocks` of them for each head, and up to `parts` more
-// work items for each head from splitting long contexts (0: none is split).
+// query head; tiles 0: the blocks of k_kv_tiles), at most `blocks` of them for
+// each head, and up to `parts` more work items for each head from splitting
+// long contexts (0: none is split).  capacity: tokens of the longest context.
 struct KvPlan {
   int tiles, parts;
   int64_t blocks;
   size_t ws_bytes;
 };
 KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
-                         int64_t capacity, bool one_each);
+                         int64_t capacity, int64_t window, bool one_each);
 hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& plan, void* workspace,
                                hipStream_t stream);
 

@@ -563,8 +563,8 @@ NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const vo
  * q, q_out   device bf16 [tokens, q_heads, head_dim] likewise, or both NULL;
  *            q_out may be q with the same stride.
  * positions  device int32 [tokens]; with rope_dim > 0.
- * rope       device fp32 [max_positions, rope_dim], 16-byte aligned: rope_dim
- *            / 2 cosines, then the sines.  A position outside the table gives
+ * rope       device fp32 [max_positions, rope_dim], 16-byte aligned, at least one
+ *            row with rope_dim > 0: rope_dim / 2 cosines, then the sines.  A position outside the table gives
  *            NaN.
  * rope_dim   0 (no rotation) .. head_dim, a multiple of 32.
  * slots      a token whose slot is not in the cache (a negative one, say) is
@@ -612,7 +612,7 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  *            rows q_starts[b] .. q_starts[b + 1] - 1 of q, out and lse; a
  *            sequence may have none.  Rows behind the last sequence's are left
  *            as they were.  NULL: one token each (tokens == sequences).
- * q_heads    a multiple of heads.
+ * q_heads    a multiple of heads; tokens * q_heads <= 2^30, sequences <= 65536.
  * scale      finite.  window: >= 0; 0 (none) without causal.
  * out        device bf16 [tokens, q_heads, head_dim] (contiguous); lse device
  *            fp32 [tokens, q_heads] or NULL.
@@ -625,7 +625,7 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  */
 NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
                                                    int64_t head_dim, int64_t page_size, int64_t table_pages,
-                                                   int one_each);
+                                                   int64_t window, int one_each);
 NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t* cache, int64_t pages,
                                  int64_t page_size, int64_t heads, int64_t head_dim, const float* k_scale,
                                  const float* v_scale, const int32_t* page_table, int64_t table_pages,

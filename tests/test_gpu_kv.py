@@ -335,7 +335,7 @@ def test_workspace():
     s = Sequences(15, [3000, 10], 1, 128, 32).append()
     q = queries(2, 2, 4, 128).cuda()
     want = nv.kv_attention(q, s.cache, s.table, s.kv_lens)
-    need = nv.kv_attention_workspace_size(2, 2, 4, 1, 128, 32, s.table.shape[1], True)
+    need = nv.kv_attention_workspace_size(2, 2, 4, 1, 128, 32, s.table.shape[1], 0, True)
     assert need > 0
     ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")  # NaN where nothing is written
     assert torch.equal(nv.kv_attention(q, s.cache, s.table, s.kv_lens, workspace=ws[:need]), want)
@@ -404,7 +404,7 @@ def test_captured_step_follows_lengths_and_slots():
     table = torch.zeros(b, 100, dtype=torch.int32, device="cuda")
     lens, slots, pos = (torch.zeros(b, dtype=torch.int32, device="cuda") for _ in range(3))
     base = Sequences(20, [3100, 40, 900], hkv, d, page, spare=20).append()
-    ws = torch.empty(nv.kv_attention_workspace_size(b, b, hq, hkv, d, page, 100, True), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(nv.kv_attention_workspace_size(b, b, hq, hkv, d, page, 100, 0, True), dtype=torch.uint8, device="cuda")
     out, lse = torch.empty(b, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(b, hq, device="cuda")
     q_out = torch.empty(b, hq, d, dtype=torch.bfloat16, device="cuda")
 

@@ -44,7 +44,7 @@ def test_append(L):
     assert "rope_dim" in L.nvfp4_last_error().decode()
     assert f(pages=1 << 26) == 2 and f(t=(1 << 27) + 1) == 2 and f(t=1 << 26) == 2  # slots, tokens, work-items
     assert f(t=-1) == 1 and f(pages=-1) == 1 and f(h=0) == 1 and f(k=None) == 1 and f(v=None) == 1 and f(slots=None) == 1
-    assert f(q=None) == 1 and f(qo=None) == 1 and f(qh=0) == 1 and f(pos=None) == 1 and f(rope=None) == 1 and f(maxp=-1) == 1
+    assert f(q=None) == 1 and f(qo=None) == 1 and f(qh=0) == 1 and f(pos=None) == 1 and f(rope=None) == 1 and f(maxp=-1) == 1 and f(maxp=0) == 1
     assert f(cache=None) == 1 and f(ks=None) == 1 and f(vs=None) == 1
     assert f(kst=1016) == 1 and f(vst=0) == 1 and f(qst=-4096) == 1 and f(qost=4088) == 1 and f(kst=1 << 41) == 1
     assert f(kst=1028) == 3 and f(k=AT["k"] + 8) == 3 and f(qo=AT["qo"] + 2) == 3 and f(slots=AT["slots"] + 2) == 3
@@ -110,10 +110,11 @@ def test_attention(L):
     assert f(ws=AT["q"], tp=64) == 1 and f(lse=AT["lens"]) == 1
     assert f(b=0) == 0 and f(t=0, b=0, q=None, out=None, lens=None, table=None) == 0
     size = L.nvfp4_kv_attention_workspace_size
-    need = size(3, 5, 32, 8, 128, 64, 64, 0)
+    need = size(3, 5, 32, 8, 128, 64, 64, 0, 0)
     assert need > 0 and f(tp=64, wsb=need - 1) == 4 and f(tp=64, ws=None) == 1 and f(tp=64, ws=AT["ws"] + 8) == 3
-    for bad in ((0, 5, 32, 8, 128, 64, 64, 0), (3, 5, 33, 8, 128, 64, 64, 0), (3, 5, 32, 8, 96, 64, 64, 0),
-                (3, 5, 32, 8, 128, 64, 64, 1), (3, 5, 32, 8, 128, 64, 0, 0), (3, 0, 32, 8, 128, 64, 64, 0)):
+    for bad in ((0, 5, 32, 8, 128, 64, 64, 0, 0), (3, 5, 33, 8, 128, 64, 64, 0, 0), (3, 5, 32, 8, 96, 64, 64, 0, 0),
+                (3, 5, 32, 8, 128, 64, 64, 0, 1), (3, 5, 32, 8, 128, 64, 0, 0, 0), (3, 0, 32, 8, 128, 64, 64, 0, 0),
+                (3, 5, 32, 8, 128, 64, 64, -1, 0)):
         assert size(*bad) == 0, bad
 
 
