@@ -97,6 +97,7 @@ SIGNATURES = {
                                _c_p]),
     "nvfp4_kv_attention_workspace_size": (_c_size, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
                                                     _c_int]),
+    "nvfp4_kv_attention_path": (_c_int, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
     "nvfp4_kv_attention": (_c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p,
                                     _c_p, _c_i64, _c_i64, _c_i64, ctypes.c_float, _c_int, _c_i64, _c_p, _c_p, _c_p,
                                     _c_size, _c_p]),
@@ -1063,6 +1064,13 @@ def kv_attention_workspace_size(sequences: int, tokens: int, q_heads: int, heads
                                 table_pages: int, window: int, one_each: bool) -> int:
     return int(lib().nvfp4_kv_attention_workspace_size(sequences, tokens, q_heads, heads, head_dim, page_size,
                                                        table_pages, window, 1 if one_each else 0))
+
+
+def kv_attention_path(sequences: int, tokens: int, q_heads: int, heads: int, head_dim: int, page_size: int,
+                      table_pages: int, window: int, one_each: bool) -> int:
+    """Rows of a workgroup of the kernel kv_attention takes (see nvfp4_kv_attention_path in include/nvfp4.h)."""
+    return int(lib().nvfp4_kv_attention_path(sequences, tokens, q_heads, heads, head_dim, page_size, table_pages, window,
+                                             1 if one_each else 0))
 
 
 def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,

@@ -116,6 +116,14 @@ int check_tokens(int64_t tokens) {
   return NVFP4_OK;
 }
 
+bool attention_sizes_ok(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int64_t head_dim,
+                        int64_t page_size, int64_t table_pages, int64_t window, int one_each) {
+  return sequences > 0 && sequences <= kMaxSequences && tokens > 0 && tokens <= kMaxTokens && table_pages > 0 &&
+         cache_sizes_ok(heads, head_dim, page_size) && table_pages <= kMaxSlots / page_size && q_heads > 0 &&
+         q_heads <= kMaxHeads && q_heads % heads == 0 && window >= 0 && tokens * q_heads <= kMaxRows &&
+         (!one_each || sequences == tokens);
+}
+
 int64_t page_bytes(int64_t heads, int64_t head_dim, int64_t page_size) { return heads * (page_size / 32) * 36 * head_dim; }
 
 }  // namespace
@@ -223,14 +231,20 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
 NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
                                                    int64_t head_dim, int64_t page_size, int64_t table_pages,
                                                    int64_t window, int one_each) {
-  if (sequences <= 0 || sequences > kMaxSequences || tokens <= 0 || tokens > kMaxTokens || table_pages <= 0 ||
-      !cache_sizes_ok(heads, head_dim, page_size) || table_pages > kMaxSlots / page_size || q_heads <= 0 ||
-      q_heads > kMaxHeads || q_heads % heads != 0 || window < 0 ||
-      tokens * q_heads > kMaxRows || (one_each && sequences != tokens))
-    return 0;
+  if (!attention_sizes_ok(sequences, tokens, q_heads, heads, head_dim, page_size, table_pages, window, one_each)) return 0;
   return nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim, table_pages * page_size, window,
                                   one_each != 0)
       .ws_bytes;
+}
+
+NVFP4_API int nvfp4_kv_attention_path(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
+                                      int64_t head_dim, int64_t page_size, int64_t table_pages, int64_t window,
+                                      int one_each) {
+  if (!attention_sizes_ok(sequences, tokens, q_heads, heads, head_dim, page_size, table_pages, window, one_each))
+    return -1;
+  return nvfp4::kv_block_rows(nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim,
+                                                       table_pages * page_size, window, one_each != 0),
+                              (int)head_dim);
 }
 
 NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t* cache, int64_t pages,

@@ -347,7 +347,8 @@ struct Rows {
   __device__ __forceinline__ void start(const KvAttend& a, const Sequence& seq, int first, int head) {
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int rows = seq.count * a.group;
-    const float base = a.scale * 1.44269504088896340736f * a.k_scale[head];
+    // in 64 bits: neither it nor its product with a row's power of two may lose bits below fp32's range
+    const double base = (double)a.scale * 1.44269504088896340736 * (double)a.k_scale[head];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = min(first + r * 16 + c, rows - 1);  // rows past the last: computed, not stored
@@ -372,7 +373,7 @@ struct Rows {
       const int exponent = (int)(__float_as_uint(top) >> 23);
       const int e = exponent == 0 || exponent == 255 ? 0 : min(14 + 127 - exponent, 126);
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      factor[r] = base * __uint_as_float((uint32_t)(127 - e) << 23);
+      factor[r] = (float)(base * (double)__uint_as_float((uint32_t)(127 - e) << 23));
       const float sign = factor[r] < 0.0f ? -up : up;
       factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
 #pragma unroll
@@ -881,8 +882,6 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
 // join; 16 ragged contexts 25.5, 24.5, 25.
 constexpr int kItems = 512, kLeastUnits = 16;
 
-int block_rows(int tiles, int head_dim) { return tiles ? 16 * tiles : head_dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows; }
-
 int64_t block_count(int64_t sequences, int64_t tokens, int64_t group, int rows, bool one_each) {
   if (one_each) return sequences * ((group + rows - 1) / rows);
   return (tokens * group + sequences * (rows - 1)) / rows;  // at most so many partly filled ones
@@ -922,6 +921,10 @@ hipError_t run_tiles(const KvAttend& a, const KvPlan& p, float* partial, float2*
 
 }  // namespace
 
+int kv_block_rows(const KvPlan& p, int head_dim) {
+  return p.tiles ? 16 * p.tiles : head_dim == 256 ? Tiles<256>::kRows : Tiles<128>::kRows;
+}
+
 KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
                          int64_t capacity, int64_t window, bool one_each) {
   KvPlan p;
@@ -941,7 +944,7 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
     p.tiles = 0;
   else
     p.tiles = !few && head_dim < 256 && work >= 32768.0 ? 2 : 1;
-  const int rows = block_rows(p.tiles, head_dim);
+  const int rows = kv_block_rows(p, head_dim);
   p.blocks = block_count(sequences, tokens, group, rows, one_each);
   // The second launch takes 4 to 6 us, what a workgroup needs for 32 units.  One
   // sequence of 1024 tokens of 8 heads: 9.2 us whole, 9.6 split; of 2048 14.4,
@@ -954,7 +957,7 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
 }
 
 hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& p, void* workspace, hipStream_t stream) {
-  const int64_t slots = (p.blocks + p.parts) * a.heads * block_rows(p.tiles, head_dim);
+  const int64_t slots = (p.blocks + p.parts) * a.heads * kv_block_rows(p, head_dim);
   float* partial = static_cast<float*>(workspace);
   float2* stats = reinterpret_cast<float2*>(partial + slots * head_dim);
   if (head_dim == 64)

@@ -252,6 +252,7 @@ struct KvPlan {
 };
 KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads, int head_dim,
                          int64_t capacity, int64_t window, bool one_each);
+int kv_block_rows(const KvPlan& plan, int head_dim);
 hipError_t launch_kv_attention(const KvAttend& a, int head_dim, const KvPlan& plan, void* workspace,
                                hipStream_t stream);
 

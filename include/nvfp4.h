@@ -626,6 +626,11 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
 NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
                                                    int64_t head_dim, int64_t page_size, int64_t table_pages,
                                                    int64_t window, int one_each);
+/* Rows (a token and a query head) of a workgroup of the kernel that nvfp4_kv_attention takes for these sizes: 16, 32,
+ * or for much work 256 (head_dim 128) or 128 (head_dim 256).  -1 for an empty call or one that is refused. */
+NVFP4_API int nvfp4_kv_attention_path(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
+                                      int64_t head_dim, int64_t page_size, int64_t table_pages, int64_t window,
+                                      int one_each);
 NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t* cache, int64_t pages,
                                  int64_t page_size, int64_t heads, int64_t head_dim, const float* k_scale,
                                  const float* v_scale, const int32_t* page_table, int64_t table_pages,

@@ -155,14 +155,33 @@ CASES = [
     ([900, 333, 20], [200, 3, 20], 4, 2, 32, True, 65),
     ([500, 30], [20, 30], 2, 2, 64, False, 0),
     ([5, 200], [9, 300], 2, 1, 64, False, 0),
+    ([700, 0, 33, 500], [300, 0, 1, 77], 4, 1, 64, True, 0),
+    ([512, 1000], [256, 513], 2, 1, 32, True, 0),
 ]
+# head_dim, rows of a workgroup
+PATHS = [(64, 16), (64, 32), (128, 16), (128, 32), (128, 256), (256, 16), (256, 128)]
 
 
-@DIMS
+def _table_for(rows, lens, new, hq, hkv, d, page, window):
+    """Pages of a table with which the call is planned with blocks of that many rows; None where it never is."""
+    need = max([-(-n // page) for n in lens] + [1])
+    one = min(new) == max(new) == 1
+    for pages in sorted({need} | {need * 2 ** i for i in range(1, 22)}):
+        if pages * page < 2 ** 31 and len(lens) * pages < 2 ** 22 and nv.kv_attention_path(
+                len(lens), sum(new), hq, hkv, d, page, pages, window, one) == rows:
+            return pages
+    return None
+
+
+@pytest.mark.parametrize("d,rows", PATHS)
 @pytest.mark.parametrize("lens,new,hq,hkv,page,causal,window", CASES)
-def test_attention(d, lens, new, hq, hkv, page, causal, window):
-    print("kv attention", d, lens, new, hq, hkv, page, causal, window, flush=True)
-    s = Sequences(len(lens) + d, lens, hkv, d, page).append()
+def test_attention(d, rows, lens, new, hq, hkv, page, causal, window):
+    """Every kernel: a wide page table makes the call look like more work than it is."""
+    pages = _table_for(rows, lens, new, hq, hkv, d, page, window)
+    if pages is None:
+        pytest.skip("few rows or a short window: never so many rows in a workgroup")
+    print("kv attention", d, rows, lens, new, hq, hkv, page, causal, window, flush=True)
+    s = Sequences(len(lens) + d, lens, hkv, d, page, table_pages=pages).append()
     q = queries(7, sum(new), hq, d)
     one = max(new) == 1 == min(new)
     out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, None if one else starts(new), causal=causal,
@@ -173,15 +192,72 @@ def test_attention(d, lens, new, hq, hkv, page, causal, window):
         assert torch.equal(out, again)  # the order of the sums is fixed, lse or not
 
 
-@DIMS
-@pytest.mark.parametrize("lens,new,hq,hkv,table_pages", [([5000], [1], 8, 1, None), ([9000, 100, 3000], [1, 1, 1], 3, 1, 600),
-                                                         ([2500, 2300], [4, 60], 8, 2, 300), ([20000], [2], 2, 1, 1000)])
-def test_attention_split_contexts(d, lens, new, hq, hkv, table_pages):
-    print("kv attention split", d, lens, new, hq, hkv, table_pages, flush=True)
-    s = Sequences(3, lens, hkv, d, 32, table_pages=table_pages).append()
+@pytest.mark.parametrize("d,rows", PATHS)
+@pytest.mark.parametrize("lens,new,hq,hkv", [([5000], [1], 8, 1), ([9000, 100, 3000], [1, 1, 1], 3, 1),
+                                             ([2500, 2300], [4, 60], 8, 2), ([20000], [2], 2, 1),
+                                             ([6000, 40, 3300], [300, 40, 1], 4, 1)])
+def test_attention_split_contexts(d, rows, lens, new, hq, hkv):
+    pages = _table_for(rows, lens, new, hq, hkv, d, 32, 0)
+    if pages is None:
+        pytest.skip("few rows: never so many in a workgroup")
+    print("kv attention split", d, rows, lens, new, hq, hkv, flush=True)
+    s = Sequences(3, lens, hkv, d, 32, table_pages=pages).append()
     q = queries(8, sum(new), hq, d)
+    assert nv.kv_attention_workspace_size(len(lens), sum(new), hq, hkv, d, 32, pages, 0, False) > 0
     out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, starts(new), return_lse=True)
     check_attention(s, new, q, out, lse, d ** -0.5)
+
+
+@pytest.mark.parametrize("d,rows", PATHS)
+@pytest.mark.parametrize("fill", [0x00, 0x7F, 0xFF])
+def test_attention_does_not_see_what_is_masked(d, rows, fill):
+    """Unwritten places of any content, pages past the length, NaN tokens behind a row's own, bad page numbers."""
+    new = [40, 150]
+    pages = _table_for(rows, [70, 200], new, 4, 2, d, 64, 0)
+    s = Sequences(9, [70, 200], 2, d, 64, fill=fill, table_pages=max(pages, 9))
+    s.k[1][190, 0, 3] = float("nan")  # seen by the last 10 tokens, through both query heads of its group
+    s.v[1][195, 1, 3] = float("inf")
+    s.append()
+    q = queries(1, sum(new), 4, d)
+    table = s.table.clone()
+    table[0, 2:] = 2 ** 31 - 1
+    table[1, 4:] = -1
+    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, starts(new), return_lse=True)
+    bad = torch.zeros(sum(new), 4, dtype=torch.bool)
+    bad[-10:, :2] = True
+    bad[-5:, 2:] = True
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), bad) and torch.equal(torch.isnan(out).any(-1).cpu(), bad)
+    assert torch.equal(torch.isnan(lse).cpu(), bad)
+    # the rest as with finite stand-ins for these tokens
+    s.k[1][190, 0, 3] = 0.0
+    s.v[1][195, 1, 3] = 0.0
+    at = 0
+    for b, m in enumerate(new):
+        k, v = s.held(b)
+        ref = okv.attention(q[at:at + m].float().numpy(), k, v, d ** -0.5, okv.visible(s.lens[b], m))
+        ok = ~bad[at:at + m].numpy()
+        assert np.abs(out[at:at + m].double().cpu().numpy() - ref[0])[ok].max() <= 2.0 ** -7 * np.abs(ref[0]).max()
+        at += m
+
+
+@pytest.mark.parametrize("d,rows", PATHS)
+def test_attention_leaves_out_pages_that_are_not_in_the_cache(d, rows):
+    n, new = 330, 70
+    pages = _table_for(rows, [n], [new], 2, 1, d, 32, 0)
+    s = Sequences(11, [n], 1, d, 32, table_pages=pages).append()
+    table = s.table.clone()
+    table[0, 1], table[0, 3] = s.cache.pages, -5  # tokens 32..63 and 96..127
+    q = queries(3, new, 2, d)
+    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, starts([new]), return_lse=True)
+    k, v = s.held(0)
+    seen = okv.visible(n, new).copy()
+    seen[:, 32:64] = seen[:, 96:128] = False
+    ref = okv.attention(q.float().numpy(), k, v, d ** -0.5, seen)
+    assert np.abs(out.double().cpu().numpy() - ref[0]).max() <= 2.0 ** -7 * np.abs(ref[0]).max()
+    assert np.abs(lse.double().cpu().numpy() - ref[1]).max() <= 1e-4
+    table.fill_(-1)
+    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, starts([new]), return_lse=True)
+    assert (out == 0).all() and torch.isneginf(lse).all()
 
 
 @pytest.mark.parametrize("b,longest", [(70, 300), (150, 40), (257, 900)])
@@ -195,15 +271,17 @@ def test_attention_of_many_sequences(b, longest):
     check_attention(s, new, q, out, lse, 0.125)
 
 
-@DIMS
+@pytest.mark.parametrize("d,rows", PATHS)
 @pytest.mark.parametrize("size,scale", [(0.0, 1.0), (1e-30, 1.0), (30.0, None), (1.0, -0.3), (1.0, 0.0), (2e38, 1e-38), (1.0, 1e-30)])
-def test_attention_of_small_and_large_logits(d, size, scale):
-    s = Sequences(5, [150, 700], 1, d, 32).append()
-    q = queries(2, 2, 3, d, size)
+def test_attention_of_small_and_large_logits(d, rows, size, scale):
+    lens, new = [150, 700], [40, 33]
+    pages = _table_for(rows, lens, new, 3, 1, d, 32, 0)
+    s = Sequences(5, lens, 1, d, 32, table_pages=pages).append()
+    q = queries(2, sum(new), 3, d, size)
     q.clamp_(-3e38, 3e38)
     scale = d ** -0.5 if scale is None else scale
-    out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, scale=scale, return_lse=True)
-    check_attention(s, [1, 1], q, out, lse, scale)
+    out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, starts(new), scale=scale, return_lse=True)
+    check_attention(s, new, q, out, lse, scale)
 
 
 def test_attention_keeps_many_small_probabilities():
@@ -226,56 +304,6 @@ def test_attention_keeps_many_small_probabilities():
         p = float(np.exp(-np.float64(np.float32(scale)) * 6))
         want = 6.0 * 60000 * p / (1 + 60000 * p)
         assert abs(float(out[0, 0, 5]) - want) <= want * (2.0 ** -8 + 2.0 ** -10), exponent
-
-
-@DIMS
-@pytest.mark.parametrize("fill", [0x00, 0x7F, 0xFF])
-@pytest.mark.parametrize("new", [[1, 1], [40, 150]])
-def test_attention_does_not_see_what_is_masked(d, fill, new):
-    """Unwritten places of any content, pages past the length, a NaN token after a row's own, bad page numbers."""
-    s = Sequences(9, [70, 200], 2, d, 64, fill=fill, table_pages=9)
-    s.k[1][190, 0, 3] = float("nan")  # seen by the last 10 tokens, through both heads of its group
-    s.v[1][195, 1, 3] = float("inf")
-    s.append()
-    q = queries(1, sum(new), 4, d)
-    st = None if max(new) == 1 else starts(new)
-    table = s.table.clone()
-    table[0, 2:] = 2 ** 31 - 1
-    table[1, 4:] = -1
-    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, st, return_lse=True)
-    bad = torch.zeros(sum(new), 4, dtype=torch.bool)
-    bad[-min(10, new[1]):, :2] = True
-    bad[-min(5, new[1]):, 2:] = True
-    assert torch.equal(torch.isnan(out).all(-1).cpu(), bad) and torch.equal(torch.isnan(out).any(-1).cpu(), bad)
-    assert torch.equal(torch.isnan(lse).cpu(), bad)
-    # the rest as without these tokens' NaN: compare with the oracle on finite stand-ins where nothing sees them
-    s.k[1][190, 0, 3] = 0.0
-    s.v[1][195, 1, 3] = 0.0
-    keep = ~bad
-    at = 0
-    for b, m in enumerate(new):
-        k, v = s.held(b)
-        ref = okv.attention(q[at:at + m].float().numpy(), k, v, d ** -0.5, okv.visible(s.lens[b], m))
-        ok = keep[at:at + m].numpy()
-        assert np.abs(out[at:at + m].double().cpu().numpy() - ref[0])[ok].max(initial=0) <= 2.0 ** -7 * np.abs(ref[0]).max()
-        at += m
-
-
-def test_attention_leaves_out_pages_that_are_not_in_the_cache():
-    s = Sequences(11, [130], 1, 64, 32).append()
-    table = s.table.clone()
-    table[0, 1], table[0, 3] = s.cache.pages, -5  # tokens 32..63 and 96..127
-    q = queries(3, 1, 2, 64)
-    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, return_lse=True)
-    k, v = s.held(0)
-    seen = np.ones((1, 130), bool)
-    seen[0, 32:64] = seen[0, 96:128] = False
-    ref = okv.attention(q.float().numpy(), k, v, 0.125, seen)
-    assert np.abs(out.double().cpu().numpy() - ref[0]).max() <= 2.0 ** -7 * np.abs(ref[0]).max()
-    assert np.abs(lse.double().cpu().numpy() - ref[1]).max() <= 1e-4
-    table.fill_(-1)
-    out, lse = nv.kv_attention(q.cuda(), s.cache, table, s.kv_lens, return_lse=True)
-    assert (out == 0).all() and torch.isneginf(lse).all()
 
 
 def test_attention_cuts_lengths_and_starts_to_their_tables():

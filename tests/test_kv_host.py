@@ -140,3 +140,21 @@ def test_binding_refuses():
         nv.kv_read(nv.KVCache(cache.data, cache.k_scale, cache.v_scale[:1], 64, 64), i)
     with pytest.raises(ValueError, match="shape"):
         nv.kv_read(nv.KVCache(cache.data[:, 16:].contiguous(), cache.k_scale, cache.v_scale, 64, 64), i)
+
+
+def test_attention_paths(L):
+    """The sizes that choose each kernel, by the work at hand."""
+    def path(t, hq, h, d, pages=64, b=1, window=0, one=0):
+        return L.nvfp4_kv_attention_path(b, t, hq, h, d, 64, pages, window, one)
+
+    assert path(1, 32, 8, 128, 1 << 20, one=1) == 16 and path(64, 64, 8, 128, 1 << 20, 64, one=1) == 16
+    assert path(1000, 32, 8, 128, 16) == 16 and path(2000, 32, 8, 128, 32) == 32 and path(4096, 32, 8, 128) == 256
+    assert path(4096, 32, 8, 128, window=100) == 16  # a short window is little work
+    assert path(300, 5, 5, 64, 5) == 16 and path(4096, 32, 8, 64) == 32 and path(1 << 20, 32, 8, 64, 1 << 20) == 32
+    assert path(1000, 16, 4, 256, 16) == 16 and path(4096, 16, 4, 256) == 128
+    assert path(0, 32, 8, 128) == -1 and path(5, 33, 8, 128) == -1 and path(5, 32, 8, 128, one=1) == -1
+    size = L.nvfp4_kv_attention_workspace_size
+    assert size(1, 1, 32, 8, 128, 64, 16, 0, 1) == 0  # 1024 tokens: not split
+    assert size(1, 1, 32, 8, 128, 64, 32, 0, 1) > 0 and size(1, 1, 32, 8, 128, 64, 32, 500, 1) == 0
+    assert size(64, 64, 32, 8, 128, 64, 32, 0, 1) == 0  # 2048 tokens of many: not split
+    assert size(64, 64, 32, 8, 128, 64, 64, 0, 1) > 0 and size(1, 4096, 32, 8, 128, 64, 64, 0, 0) == 0
