@@ -17,8 +17,9 @@
 //       the row's largest.  The row's sum adds the p before their rounding.
 //   O^T += V^T P^T: a lane's results of S^T are its operand of P^T (kv_device.h).
 //
-//  k_kv_rows  a workgroup of 4 waves per row block, head and part of the
-//             context; a wave takes every fourth unit of 32 tokens
+//  k_kv_rows  a workgroup of 4 or 8 waves per row block, head and part of the
+//             context; a wave takes every fourth (eighth) unit of 32 tokens
+//  k_kv_tiles many rows: 8 waves decode the units together into LDS
 //  k_kv_join  adds the parts of the rows whose context was split
 #include <algorithm>
 
@@ -160,7 +161,7 @@ __device__ bool find(const KvAttend& a, int parts, int least, int number, Item& 
 __device__ __forceinline__ void visible(const KvAttend& a, const Sequence& s, int t, int& lo, int& hi) {
   const int end = s.len - s.count + t + 1;
   hi = a.causal ? max(0, min(end, s.len)) : s.len;
-  lo = a.window > 0 ? max(0, end - a.window) : 0;
+  lo = a.window > 0 ? (int)max((int64_t)0, (int64_t)end - a.window) : 0;
 }
 
 // Units [first, end) that rows [row, row + ROWS) of a sequence see.
@@ -549,11 +550,12 @@ __device__ __forceinline__ void store_row(const KvAttend& a, const Sequence& s, 
 
 // -------------------------------------------------------------- the kernels
 
-template <int D, int R>
-__global__ __launch_bounds__(256, 2) void k_kv_rows(KvAttend a, int parts, int least, float* __restrict__ partial,
+template <int D, int R, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts, int least, float* __restrict__ partial,
                                                     float2* __restrict__ stats) {
   using X = Rows<D, R>;
-  constexpr int P = X::P, T = X::T, ROWS = 16 * R, WAVES = 4, DEPTH = 2;
+  constexpr int P = X::P, T = X::T, ROWS = 16 * R, DEPTH = 2;
+  constexpr int E = 16 / WAVES, LANES = 64 / E;  // of the sums: elements of a thread, threads of a row
   __shared__ float s_o[WAVES][16][68];
   __shared__ float2 s_ml[WAVES][ROWS];
 
@@ -598,7 +600,7 @@ __global__ __launch_bounds__(256, 2) void k_kv_rows(KvAttend a, int parts, int l
   __syncthreads();
   const float vs = a.v_scale[head];
   const int64_t slot = (int64_t)blockIdx.x * ROWS;  // of the workspace
-  const int tr = threadIdx.x >> 4, td = (threadIdx.x & 15) * 4;
+  const int tr = threadIdx.x / LANES, td = threadIdx.x % LANES * E;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     float top = kLow, m_row = kLow, l_row = 0.0f;
@@ -631,18 +633,19 @@ __global__ __launch_bounds__(256, 2) void k_kv_rows(KvAttend a, int parts, int l
           *reinterpret_cast<float4*>(&s_o[wave][c][g * 16 + i * T + t]) = o;
         }
       __syncthreads();
-      float o[4] = {};
+      float o[E] = {};
 #pragma unroll
       for (int v = 0; v < WAVES; ++v)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += s_o[v][tr][td + i];
+        for (int i = 0; i < E; ++i) o[i] += s_o[v][tr][td + i];
       if (row >= rows) continue;
       const int d = D == 64 ? td : p * 128 + (td >> 4) * 32 + k * 16 + (td & 15);
       if (block_parts > 1) {
-        *reinterpret_cast<float4*>(partial + (slot + r * 16 + tr) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+        float* to = partial + (slot + r * 16 + tr) * D + d;  // (WAVES 8: never split)
+        if constexpr (E == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
         if (d == 0) stats[slot + r * 16 + tr] = make_float2(m_row, l_row);
       } else {
-        store_row<D, 4>(a, seq, row, head, d, o, m_row, l_row, vs);
+        store_row<D, E>(a, seq, row, head, d, o, m_row, l_row, vs);
       }
     }
   }
@@ -819,7 +822,8 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
 // (4 LANES) neighbours that take the other elements: eight lanes to a part read
 // 64 parts in one round of loads where few blocks leave the GPU empty.
 template <int D, int ROWS, int LANES>
-__global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int least, const float* __restrict__ partial,
+__global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int least, int items,
+                                                  const float* __restrict__ partial,
                                                   const float2* __restrict__ stats) {
   constexpr int AT_ONCE = 64 / LANES, SLICES = D / (4 * LANES);
   const int slice = blockIdx.x % SLICES, sixteen = blockIdx.x / SLICES % (ROWS / 16), at_ = blockIdx.x / (SLICES * (ROWS / 16));
@@ -829,7 +833,8 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
   int first, end;
   block_units<ROWS>(a, w.seq, w.local * ROWS, first, end);
   const int block_parts = (end - first + w.part_units - 1) / w.part_units;
-  if (block_parts <= 1) return;
+  // (q_starts that decrease could number items past the workspace)
+  if (block_parts <= 1 || (int64_t)w.base + (int64_t)block_parts * w.blocks > items) return;
   const int lane = threadIdx.x & 63, sub = lane / LANES, d = (slice * LANES + lane % LANES) * 4;
   const float vs = a.v_scale[head];
   const int rows = w.seq.count * a.group;
@@ -891,19 +896,26 @@ template <int D, int ROWS>
 void join_parts(const KvAttend& a, const KvPlan& p, const float* partial, const float2* stats, hipStream_t stream) {
   if (p.parts == 0) return;
   const unsigned blocks = (unsigned)(p.blocks * a.heads) * (ROWS / 16);
+  const int items = (int)(p.blocks + p.parts);
   const unsigned waves = a.starts ? 16 : (unsigned)(a.group < 16 ? a.group : 16);
   if (blocks <= 128)
     hipLaunchKernelGGL((k_kv_join<D, ROWS, 8>), dim3(blocks * (D / 32)), dim3(64 * waves), 0, stream, a, p.parts,
-                       kLeastUnits, partial, stats);
+                       kLeastUnits, items, partial, stats);
   else
     hipLaunchKernelGGL((k_kv_join<D, ROWS, D / 4>), dim3(blocks), dim3(64 * waves), 0, stream, a, p.parts, kLeastUnits,
-                       partial, stats);
+                       items, partial, stats);
 }
 
 template <int D, int R>
 hipError_t run_rows(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
-  hipLaunchKernelGGL((k_kv_rows<D, R>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(256), 0, stream, a,
-                     p.parts, kLeastUnits, partial, stats);
+  const unsigned items = (unsigned)((p.blocks + p.parts) * a.heads);
+  if constexpr (R == 1) {
+    if (p.waves == 8) {
+      hipLaunchKernelGGL((k_kv_rows<D, 1, 8>), dim3(items), dim3(512), 0, stream, a, 0, kLeastUnits, partial, stats);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((k_kv_rows<D, R, 4>), dim3(items), dim3(256), 0, stream, a, p.parts, kLeastUnits, partial, stats);
   join_parts<D, 16 * R>(a, p, partial, stats, stream);
   return hipGetLastError();
 }
@@ -934,16 +946,18 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   // Blocks of 32 rows times the units that each may see.  Work enough to fill
   // the GPU with fewer, larger workgroups takes them.  1000 tokens of 32 heads
   // in groups of 4, head_dim 128: 29 us with blocks of 16 rows, 35 with 32, 52
-  // in tiles; 2000: 75, 62, 73; 4096: 252, 192, 160.  Head_dim 64 has no
-  // tiles: 4000 tokens of 16 heads 78, 59, 106 us, 16000 of 32 1017, 723, 809.
-  // Head_dim 256 has no room for 32 rows: 1500 tokens of 16 heads in groups of
-  // 4 take 48 us with 16 rows, 73 in tiles, 4096 tokens 242 and 177.
+  // in tiles; 2000: 75, 62, 73; 4096: 252, 192, 157.  8 tokens of each of 16
+  // contexts of 8192: 61, 46, 132.  Head_dim 64 has no tiles: 4000 tokens of 16
+  // heads 78, 59, 106 us, 16000 of 32 1017, 723, 809.  Head_dim 256 has no room
+  // for 32 rows: 1500 tokens of 16 heads in groups of 4 take 48 us with 16
+  // rows, 73 in tiles, 4096 tokens 242 and 177; 16 tokens of each of 8 contexts
+  // of 8192 80 and 102, 32 tokens 181 and 130.
   const double work = (double)block_count(sequences, tokens, group, 32, one_each) * (double)heads * (double)units;
-  const bool few = tokens * group <= 32 * sequences;
-  if (!few && ((head_dim == 256 && work >= 65536.0) || (head_dim == 128 && work >= 262144.0)))
+  const int64_t mean = (tokens * group + sequences - 1) / sequences;  // rows of a sequence
+  if (mean >= 128 && ((head_dim == 256 && work >= 65536.0) || (head_dim == 128 && work >= 262144.0)))
     p.tiles = 0;
   else
-    p.tiles = !few && head_dim < 256 && work >= 32768.0 ? 2 : 1;
+    p.tiles = mean > 16 && head_dim < 256 && work >= 32768.0 ? 2 : 1;
   const int rows = kv_block_rows(p, head_dim);
   p.blocks = block_count(sequences, tokens, group, rows, one_each);
   // The second launch takes 4 to 6 us, what a workgroup needs for 32 units.  One
@@ -951,6 +965,10 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   // 10.9; 32 of 1024 12.6, 17; 32 of 2048 21.9, 24.6.
   const int64_t items = p.blocks * heads;
   const bool split = units > (items < 192 ? 32 : 64) && items < (p.tiles ? 1024 : 256);
+  // Long contexts that are not split, on a GPU that is not full: eight waves to
+  // a workgroup.  24 sequences with windows of 1024: 10.4 us with 4, 9.3; 32 of
+  // 2048 22.5, 20; but 8 of 300 tokens 5.5, 5.9.
+  p.waves = p.tiles == 1 && !split && items <= 512 && units > 16 ? 8 : 4;
   p.parts = split ? (int)((kItems + heads - 1) / heads) : 0;
   p.ws_bytes = split ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
   return p;

@@ -243,10 +243,11 @@ struct KvAttend {
 };
 // How a call is laid out: row blocks of 16 * tiles rows (a row: a token and a
 // query head; tiles 0: the blocks of k_kv_tiles), at most `blocks` of them for
-// each head, and up to `parts` more work items for each head from splitting
-// long contexts (0: none is split).  capacity: tokens of the longest context.
+// each head, `waves` to a workgroup where tiles is not 0, and up to `parts`
+// more work items for each head from splitting long contexts (0: none is
+// split).  capacity: tokens of the longest context.
 struct KvPlan {
-  int tiles, parts;
+  int tiles, waves, parts;
   int64_t blocks;
   size_t ws_bytes;
 };

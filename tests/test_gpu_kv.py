@@ -144,6 +144,8 @@ CASES = [
     ([129, 1, 2000, 400], [1] * 4, 8, 2, 64, True, 0),
     ([700, 5, 0, 1300], [1] * 4, 16, 1, 128, True, 0),
     ([257, 90], [1] * 2, 34, 2, 32, True, 0),
+    ([600, 1025, 31], [1] * 3, 64, 1, 64, True, 0),
+    ([1000, 640], [2, 1], 3, 3, 32, True, 700),
     ([40, 300, 5, 77], [3, 8, 5, 1], 6, 2, 32, True, 0),
     ([40, 300, 5, 77], [3, 0, 5, 0], 6, 2, 32, True, 0),
     ([3, 0, 64], [7, 4, 64], 3, 1, 32, True, 0),
@@ -319,6 +321,30 @@ def test_attention_cuts_lengths_and_starts_to_their_tables():
     # a table without pages
     out, lse = nv.kv_attention(q.cuda(), s.cache, s.table[:, :0].contiguous(), s.kv_lens, return_lse=True)
     assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_attention_of_starts_in_disorder_stays_in_bounds():
+    """Row numbers that decrease or leave the call's tokens: unspecified rows, but none outside its own buffers."""
+    s = Sequences(22, [4000, 3000, 2000], 1, 64, 32).append()
+    q = queries(5, 50, 20, 64).cuda()
+    need = nv.kv_attention_workspace_size(3, 50, 20, 1, 64, 32, s.table.shape[1], 0, False)
+    assert need > 0
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.full((60, 20, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((60, 20), 7.0, device="cuda")
+    for st in ([0, 50, 0, 50], [50, 0, 50, 0], [-9, 70, -9, 70], [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 50]):
+        st = torch.tensor(st, dtype=torch.int32, device="cuda")
+        nv.kv_attention(q, s.cache, s.table, s.kv_lens, st, out=out[:50], lse=lse[:50], workspace=ws[:need])
+        assert (ws[need:] == 0x5A).all() and (out[50:] == 7.0).all() and (lse[50:] == 7.0).all()
+
+
+def test_attention_windows_past_every_context():
+    """A window as long as int32 goes, contexts shorter than the new tokens: as without a window."""
+    s = Sequences(23, [5, 300], 1, 64, 32).append()
+    q = queries(6, 120, 2, 64).cuda()
+    want = nv.kv_attention(q, s.cache, s.table, s.kv_lens, starts([40, 80]))
+    for window in (300, 2 ** 31 - 2, 2 ** 31 - 1, 2 ** 40):
+        assert torch.equal(nv.kv_attention(q, s.cache, s.table, s.kv_lens, starts([40, 80]), window=window), want)
 
 
 def test_attention_leaves_other_rows_as_they_were():
