@@ -522,31 +522,43 @@ struct Rows {
   }
 };
 
-// Elements [d, d + E) of a row of the output, and its log sum (natural) at d = 0.
-template <int D, int E>
-__device__ __forceinline__ void store_row(const KvAttend& a, const Sequence& s, int row, int head, int d,
-                                          const float* o, float m, float l, float v_scale) {
-  const int t = row / a.group;
-  const int64_t at = (int64_t)(s.first + t) * (a.heads * a.group) + head * a.group + (row - t * a.group);
-  // l is 0 where nothing is visible, and NaN where a visible token is
-  const float f = l == 0.0f ? 0.0f : v_scale / l;
-  typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
-  uint32_t w[E / 2];
-#pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    const bf16x2_t v = {(__bf16)(o[i] * f), (__bf16)(o[i + 1] * f)};
-    w[i / 2] = __builtin_bit_cast(uint32_t, v);
+// A row of the output: where it lies, its sums' bound and total.
+template <int D>
+struct RowOut {
+  uint16_t* to;
+  float* lse;
+  float m, l, f;
+
+  __device__ __forceinline__ RowOut(const KvAttend& a, const Sequence& s, int row, int head, float m_, float l_)
+      : m(m_), l(l_) {
+    const int t = row / a.group;
+    const int64_t at = (int64_t)(s.first + t) * (a.heads * a.group) + head * a.group + (row - t * a.group);
+    to = a.out + at * D;
+    lse = a.lse ? a.lse + at : nullptr;
+    f = l == 0.0f ? 0.0f : a.v_scale[head] / l;  // l is 0 where nothing is visible, and NaN where a visible token is
   }
-  uint16_t* to = a.out + at * D + d;
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-  else if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(to) = w[0];
-  if (a.lse && d == 0)
-    a.lse[at] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994530942f;
-}
+  // Elements [d, d + E).
+  template <int E>
+  __device__ __forceinline__ void store(int d, const float* o) const {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const bf16x2_t v = {(__bf16)(o[i] * f), (__bf16)(o[i + 1] * f)};
+      w[i / 2] = __builtin_bit_cast(uint32_t, v);
+    }
+    if constexpr (E == 8)
+      *reinterpret_cast<uint4*>(to + d) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (E == 4)
+      *reinterpret_cast<uint2*>(to + d) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(to + d) = w[0];
+  }
+  // The natural logarithm of the sum.
+  __device__ __forceinline__ void store_lse() const {
+    if (lse) *lse = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.69314718055994530942f;
+  }
+};
 
 // -------------------------------------------------------------- the kernels
 
@@ -598,7 +610,6 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts
   for (int r = 0; r < R; ++r)
     if (g == 0) s_ml[wave][r * 16 + c] = make_float2(z.m[r], z.l[r]);
   __syncthreads();
-  const float vs = a.v_scale[head];
   const int64_t slot = (int64_t)blockIdx.x * ROWS;  // of the workspace
   const int tr = threadIdx.x / LANES, td = threadIdx.x % LANES * E;
 #pragma unroll
@@ -614,6 +625,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts
       l_row += s_ml[v][r * 16 + tr].y * __builtin_amdgcn_exp2f(s_ml[v][r * 16 + tr].x - m_row);
     const float shrink = __builtin_amdgcn_exp2f(z.m[r] - top);
     const int row = block * ROWS + r * 16 + tr;
+    const RowOut<D> row_out(a, seq, min(row, rows - 1), head, m_row, l_row);
     // element 128 p + 32 g + 8 i + t of row c is result i of tile t (D = 64: 16 g + 4 i + t); a
     // pass takes the results 2 k and 2 k + 1 (D = 64: all)
     constexpr int PASSES = D == 64 ? 1 : 2;
@@ -645,7 +657,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts
         if constexpr (E == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2], o[3]);
         if (d == 0) stats[slot + r * 16 + tr] = make_float2(m_row, l_row);
       } else {
-        store_row<D, E>(a, seq, row, head, d, o, m_row, l_row, vs);
+        row_out.template store<E>(d, o);
+        if (d == 0) row_out.store_lse();
       }
     }
   }
@@ -793,26 +806,35 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   }
 
   z.finish();
-  const float vs = a.v_scale[head];
   const int64_t slot = (int64_t)blockIdx.x * ROWS + wave * 16 * C::R;
 #pragma unroll
   for (int r = 0; r < C::R; ++r) {
     const int row = row0 + r * 16 + c;
     if (row >= rows) continue;
+    const RowOut<D> row_out(a, seq, row, head, z.m[r], z.l[r]);
+    float* to = partial + (slot + r * 16 + c) * D;
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i) {
+        // result i of tile t: element 32 g + 8 i + t of the panel
+        float o[T];
 #pragma unroll
-        for (int t = 0; t < T; t += 4) {
-          const float o[4] = {z.acc[r][p][t][i], z.acc[r][p][t + 1][i], z.acc[r][p][t + 2][i], z.acc[r][p][t + 3][i]};
-          const int d = p * 128 + g * (4 * T) + i * T + t;
-          if (block_parts > 1)
-            *reinterpret_cast<float4*>(partial + (slot + r * 16 + c) * D + d) = make_float4(o[0], o[1], o[2], o[3]);
-          else
-            store_row<D, 4>(a, seq, row, head, d, o, z.m[r], z.l[r], vs);
+        for (int t = 0; t < T; ++t) o[t] = z.acc[r][p][t][i];
+        const int d = p * 128 + g * 32 + i * 8;
+        if (block_parts > 1) {
+          reinterpret_cast<float4*>(to + d)[0] = make_float4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<float4*>(to + d)[1] = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+          row_out.template store<8>(d, o);
         }
-    if (block_parts > 1 && g == 0) stats[slot + r * 16 + c] = make_float2(z.m[r], z.l[r]);
+      }
+    if (g == 0) {
+      if (block_parts > 1)
+        stats[slot + r * 16 + c] = make_float2(z.m[r], z.l[r]);
+      else
+        row_out.store_lse();
+    }
   }
 }
 
@@ -836,7 +858,6 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
   // (q_starts that decrease could number items past the workspace)
   if (block_parts <= 1 || (int64_t)w.base + (int64_t)block_parts * w.blocks > items) return;
   const int lane = threadIdx.x & 63, sub = lane / LANES, d = (slice * LANES + lane % LANES) * 4;
-  const float vs = a.v_scale[head];
   const int rows = w.seq.count * a.group;
   const int64_t step = (int64_t)w.blocks * a.heads * ROWS;  // from part to part
   const int64_t slot0 = ((int64_t)(w.base + w.blocks - 1 - w.local) * a.heads + head) * ROWS;
@@ -877,7 +898,11 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
     for (int k = 32; k >= LANES; k >>= 1)
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[x] += __shfl_xor(o[x], k, 64);
-    if (sub == 0) store_row<D, 4>(a, w.seq, row, head, d, o, m, l, vs);
+    if (sub == 0) {
+      const RowOut<D> row_out(a, w.seq, row, head, m, l);
+      row_out.template store<4>(d, o);
+      if (d == 0) row_out.store_lse();
+    }
   }
 }
 
