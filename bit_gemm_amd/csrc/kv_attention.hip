@@ -906,11 +906,7 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
   }
 }
 
-// Parts: two work items for each CU beside the blocks, none of fewer than 16
-// units (four for each wave).  One token on 131072 of 8 heads takes 46 us with
-// one item for each CU, 41 with two, 41 with three, whose parts take longer to
-// join; 16 ragged contexts 25.5, 24.5, 25.
-constexpr int kItems = 512, kLeastUnits = 16;
+constexpr int kLeastUnits = 16;  // of a part: four for each wave
 
 int64_t block_count(int64_t sequences, int64_t tokens, int64_t group, int rows, bool one_each) {
   if (one_each) return sequences * ((group + rows - 1) / rows);
@@ -994,7 +990,13 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   // a workgroup.  24 sequences with windows of 1024: 10.4 us with 4, 9.3; 32 of
   // 2048 22.5, 20; but 8 of 300 tokens 5.5, 5.9.
   p.waves = p.tiles == 1 && !split && items <= 512 && units > 16 ? 8 : 4;
-  p.parts = split ? (int)((kItems + heads - 1) / heads) : 0;
+  // As many work items as the GPU holds workgroups (three to a CU; of k_kv_tiles
+  // one, but two rounds even out) if every block's last part counts half.  16
+  // ragged contexts: 24.8 us with 512 parts beside the blocks, 22.8; 8 of 9000
+  // to 15300, head_dim 64, 38.6, 32.2; 8 with 1 to 700 new tokens, head_dim 256
+  // (tiles), 146, 137.
+  const int64_t parts = std::max<int64_t>(1, (p.tiles ? 768 : 512) - items / 2);
+  p.parts = split ? (int)((parts + heads - 1) / heads) : 0;
   p.ws_bytes = split ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
   return p;
 }
