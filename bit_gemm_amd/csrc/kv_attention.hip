@@ -488,28 +488,41 @@ struct Rows {
         }
   }
 
+  __device__ __forceinline__ void add(f16x8_t v, int p, int t, const f16x8_t (&pr)[R]) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r][p][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pr[r], acc[r][p][t], 0, 0, 0);
+  }
   template <class Operands>
   __device__ __forceinline__ void add(const Operands& x, const f16x8_t (&pr)[R]) {
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int t = 0; t < T; ++t) {
-        const f16x8_t v = x.value(p, t);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          acc[r][p][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, pr[r], acc[r][p][t], 0, 0, 0);
-      }
+      for (int t = 0; t < T; ++t) add(x.value(p, t), p, t, pr);
   }
 
-  template <class Operands>
+  // One unit.  AHEAD: the values' operands are asked for before the softmax.
+  template <bool AHEAD, class Operands>
   __device__ __forceinline__ void attend(const Operands& x, int t0, bool held) {
     f32x4_t s[R][2], y[R][2];
-    f16x8_t pr[R];
+    f16x8_t pr[R], v[P][T];
     logits(x, s);
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int t = 0; t < T; ++t) v[p][t] = x.value(p, t);
+    }
     if (!whole(t0, held)) mask(s, t0, held);
     if (exponents(s, y)) raise(s, y);
     probabilities(y, pr);
-    add(x, pr);
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int t = 0; t < T; ++t) add(v[p][t], p, t, pr);
+    } else {
+      add(x, pr);
+    }
   }
 
   // The sums over a row's four lanes.
@@ -599,7 +612,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts
     for (int n = 0; n < DEPTH; ++n) {
       const int at = u + n * WAVES;
       if (at >= end) break;
-      z.attend(x[n], at * 32, held[n]);
+      z.template attend<false>(x[n], at * 32, held[n]);
       load(n, at + DEPTH * WAVES);
     }
   }
@@ -697,7 +710,6 @@ struct Share {
     s.x = w[0];
     s.y = w[1];
   }
-  // Without branches, to be scheduled among matrix instructions.
   __device__ __forceinline__ void store(uint8_t* to, int share) const {
     const int kind = share & 3;
     const bool key = kind < 2;
@@ -727,6 +739,13 @@ struct Tiles {
   static constexpr int kUnits = D == 256 ? 1 : 2;
   static_assert(kUnits * Share<D>::kCount == kWaves, "a share for each wave");
   static constexpr int kTileBytes = kUnits * Staged<D>::kBytes;
+  // Head_dim 256 has no registers to ask for a unit's values before its softmax.
+  // There the logits of a unit are made while the one before is added up (which
+  // reads a tile ahead and takes a third buffer): 4096 tokens of 16 heads in
+  // groups of 4 take 169 us, unit by unit 181.  Head_dim 128, 32 heads: 150 and,
+  // unit by unit with the values asked for, 145.
+  static constexpr bool kOverlap = D == 256;
+  static constexpr int kBuffers = kOverlap ? 3 : 2;
 };
 
 template <int D>
@@ -735,7 +754,7 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   using C = Tiles<D>;
   using X = Rows<D, C::R>;
   constexpr int P = X::P, T = X::T, ROWS = C::kRows;
-  extern __shared__ __align__(16) uint8_t s_kv[];  // three tiles
+  extern __shared__ __align__(16) uint8_t s_kv[];  // kBuffers tiles
 
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -753,56 +772,64 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   const int share = wave % Share<D>::kCount, share_of = wave / Share<D>::kCount;  // of unit share_of of a tile
   auto load = [&](int tile) { x.load(ahead.at(min(tile + share_of, end - 1)), share, lane); };
   auto store = [&](uint8_t* to) { x.store(to + share_of * Staged<D>::kBytes + lane * 16, share); };
-  // While tile i is multiplied, tile i + 1 is decoded into the next of three
-  // buffers and tile i + 2 is on its way from memory.  The one barrier of a
-  // turn stands before the first use of tile i + 1; the buffer that a turn
-  // writes was last read before the barrier of the turn before.
-  uint8_t *now = s_kv, *next = s_kv + C::kTileBytes, *spare = s_kv + 2 * C::kTileBytes;
+  uint8_t *now = s_kv, *next = s_kv + C::kTileBytes;
   if (first < end) load(first);
   X z;
   z.start(a, seq, min(row0, rows - 1), head);
   store(now);
   if (first < end) load(first + C::kUnits);
   __syncthreads();
-  // The logits of a unit are made while the one before is added up.
-  f32x4_t y[C::R][2];
-  if (active && first < end) {
-    f32x4_t s[C::R][2];
-    const bool held = mine.held(first);
-    z.logits(Staged<D>{now + lane * 16}, s);
-    if (!z.whole(first * 32, held)) z.mask(s, first * 32, held);
-    if (z.exponents(s, y)) z.raise(s, y);
-  }
-  for (int tile = first; tile < end; tile += C::kUnits) {
+  if constexpr (!C::kOverlap) {
+    // While tile i is multiplied, tile i + 1 is on its way from memory; then it
+    // is decoded into the other buffer, which was last read before the barrier
+    // of the turn before.  (Past the end: what the registers hold, never used.)
+    for (int tile = first; tile < end; tile += C::kUnits) {
 #pragma unroll
-    for (int n = 0; n < C::kUnits; ++n) {
-      const bool last = n == C::kUnits - 1;
-      if (last) {
-        if (C::kUnits == 1) store(next);
-        load(tile + 2 * C::kUnits);
-        __syncthreads();
+      for (int n = 0; n < C::kUnits; ++n) {
+        const int u = tile + n;
+        if (active && u < end)
+          z.template attend<true>(Staged<D>{now + n * Staged<D>::kBytes + lane * 16}, u * 32, mine.held(u));
       }
-      const int u = tile + n;
-      if (active && u < end) {
-        const Staged<D> at = {now + n * Staged<D>::kBytes + lane * 16};
-        const Staged<D> after = {(last ? next : now + (n + 1) * Staged<D>::kBytes) + lane * 16};
+      store(next);
+      load(tile + 2 * C::kUnits);
+      __syncthreads();
+      uint8_t* const done = now;
+      now = next;
+      next = done;
+    }
+  } else {
+    // A tile is one unit.  While unit i is added up, the logits of unit i + 1 are
+    // made.  Of three buffers, a turn writes that of unit i + 1, last read (as
+    // values) two turns before: before the barrier of the turn before.
+    static_assert(!C::kOverlap || C::kUnits == 1, "one unit");
+    uint8_t* spare = s_kv + 2 * C::kTileBytes;
+    f32x4_t y[C::R][2];
+    if (active && first < end) {
+      f32x4_t s[C::R][2];
+      const bool held = mine.held(first);
+      z.logits(Staged<D>{now + lane * 16}, s);
+      if (!z.whole(first * 32, held)) z.mask(s, first * 32, held);
+      if (z.exponents(s, y)) z.raise(s, y);
+    }
+    for (int u = first; u < end; ++u) {
+      store(next);
+      load(u + 2);
+      __syncthreads();
+      if (active) {
         const bool held = u + 1 < end && mine.held(u + 1);  // past the end: what lies there is masked
         f16x8_t pr[C::R];
         f32x4_t s[C::R][2];
         z.probabilities(y, pr);
-        z.logits(after, s);
-        z.add(at, pr);
-        if (!last) store(next);
+        z.logits(Staged<D>{next + lane * 16}, s);
+        z.add(Staged<D>{now + lane * 16}, pr);
         if (!z.whole(u * 32 + 32, held)) z.mask(s, u * 32 + 32, held);
         if (z.exponents(s, y)) z.raise(s, y);
-      } else if (!last) {
-        store(next);
       }
+      uint8_t* const done = now;
+      now = next;
+      next = spare;
+      spare = done;
     }
-    uint8_t* const done = now;
-    now = next;
-    next = spare;
-    spare = done;
   }
 
   z.finish();
@@ -943,7 +970,7 @@ hipError_t run_rows(const KvAttend& a, const KvPlan& p, float* partial, float2* 
 
 template <int D>
 hipError_t run_tiles(const KvAttend& a, const KvPlan& p, float* partial, float2* stats, hipStream_t stream) {
-  constexpr size_t lds = 3 * Tiles<D>::kTileBytes;
+  constexpr size_t lds = Tiles<D>::kBuffers * Tiles<D>::kTileBytes;
   const hipError_t e = set_lds_limit<k_kv_tiles<D>>(lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((k_kv_tiles<D>), dim3((unsigned)((p.blocks + p.parts) * a.heads)), dim3(512), lds, stream, a,
