@@ -274,7 +274,7 @@ def test_attention_of_many_sequences(b, longest):
 
 
 @pytest.mark.parametrize("d,rows", PATHS)
-@pytest.mark.parametrize("size,scale", [(0.0, 1.0), (1e-30, 1.0), (30.0, None), (1.0, -0.3), (1.0, 0.0), (2e38, 1e-38), (1.0, 1e-30)])
+@pytest.mark.parametrize("size,scale", [(0.0, 1.0), (1e-30, 1.0), (30.0, None), (1.0, -0.3), (1.0, 0.0), (2e38, 1e-38), (1.0, 1e-30), (1e-39, 1e37)])
 def test_attention_of_small_and_large_logits(d, rows, size, scale):
     lens, new = [150, 700], [40, 33]
     pages = _table_for(rows, lens, new, 3, 1, d, 32, 0)
