@@ -905,32 +905,37 @@ __global__ __launch_bounds__(1024) void k_kv_join(KvAttend a, int parts, int lea
     if (row >= rows) break;
     const float2* st = stats + slot0 + i;
     const float* src = partial + (slot0 + i) * D + d;
+    // 8 AT_ONCE parts, asked for before their weights are; past the last part: that one again, with a weight of 0
+    float4 x[8];
+    auto load = [&](int n0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = *reinterpret_cast<const float4*>(src + min(n0 + sub + k * AT_ONCE, block_parts - 1) * step * D);
+    };
+    load(0);
     float m = kLow;
     for (int n = lane; n < block_parts; n += 64) m = fmaxf(m, st[n * step].x);
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-    float l = 0.0f, o[4] = {};
-    for (int n0 = 0; n0 < block_parts; n0 += 64) {
-      const int count = min(64, block_parts - n0);
-      float f = 0.0f;
-      if (lane < count) {
-        const float2 z = st[(n0 + lane) * step];
-        f = __builtin_amdgcn_exp2f(z.x - m);
-        l = __builtin_fmaf(z.y, f, l);
-      }
-      for (int n = sub; n - sub < count; n += 8 * AT_ONCE) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // past the last part: that one again, with a weight of 0
-          const float weight = __shfl(f, (n + k * AT_ONCE) & 63, 64);
-          const float used = n + k * AT_ONCE < count ? weight : 0.0f;
-          const float4 x = *reinterpret_cast<const float4*>(src + (n0 + min(n + k * AT_ONCE, count - 1)) * step * D);
-          o[0] = __builtin_fmaf(x.x, used, o[0]);
-          o[1] = __builtin_fmaf(x.y, used, o[1]);
-          o[2] = __builtin_fmaf(x.z, used, o[2]);
-          o[3] = __builtin_fmaf(x.w, used, o[3]);
+    float l = 0.0f, o[4] = {}, f = 0.0f;
+    for (int n0 = 0; n0 < block_parts; n0 += 8 * AT_ONCE) {
+      if (n0 % 64 == 0) {  // the weights of 64 parts, one per lane
+        f = 0.0f;
+        if (n0 + lane < block_parts) {
+          const float2 z = st[(n0 + lane) * step];
+          f = __builtin_amdgcn_exp2f(z.x - m);
+          l = __builtin_fmaf(z.y, f, l);
         }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float weight = __shfl(f, n0 % 64 + sub + k * AT_ONCE, 64);
+        o[0] = __builtin_fmaf(x[k].x, weight, o[0]);
+        o[1] = __builtin_fmaf(x[k].y, weight, o[1]);
+        o[2] = __builtin_fmaf(x[k].z, weight, o[2]);
+        o[3] = __builtin_fmaf(x[k].w, weight, o[3]);
+      }
+      if (n0 + 8 * AT_ONCE < block_parts) load(n0 + 8 * AT_ONCE);
     }
     l = wave_sum(l);
 #pragma unroll
