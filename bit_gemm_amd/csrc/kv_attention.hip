@@ -28,7 +28,8 @@
 namespace nvfp4 {
 namespace {
 
-constexpr float kLow = -1e37f;  // the bound before a row has seen a token
+constexpr float kLow = -3e38f;  // the bound before a row has seen a token
+constexpr float kFine = 1.0f / 4096;  // bounds past 15 / kFine: see Rows::exponents
 
 // Inclusive sums over the lanes of a wave (all active), in six cross-lane adds.
 template <int CTRL, int ROWS_>
@@ -440,11 +441,14 @@ struct Rows {
         }
   }
 
-  // Logits in powers of two over the rows' bounds; true: some passed 15 and the bounds must be raised.
+  // Logits in powers of two over the rows' bounds; true: some passed 15 and the
+  // bounds must be raised, or a bound lies so far out (beyond 61440) that the
+  // rounding of m and not of the logits would decide: `raise` makes the exponents then.
   __device__ __forceinline__ bool exponents(const f32x4_t (&s)[R][2], f32x4_t (&y)[R][2]) const {
     float top = 0.0f;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r) {
+      top = fmaxf(top, fabsf(m[r]) * kFine);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -452,10 +456,14 @@ struct Rows {
         top = fmaxf(fmaxf(top, y[r][h][0]), y[r][h][1]);
         top = fmaxf(fmaxf(top, y[r][h][2]), y[r][h][3]);
       }
+    }
     return __any(top > 15.0f);
   }
 
   // Raises the bounds of rows with a logit 15 above to 7 below their largest.
+  // The exponents then: a logit is rounded before its bound is taken off, as the
+  // bound's was, so that the row's largest comes out between 0 and 15 whatever
+  // its magnitude, and equal logits alike.
   __device__ __forceinline__ void raise(const f32x4_t (&s)[R][2], f32x4_t (&y)[R][2]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -471,8 +479,11 @@ struct Rows {
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int t = 0; t < T; ++t) acc[r][p][t] *= shrink;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[r][h][i] = s[r][h][i] * factor[r] - m[r];  // (two roundings: no contraction)
     }
-    exponents(s, y);
   }
 
   __device__ __forceinline__ void probabilities(const f32x4_t (&y)[R][2], f16x8_t (&pr)[R]) {

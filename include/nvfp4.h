@@ -558,14 +558,14 @@ NVFP4_API int nvfp4_add_rmsnorm_backward(const void* dh, const void* s, const vo
  * values from their own, per block as nvfp4_quantize_act with s_t = the head's
  * scale; queries are rounded to bf16.
  * k, v       device bf16 [tokens, heads, head_dim], tokens k_stride (v_stride)
- *            elements apart (a multiple of 8; they may be columns of one
- *            matrix), 16-byte aligned.
+ *            elements apart (a multiple of 8, at most 2^34; they may be columns of
+ *            one matrix), 16-byte aligned.
  * q, q_out   device bf16 [tokens, q_heads, head_dim] likewise, or both NULL;
  *            q_out may be q with the same stride.
  * positions  device int32 [tokens]; with rope_dim > 0.
  * rope       device fp32 [max_positions, rope_dim], 16-byte aligned, at least one
- *            row with rope_dim > 0: rope_dim / 2 cosines, then the sines.  A position outside the table gives
- *            NaN.
+ *            row with rope_dim > 0: rope_dim / 2 cosines, then the sines.  A
+ *            position outside the table gives NaN.
  * rope_dim   0 (no rotation) .. head_dim, a multiple of 32.
  * slots      a token whose slot is not in the cache (a negative one, say) is
  *            left out: neither the cache nor its row of q_out is written.
@@ -618,8 +618,9 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  *            fp32 [tokens, q_heads] or NULL.
  * workspace  >= nvfp4_kv_attention_workspace_size bytes, 16-byte aligned (0
  *            bytes for short contexts: NULL allowed, one launch); one_each: q_starts is NULL.
- * Logits and the softmax's sums are fp32; the products are exact in their fp16
- * operands but for p, rounded to fp16 (11 bits).  Lengths are read on the
+ * Logits and the softmax's sums are fp32 (a logit below -2e38 counts as not
+ * seen); the products are exact in their fp16 operands but for p, rounded to
+ * fp16 (11 bits).  Lengths are read on the
  * device alone: a captured call follows them.  The order of the sums is fixed
  * for given sizes and lengths.
  */

@@ -286,6 +286,54 @@ def test_attention_of_small_and_large_logits(d, rows, size, scale):
     check_attention(s, new, q, out, lse, scale)
 
 
+@pytest.mark.parametrize("d,rows", PATHS)
+@pytest.mark.parametrize("logit", [3e4, 1e6, -1e6, 7e8, -7e8, 3e12, -1e20, 2e37, -2e37, -2e38])
+def test_attention_of_logits_past_the_steps_of_fp32(d, rows, logit):
+    """Logits whose neighbours in fp32 are further apart than exponentials tell: the largest ones share the row alike,
+    in whichever units they lie.  Keys are 4 (held as 6 * 0.6875) or 6 in one element and a logit's rounding is common to equal
+    keys; the p of the others are 0.  The larger ones' p are equal but for p's rounding to fp16 (2^-11) and what an
+    exponential is off (2^-16, as in `bounds`); the quotient is rounded to bf16 (2^-8)."""
+    n, new = 1500, 70
+    pages = _table_for(rows, [n], [new], 4, 1, d, 32, 0)
+    print("kv attention logits", d, rows, logit, flush=True)
+    rng = np.random.default_rng(6)
+    k, v = np.zeros((n, 1, d)), rng.choice([0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], (n, 1, d)) * rng.choice([-1.0, 1.0], (n, 1, d))
+    v[:, 0, ::16] = 6.0  # every block's scale is 1
+    large = rng.random(n) < 0.03
+    large[:40], large[41] = False, True  # (the first of them behind the first unit)
+    best = 6.0 if logit > 0 else 4.0
+    k[:, 0, 5] = np.where(large, best, 10.0 - best)
+    cache = nv.KVCache.empty(-(-n // 32), 32, 1, d)
+    nv.kv_append(cache, bf16(k).cuda(), bf16(v).cuda(), torch.arange(n, dtype=torch.int32, device="cuda"))
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    table[0, : cache.pages] = torch.arange(cache.pages)
+    q = torch.zeros(new, 4, d, dtype=torch.bfloat16)
+    q[:, :, 5] = torch.tensor([logit / 6.0, logit / 5.0, logit / 4.0, logit / 3.0]).bfloat16()
+    scale = 0.75
+    out, lse = nv.kv_attention(q.cuda(), cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), starts([new]),
+                               scale=scale, return_lse=True)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    held = {6.0: 6.0, 4.0: 4.125}[best]
+    for t in range(new):
+        at = np.flatnonzero(large[: n - new + t + 1])
+        want = v[at, 0].mean(0)
+        rounded = (2.0 ** -11 + 2.0 ** -16) * np.abs(v[at, 0]).mean(0)
+        assert (np.abs(out[t] - want) <= rounded + 2.0 ** -8 * (np.abs(want) + rounded)).all(), t
+        top = q[t, :, 5].double().numpy() * held * scale
+        assert (np.abs(lse[t] - top - np.log(len(at))) <= 2.0 ** -21 * np.abs(top) + 2.0 ** -20).all(), t
+
+
+@DIMS
+@pytest.mark.parametrize("b,hq,hkv", [(300, 2, 1), (600, 40, 1)])
+def test_attention_of_many_single_tokens(d, b, hq, hkv):
+    rng = np.random.default_rng(b + d)
+    lens = [int(x) for x in rng.integers(0, 90, b)]
+    s = Sequences(b, lens, hkv, d, 32).append()
+    q = queries(9, b, hq, d)
+    out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, return_lse=True)
+    check_attention(s, [1] * b, q, out, lse, d ** -0.5)
+
+
 def test_attention_keeps_many_small_probabilities():
     """One token of probability 1 and 60000 whose own is about 2^-24 each: together 2^-8 of the row's sum, which fp16
     probabilities below 2^-24 would lose."""
