@@ -31,11 +31,11 @@ int done(hipError_t e, const char* where) { return e == hipSuccess ? NVFP4_OK : 
 
 constexpr int64_t kMaxHeads = 65536;
 constexpr int64_t kMaxSlots = ((int64_t)1 << 31) - 1;  // slots are int32
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 34;  // spans of kMaxTokens rows stay below 2^63 bytes
 constexpr int64_t kMaxTokens = (int64_t)1 << 27;
 constexpr int64_t kMaxSequences = 65536;
 constexpr int64_t kMaxRows = (int64_t)1 << 30;  // of a call of attention: numbered by int32
-constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of 256 threads: a launch stays below 2^32 work-items
+constexpr int64_t kMaxGroups = (int64_t)1 << 24;  // of 256 threads, half of it of 512: a launch stays below 2^32 work-items
 
 int page_shift(int64_t page_size) {
   int s = 0;
@@ -70,7 +70,7 @@ int check_cache(const void* cache, int64_t pages, int64_t page_size, int64_t hea
 int check_rows(const void* p, int64_t stride, int64_t width, const char* name) {
   if (!p) return fail(NVFP4_ERR_INVALID_VALUE, "%s is required", name);
   if (stride < width || stride > kMaxStride)
-    return fail(NVFP4_ERR_INVALID_VALUE, "%s's stride %lld: at least its %lld elements, at most 2^40", name,
+    return fail(NVFP4_ERR_INVALID_VALUE, "%s's stride %lld: at least its %lld elements, at most 2^34", name,
                 (long long)stride, (long long)width);
   if (stride % 8 != 0 || !aligned(p, 16))
     return fail(NVFP4_ERR_MISALIGNED, "%s must be 16-byte aligned, its stride a multiple of 8", name);
@@ -281,7 +281,7 @@ NVFP4_API int nvfp4_kv_attention(const void* q, int64_t q_stride, const uint8_t*
   if (pages == 0 && table_pages > 0) return fail(NVFP4_ERR_INVALID_VALUE, "a page table without pages");
   const nvfp4::KvPlan plan = nvfp4::plan_kv_attention(sequences, tokens, q_heads, heads, (int)head_dim,
                                                       table_pages * page_size, window, q_starts == nullptr);
-  if ((plan.blocks + plan.parts) * heads >= kMaxGroups)
+  if ((plan.blocks + plan.parts) * heads >= (plan.tiles ? kMaxGroups : kMaxGroups / 2))
     return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, "%lld tokens of %lld heads in one call", (long long)tokens,
                 (long long)q_heads);
   if (plan.ws_bytes > 0) {

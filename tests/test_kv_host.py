@@ -76,6 +76,12 @@ def test_append_refuses_overlaps(L):
         assert _append(L, **wide, qo=AT["q"] + 2 * row) > ok
 
 
+def test_strides_past_any_memory(L):
+    """Refused before spans of rows are computed, which would pass 64 bits."""
+    for name in ("kst", "vst", "qst", "qost"):
+        assert _append(L, **{name: (1 << 34) + 8}) == 1 and "2^34" in L.nvfp4_last_error().decode(), name
+
+
 def test_read(L):
     def f(**o):
         a = dict(cache=AT["cache"], pages=10, page=64, h=8, d=128, ks=AT["ks"], vs=AT["vs"], slots=AT["slots"], t=5,
@@ -116,6 +122,16 @@ def test_attention(L):
                 (3, 5, 32, 8, 128, 64, 64, 0, 1), (3, 5, 32, 8, 128, 64, 0, 0, 0), (3, 0, 32, 8, 128, 64, 64, 0, 0),
                 (3, 5, 32, 8, 128, 64, 64, -1, 0)):
         assert size(*bad) == 0, bad
+
+
+def test_attention_refuses_more_work_items_than_a_launch_holds(L):
+    """More workgroups of 256 threads than 2^24, of 512 (the tiles) than 2^23: below them memory is what bounds a call."""
+    h, b = 256, 1 << 15  # 2^23 pairs of a sequence and a head, 128 rows and more of each pair
+    t = (1 << 30) // h
+    assert L.nvfp4_kv_attention_path(b, t, h, h, 128, 64, 4, 0, 0) == 256
+    assert L.nvfp4_kv_attention(AT["q"], h * 128, 1 << 41, 10, 64, h, 128, AT["ks"], AT["vs"], AT["table"], 4, AT["lens"],
+                                AT["starts"], b, t, h, 0.1, 1, 0, 1 << 42, None, None, 0, None) == 2
+    assert "in one call" in L.nvfp4_last_error().decode()
 
 
 def test_binding_refuses():
