@@ -111,6 +111,15 @@ template <int ROWS, bool BLOCK>
 __device__ bool find(const KvAttend& a, int parts, int least, int number, Item& w) {
   const int lane = threadIdx.x & 63;
   w.part_units = 1 << 28;
+  if (!a.starts && parts == 0) {  // one token each, no context split: as many row blocks in every sequence
+    w.blocks = (a.group + ROWS - 1) / ROWS;
+    w.index = number / w.blocks;
+    w.local = number - w.index * w.blocks;
+    w.base = 0;
+    if (w.index >= a.sequences) return false;
+    w.seq = sequence(a, w.index);
+    return true;
+  }
   if (a.sequences == 1) {
     w.index = w.base = 0;
     w.local = number;
