@@ -1046,10 +1046,16 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   const int rows = kv_block_rows(p, head_dim);
   p.blocks = block_count(sequences, tokens, group, rows, one_each);
   // The second launch takes 4 to 6 us, what a workgroup needs for 32 units.  One
-  // sequence of 1024 tokens of 8 heads: 9.2 us whole, 9.6 split; of 2048 14.4,
-  // 10.9; 32 of 1024 12.6, 17; 32 of 2048 21.9, 24.6.
+  // sequence of 1024 tokens of 8 heads: 9.2 us whole, 9.6 split; of 2048 13.0,
+  // 10.9; 8 of 2048 14.7, 14.2; 12 15.1, 16.6; 20 16.7, 20.3; 4 heads of 256, 16
+  // of 2048 22.1, 18.8, 24 25.0, 24.9.  Past 64 units as long as workgroups
+  // are few: 40 sequences of 1 to 4096 tokens of 8 heads 48, 31; 64 51, 42; 80
+  // 55, 53 (all of 4096: 76, 86); 100 61, 69.  A table of more than 8192 tokens
+  // may hold one context far longer than the rest, which a workgroup alone would
+  // take long for: split up to 1024 (100 of 1 to 8192 114 us whole, 123).
   const int64_t items = p.blocks * heads;
-  const bool split = units > (items < 192 ? 32 : 64) && items < (p.tiles ? 1024 : 256);
+  const bool split =
+      units > (items < (head_dim == 256 ? 96 : 64) ? 32 : 64) && items < (!p.tiles ? 256 : units > 256 ? 1024 : 640);
   // Long contexts that are not split, on a GPU that is not full: eight waves to
   // a workgroup.  24 sequences with windows of 1024: 10.4 us with 4, 9.3; 32 of
   // 2048 22.5, 20; but 8 of 300 tokens 5.5, 5.9.
