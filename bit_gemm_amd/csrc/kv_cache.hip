@@ -149,8 +149,8 @@ __device__ __forceinline__ void store_value(uint8_t* unit, int t, int b, uint2 c
 // (their bytes of a unit share cache lines).  The other workgroups rotate
 // queries.  A token that is left out is computed and not stored, so that its
 // inputs are asked for beside its slot and not after it.  Bound by bandwidth:
-// 4096 tokens of 32 heads each of q, k and v take 35 us (153 MB, 4.4 TB/s), one
-// token 3.5.  Threads that turn two or four heads by the angles they read once
+// 4096 tokens of 32 heads each of q, k and v take 35 us (155 MB, 4.4 TB/s), one
+// token 3.3.  Threads that turn two or four heads by the angles they read once
 // take 34 us for the 4096 tokens, and 4.2 and 6 for one.
 template <int D, bool INTERLEAVED>
 __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256) void k_kv_append(KvAppend a) {
 }
 
 // A thread per 16 bytes of output: 8 elements in bf16, 4 in fp32 (neighbouring
-// lanes then store whole lines: 32768 tokens of 8 heads of 128 take 34 us, 5.1
+// lanes then store whole lines: 32768 tokens of 8 heads of 128 take 33 us, 5.2
 // TB/s; with a thread for each block of 16 they took 48).
 template <int D, bool F32>
 __global__ __launch_bounds__(256) void k_kv_read(KvRead a) {
