@@ -1002,7 +1002,8 @@ def kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Ten
               q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
     """Write bf16 [tokens, heads, head_dim] keys and values into the cache's
     slots (int32 [tokens], page * page_size + place in the page; a token whose
-    slot is negative or past the cache is left out).
+    slot is negative or past the cache is left out; two tokens of one call must
+    not have the same slot).
 
     With rope (float32 [max_positions, rope_dim]: cosines, then sines) keys
     and q (bf16 [tokens, q_heads, head_dim]) are first rotated by their
@@ -1088,7 +1089,9 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_l
     only its last `window` tokens.  Returns out, bf16 like q, or with
     return_lse (or lse) also the float32 [tokens, q_heads] logarithms of the
     softmax's sums.  Rows that see nothing are 0 and -inf; rows behind the
-    last sequence are left as they were in out and lse."""
+    last sequence are left as they were in out and lse.  workspace: uint8 of
+    kv_attention_workspace_size bytes, a new one by default; calls that may run
+    at once need one each."""
     pages, heads, index = _kv_cache(cache)
     d = cache.head_dim
     n, q_heads, q_stride = _token_rows(q, "q", d, index)
