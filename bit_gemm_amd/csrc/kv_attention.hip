@@ -598,7 +598,7 @@ struct RowOut {
 // A workgroup takes 16 R rows and a part of their context; its waves take the
 // part's units in turn, decode them in registers and add up at the end.  Bound
 // by HBM where the context is long: one token on 131072 of 8 heads (151 MB) is
-// read in 32 us, 4.7 TB/s, what a copy reaches; with few units by latency (lens,
+// read in 32.6 us, 4.6 TB/s (a copy: 4.76); with few units by latency (lens,
 // page numbers, the first unit, the sums: about 7 us).  With more rows the
 // decoding bounds it, 64 conversions and as many products a unit: 4096 tokens,
 // 32 heads in groups of 4, take 252 us with R = 1, 192 with 2.
@@ -762,7 +762,7 @@ struct Share {
 // together into LDS operands, a share of a unit each, so that a unit is decoded
 // once for 256 (128) rows.  Two waves to a SIMD: 200 registers at R = 2, and
 // with R = 1 and four waves LDS is read twice as often (the same prompt 166 us).
-// 4096 tokens, 32 heads in groups of 4: 145 us, 0.95 PFLOP/s; 16384: 2.0 ms, 1.1
+// 4096 tokens, 32 heads in groups of 4: 147 us, 0.94 PFLOP/s; 16384: 2.0 ms, 1.1
 // (the library's fp16 8192^3 product 1.15).  The matrix cores work a third of
 // the time, the vector units half; the rest is waiting, mostly for LDS.
 template <int D>
@@ -775,7 +775,8 @@ struct Tiles {
   // There the logits of a unit are made while the one before is added up (which
   // reads a tile ahead and takes a third buffer): 4096 tokens of 16 heads in
   // groups of 4 take 169 us, unit by unit 181.  Head_dim 128, 32 heads: 150 and,
-  // unit by unit with the values asked for, 145.
+  // unit by unit with the values asked for, 145 (147
+  // since bounds far out are looked for).
   static constexpr bool kOverlap = D == 256;
   static constexpr int kBuffers = kOverlap ? 3 : 2;
 };
