@@ -380,12 +380,14 @@ struct Rows {
         }
       top = fmaxf(top, __shfl_xor(top, 16, 64));
       top = fmaxf(top, __shfl_xor(top, 32, 64));
-      // 2^e, e = 14 - floor(log2(top)) as far as fp32 goes; rows with an infinity keep theirs
+      // 2^e, e = 14 - floor(log2(top)) as far as fp32 goes
       const int exponent = (int)(__float_as_uint(top) >> 23);
       const int e = exponent == 255 ? 0 : min(14 + 127 - exponent, 126);
       const float up = __uint_as_float((uint32_t)(127 + e) << 23);
       factor[r] = (float)(base * (double)__uint_as_float((uint32_t)(127 - e) << 23));
-      const float sign = factor[r] < 0.0f ? -up : up;
+      // With an infinity (or a NaN) in the row every logit is an infinity or a NaN, and so is the softmax NaN, also of
+      // logits that are all -inf, which the kernels take for tokens not seen: the whole row is made NaN.
+      const float sign = exponent == 255 ? __builtin_nanf("") : factor[r] < 0.0f ? -up : up;
       factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
 #pragma unroll
       for (int p = 0; p < P; ++p) {

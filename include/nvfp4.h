@@ -600,7 +600,8 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  *   lse = log sum_j p_j
  * over the visible tokens j: all of the context; with causal j <= kv_len - n +
  * i; with window > 0 also j > kv_len - n + i - window.  Rows that see nothing
- * (kv_len 0, or fewer than the new tokens): out = 0, lse = -infinity.
+ * (kv_len 0, or fewer than the new tokens): out = 0, lse = -infinity.  A row of
+ * q that holds an infinity or a NaN is NaN in out and lse wherever it sees a token.
  *
  * q          device bf16 [tokens, q_heads, head_dim], tokens q_stride elements
  *            apart (a multiple of 8), 16-byte aligned.

@@ -1,0 +1,74 @@
+"""Attention over the NVFP4 key/value cache at the ends of its numbers' range:
+infinities and NaN in queries, rows of queries of very different sizes, head
+scales next to fp32's least, factors past its largest."""
+
+import numpy as np
+import pytest
+import torch
+
+import bit_gemm_amd as nv
+import oracle.kv as okv
+from kv_cases import Sequences, check_attention, queries, starts
+from test_gpu_kv import PATHS, _table_for
+
+pytestmark = pytest.mark.gpu
+
+EVERY_PATH = pytest.mark.parametrize("d,rows", PATHS)
+INF, NAN = float("inf"), float("nan")
+
+
+# ------------------------------------------------- infinities and NaN in queries
+
+
+@EVERY_PATH
+@pytest.mark.parametrize("scale", [None, -0.3, 0.0])
+def test_queries_that_are_not_finite_give_nan(d, rows, scale):
+    """A row of q that holds an infinity or a NaN is NaN in out and lse wherever it sees a token: each of its logits is
+    NaN or an infinity, also where all of them are -inf.  Rows that see nothing are as without it, and so are all other
+    rows within the bounds of any row: rows of one wave raise their bounds together, and the exponent of a logit is
+    s f - m rounded once where none is raised and s f rounded before m is taken off where one is, so that a neighbour's
+    NaN may change a row by such a rounding (2^-24 of the logit), which `bounds` counts."""
+    lens, new = [70, 200, 5], [40, 150, 9]
+    pages = _table_for(rows, lens, new, 4, 2, d, 32, 0)
+    print("kv attention infinite queries", d, rows, scale, flush=True)
+    s = Sequences(31, lens, 2, d, 32, table_pages=pages)
+    for k in s.k:
+        k[:, :, 3], k[:, :, 4] = 50.0, -50.0  # of one sign each in every token
+        k[:, :, 16:32] = 0.0
+    s.append()
+    q = queries(32, sum(new), 4, d)
+    bad = q.clone()
+    at = {(1, 0): {3: -INF}, (5, 1): {3: INF}, (17, 2): {4: INF}, (39, 3): {7: NAN}, (40, 0): {20: INF}, (63, 1): {d - 1: -INF},
+          (100, 2): {3: INF, 4: INF}, (101, 3): {3: -INF, 4: INF}, (189, 0): {3: -INF, 9: NAN}, (188, 0): {4: -INF},
+          (190, 1): {3: -INF}, (193, 3): {5: NAN}, (194, 0): {3: -INF}, (198, 2): {4: INF}}  # 190 .. 193 see nothing
+    poisoned = torch.zeros(sum(new), 4, dtype=torch.bool)
+    for (t, h), elements in at.items():
+        for i, x in elements.items():
+            bad[t, h, i] = x
+        poisoned[t, h] = not 190 <= t < 194
+    args = s.cache, s.table, s.kv_lens, starts(new)
+    scale = d ** -0.5 if scale is None else scale
+    want, want_lse = nv.kv_attention(q.cuda(), *args, scale=scale, return_lse=True)
+    out, lse = nv.kv_attention(bad.cuda(), *args, scale=scale, return_lse=True)
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), poisoned) and torch.equal(torch.isnan(lse).cpu(), poisoned)
+    at = poisoned.cuda()
+    check_attention(s, new, q, torch.where(at[..., None], want, out), torch.where(at, want_lse, lse), scale)
+    assert (out[190:194] == 0).all() and torch.isneginf(lse[190:194]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_that_are_not_finite_over_a_split_context(d):
+    s = Sequences(33, [5000, 3000], 1, d, 32)
+    for k in s.k:
+        k[:, :, 3] = 50.0
+    s.append()
+    q = queries(34, 2, 8, d)
+    bad = q.clone()
+    bad[0, 1, 3], bad[0, 2, 3], bad[1, 7, 9] = -INF, INF, NAN
+    assert nv.kv_attention_workspace_size(2, 2, 8, 1, d, 32, s.table.shape[1], 0, True) > 0
+    want, want_lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, return_lse=True)
+    out, lse = nv.kv_attention(bad.cuda(), s.cache, s.table, s.kv_lens, return_lse=True)
+    at = torch.zeros(2, 8, dtype=torch.bool, device="cuda")
+    at[0, 1] = at[0, 2] = at[1, 7] = True
+    assert torch.equal(torch.isnan(out).all(-1), at) and torch.equal(torch.isnan(lse), at)
+    check_attention(s, [1, 1], q, torch.where(at[..., None], want, out), torch.where(at, want_lse, lse), d ** -0.5)
