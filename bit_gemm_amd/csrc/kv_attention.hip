@@ -557,12 +557,15 @@ struct Rows {
   }
 };
 
-// A row of the output: where it lies, its sums' bound and total.
+// A row of the output: where it lies, its sums' bound and total.  The sums are
+// multiplied by f = v_scale / l.  l is up to 2^15 a token, so next to fp32's least
+// v_scale the quotient is made of v_scale 2^100, exact, and 2^-100 taken off after
+// it (`drop`); elsewhere drop is 1 and changes nothing.
 template <int D>
 struct RowOut {
   uint16_t* to;
   float* lse;
-  float m, l, f;
+  float m, l, f, drop;
 
   __device__ __forceinline__ RowOut(const KvAttend& a, const Sequence& s, int row, int head, float m_, float l_)
       : m(m_), l(l_) {
@@ -570,7 +573,10 @@ struct RowOut {
     const int64_t at = (int64_t)(s.first + t) * (a.heads * a.group) + head * a.group + (row - t * a.group);
     to = a.out + at * D;
     lse = a.lse ? a.lse + at : nullptr;
-    f = l == 0.0f ? 0.0f : a.v_scale[head] / l;  // l is 0 where nothing is visible, and NaN where a visible token is
+    const float scale = a.v_scale[head];
+    const bool small = scale < 0x1p-40f;
+    drop = small ? 0x1p-100f : 1.0f;
+    f = l == 0.0f ? 0.0f : (small ? scale * 0x1p100f : scale) / l;  // l is 0 where nothing is visible, and NaN where a visible token is
   }
   // Elements [d, d + E).
   template <int E>
@@ -579,7 +585,7 @@ struct RowOut {
     uint32_t w[E / 2];
 #pragma unroll
     for (int i = 0; i < E; i += 2) {
-      const bf16x2_t v = {(__bf16)(o[i] * f), (__bf16)(o[i + 1] * f)};
+      const bf16x2_t v = {(__bf16)(o[i] * f * drop), (__bf16)(o[i + 1] * f * drop)};
       w[i / 2] = __builtin_bit_cast(uint32_t, v);
     }
     if constexpr (E == 8)

@@ -72,3 +72,29 @@ def test_queries_that_are_not_finite_over_a_split_context(d):
     at[0, 1] = at[0, 2] = at[1, 7] = True
     assert torch.equal(torch.isnan(out).all(-1), at) and torch.equal(torch.isnan(lse), at)
     check_attention(s, [1, 1], q, torch.where(at[..., None], want, out), torch.where(at, want_lse, lse), d ** -0.5)
+
+
+# ------------------------------------------------------------ factors
+
+
+@EVERY_PATH
+@pytest.mark.parametrize("power", [-100, -119, -122])
+def test_value_scales_next_to_the_least(d, rows, power):
+    """Values and their head's scale times 2^power: the same codes, the output 2^power of what it was."""
+    lens, new = [150, 2700], [40, 33]
+    pages = _table_for(rows, lens, new, 3, 2, d, 32, 0) if rows != 16 else -(-max(lens) // 32)
+    print("kv attention value scales", d, rows, power, flush=True)
+    s = Sequences(37, lens, 3, d, 32, table_pages=pages)
+    s.v = [(v.float().clamp(-30, 30).bfloat16()) for v in s.v]
+    s.append()
+    q = queries(38, sum(new), 3, d)
+    want, want_lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, starts(new), return_lse=True)
+    cache = nv.KVCache(s.cache.data, s.cache.k_scale, s.cache.v_scale * 2.0 ** power, d, 32)
+    out, lse = nv.kv_attention(q.cuda(), cache, s.table, s.kv_lens, starts(new), return_lse=True)
+    assert torch.equal(lse, want_lse)
+    # the scale times 2^power may be subnormal: the output then goes with what is left of it
+    ratio = (cache.v_scale.double() / s.cache.v_scale.double())[None, :, None]
+    exact = want.double() * ratio
+    # each side rounded to bf16 once, the quotients of fp32 before; subnormal results to steps of 2^-133
+    assert ((out.double() - exact).abs() <= 2.0 ** -7 * (1 + 2.0 ** -8) * exact.abs() + 2.0 ** -133).all()
+    assert (out != 0).any()
