@@ -9,8 +9,10 @@
 // S, one per head, goes into the logits' factor and the output's.
 //   S^T = K Q^T  (16 tokens x 16 rows per instruction) on fp16 matrix
 //       instructions, accumulated in fp32.  A row of q is scaled by the power
-//       of two that brings its largest element to [2^14, 2^15): its elements
-//       down to 2^-38 of that are exact in fp16.
+//       of two that brings its largest element to [2^14, 2^15): a bf16 element
+//       down to 2^-31 of that is exact in fp16.  Where a wave has a row with
+//       smaller elements, both operands are bf16 (6 bits of a key fit its 8) and
+//       the largest element is brought to [2^60, 2^61): exact down to 2^-186.
 //   p = 2^(y - m), y = S^T * scale * S * log2(e) and m a bound 7 below a
 //       running maximum that is raised only when some y passes m by 15: p stays
 //       below 2^15 and is rounded to fp16 to within 2^-12 relative or 2^-32 of
@@ -22,6 +24,7 @@
 //  k_kv_tiles many rows: 8 waves decode the units together into LDS
 //  k_kv_join  adds the parts of the rows whose context was split
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_device.h"
 
@@ -29,6 +32,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr float kLow = -3e38f;  // the bound before a row has seen a token
+constexpr int kPoisoned = 1 << 20;  // in the place of a row's power of two: it is not finite
+constexpr int kWide = 46;  // of rows of q in bf16: powers of two above those in fp16
 constexpr float kFine = 1.0f / 4096;  // bounds past 15 / kFine: see Rows::exponents
 
 // Inclusive sums over the lanes of a wave (all active), in six cross-lane adds.
@@ -348,11 +353,12 @@ struct Units {
 template <int D, int R>
 struct Rows {
   static constexpr int P = Unit<D>::P, N = D == 64 ? 2 : 4, T = 2 * N;  // K steps and tiles of V per panel
-  f16x8_t q[R][P][N];  // operands of Q^T: of elements 128 p + 8 N g ..
+  f16x8_t q[R][P][N];  // operands of Q^T: of elements 128 p + 8 N g .. (wide: the bits of bf16)
   f32x4_t acc[R][P][T];
   float factor[R], m[R], l[R];
   int lo[R], hi[R];
   int lo_all, hi_all;  // tokens that every row sees
+  bool wide;           // of the wave
 
   // rows [first, first + 16 R) of a sequence
   __device__ __forceinline__ void start(const KvAttend& a, const Sequence& seq, int first, int head) {
@@ -360,52 +366,85 @@ struct Rows {
     const int rows = seq.count * a.group;
     // in 64 bits: neither it nor its product with a row's power of two may lose bits below fp32's range
     const double base = (double)a.scale * 1.44269504088896340736 * (double)a.k_scale[head];
+    const uint16_t* src[R];
+    int e[R];
+    bool far = false;
+    // read twice, the second time from the cache: fewer registers than held meanwhile
+    auto raw = [&](int r, int p, int n) { return *reinterpret_cast<const u32x4_t*>(src[r] + p * 128 + g * (8 * N) + n * 8); };
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       const int row = min(first + r * 16 + c, rows - 1);  // rows past the last: computed, not stored
       const int t = row / a.group;
       visible(a, seq, t, lo[r], hi[r]);
-      const uint16_t* src = a.q + (int64_t)(seq.first + t) * a.q_stride + (head * a.group + row - t * a.group) * D;
-      // read twice, the second time from the cache: fewer registers than held meanwhile
-      auto raw = [&](int p, int n) { return *reinterpret_cast<const u32x4_t*>(src + p * 128 + g * (8 * N) + n * 8); };
-      float top = 0.0f;
+      src[r] = a.q + (int64_t)(seq.first + t) * a.q_stride + (head * a.group + row - t * a.group) * D;
+      // the bits of the largest magnitude, and of the smallest but zero less 1 (65535: all are zero)
+      u16x2_t top2 = {0, 0}, low2 = {65535, 65535};
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          const u32x4_t x = raw(p, n);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(x[i] << 16)), fabsf(__uint_as_float(x[i] & 0xFFFF0000u))));
-        }
-      top = fmaxf(top, __shfl_xor(top, 16, 64));
-      top = fmaxf(top, __shfl_xor(top, 32, 64));
-      // 2^e, e = 14 - floor(log2(top)) as far as fp32 goes
-      const int exponent = (int)(__float_as_uint(top) >> 23);
-      const int e = exponent == 255 ? 0 : min(14 + 127 - exponent, 126);
-      const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-      factor[r] = (float)(base * (double)__uint_as_float((uint32_t)(127 - e) << 23));
-      // With an infinity (or a NaN) in the row every logit is an infinity or a NaN, and so is the softmax NaN, also of
-      // logits that are all -inf, which the kernels take for tokens not seen: the whole row is made NaN.
-      const float sign = exponent == 255 ? __builtin_nanf("") : factor[r] < 0.0f ? -up : up;
-      factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        float x[8 * N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const u32x4_t y = raw(p, n);
+          const u32x4_t x = raw(r, p, n);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[8 * n + 2 * i] = __uint_as_float(y[i] << 16) * sign;
-            x[8 * n + 2 * i + 1] = __uint_as_float(y[i] & 0xFFFF0000u) * sign;
+            const u16x2_t y = __builtin_bit_cast(u16x2_t, x[i] & 0x7FFF7FFFu);
+            top2 = __builtin_elementwise_max(top2, y);
+            low2 = __builtin_elementwise_min(low2, y - u16x2_t{1, 1});
           }
         }
+      int top = max((int)top2[0], (int)top2[1]), low = min((int)low2[0], (int)low2[1]);
+      top = max(top, __shfl_xor(top, 16, 64));
+      top = max(top, __shfl_xor(top, 32, 64));
+      low = min(low, __shfl_xor(low, 16, 64));
+      low = min(low, __shfl_xor(low, 32, 64));
+      // 2^e, e = 14 - floor(log2(top)) as far as fp32 goes; an element's 8 bits must not pass below fp16's 2^-24 then
+      const int exponent = top >> 7;
+      e[r] = exponent == 255 ? kPoisoned : min(14 + 127 - exponent, 126);
+      far |= exponent != 255 && ((low + 1) >> 7) - 127 + e[r] - 7 < -24;
+    }
+    auto fill = [&](auto wide_) {
+      constexpr bool WIDE = decltype(wide_)::value;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+      for (int r = 0; r < R; ++r) {
+        // With an infinity (or a NaN) in the row every logit is an infinity or a NaN, and so is the softmax NaN, also of
+        // logits that are all -inf, which the kernels take for tokens not seen: the whole row is made NaN.
+        const bool poisoned = e[r] == kPoisoned;
+        const int power = poisoned ? 0 : WIDE ? min(e[r] + kWide, 126) : e[r];
+        const float up = __uint_as_float((uint32_t)(127 + power) << 23);
+        factor[r] = (float)(base * (double)__uint_as_float((uint32_t)(127 - power) << 23));
+        const float sign = poisoned ? __builtin_nanf("") : factor[r] < 0.0f ? -up : up;
+        factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[r][p][n][i] = (_Float16)x[key_element<D>(n, i)];
+        for (int p = 0; p < P; ++p) {
+          float x[8 * N];
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            const u32x4_t y = raw(r, p, n);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[8 * n + 2 * i] = __uint_as_float(y[i] << 16) * sign;
+              x[8 * n + 2 * i + 1] = __uint_as_float(y[i] & 0xFFFF0000u) * sign;
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            if constexpr (WIDE) {
+              bf16x8_t z;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[i] = (__bf16)x[key_element<D>(n, i)];
+              q[r][p][n] = __builtin_bit_cast(f16x8_t, z);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) q[r][p][n][i] = (_Float16)x[key_element<D>(n, i)];
+            }
+          }
+        }
       }
+    };
+    fill(std::false_type{});
+    wide = __any(far);
+    if (__builtin_expect(wide, 0)) fill(std::true_type{});  // again
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
       m[r] = kLow;
       l[r] = 0.0f;
 #pragma unroll
@@ -418,8 +457,8 @@ struct Rows {
     visible(a, seq, (min(first + 16 * R, rows) - 1) / a.group, lo_all, skip);
   }
 
-  template <class Operands>
-  __device__ __forceinline__ void logits(const Operands& x, f32x4_t (&s)[R][2]) {
+  template <bool WIDE, class Operands>
+  __device__ __forceinline__ void products(const Operands& x, f32x4_t (&s)[R][2]) {
 #pragma unroll
     for (int r = 0; r < R; ++r) s[r][0] = s[r][1] = f32x4_t{};
 #pragma unroll
@@ -429,10 +468,29 @@ struct Rows {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
           const f16x8_t k = x.key(p, h, n);
+          if constexpr (WIDE) {
+            bf16x8_t z;
 #pragma unroll
-          for (int r = 0; r < R; ++r)
-            s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][p][n], s[r][h], 0, 0, 0);
+            for (int i = 0; i < 8; ++i) z[i] = (__bf16)(float)k[i];
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(z, __builtin_bit_cast(bf16x8_t, q[r][p][n]), s[r][h], 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              s[r][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[r][p][n], s[r][h], 0, 0, 0);
+          }
         }
+  }
+
+  // FAR: the wave may be a wide one.  A branch for every unit costs a prompt 3 to
+  // 5 %, so the kernels choose between loops with and without it.
+  template <bool FAR, class Operands>
+  __device__ __forceinline__ void logits(const Operands& x, f32x4_t (&s)[R][2]) {
+    if (FAR && __builtin_expect(wide, 0))
+      products<true>(x, s);
+    else
+      products<false>(x, s);
   }
 
   // Whether every row sees all of the unit at token t0.
@@ -523,11 +581,11 @@ struct Rows {
   }
 
   // One unit.  AHEAD: the values' operands are asked for before the softmax.
-  template <bool AHEAD, class Operands>
+  template <bool AHEAD, bool FAR, class Operands>
   __device__ __forceinline__ void attend(const Operands& x, int t0, bool held) {
     f32x4_t s[R][2], y[R][2];
     f16x8_t pr[R], v[P][T];
-    logits(x, s);
+    logits<FAR>(x, s);
     if constexpr (AHEAD) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
@@ -642,12 +700,20 @@ __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts
   for (int n = 0; n < DEPTH; ++n) load(n, u + n * WAVES);
   X z;
   z.start(a, seq, block * ROWS, head);
+  if (__builtin_expect(z.wide, 0)) {  // one unit at a time, in no more registers than the loop below
+    Units<D> again(a, w.index, head);
+#pragma unroll 1
+    for (; u < end; u += WAVES) {
+      x[0].load(again.at(u), lane);
+      z.template attend<false, true>(x[0], u * 32, again.held(u));
+    }
+  }
   for (; u < end; u += DEPTH * WAVES) {
 #pragma unroll
     for (int n = 0; n < DEPTH; ++n) {
       const int at = u + n * WAVES;
       if (at >= end) break;
-      z.template attend<false>(x[n], at * 32, held[n]);
+      z.template attend<false, false>(x[n], at * 32, held[n]);
       load(n, at + DEPTH * WAVES);
     }
   }
@@ -796,6 +862,7 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   using X = Rows<D, C::R>;
   constexpr int P = X::P, T = X::T, ROWS = C::kRows;
   extern __shared__ __align__(16) uint8_t s_kv[];  // kBuffers tiles
+  __shared__ int s_wide[C::kWaves];
 
   const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -813,65 +880,77 @@ __global__ __launch_bounds__(64 * Tiles<D>::kWaves, 2) void k_kv_tiles(KvAttend 
   const int share = wave % Share<D>::kCount, share_of = wave / Share<D>::kCount;  // of unit share_of of a tile
   auto load = [&](int tile) { x.load(ahead.at(min(tile + share_of, end - 1)), share, lane); };
   auto store = [&](uint8_t* to) { x.store(to + share_of * Staged<D>::kBytes + lane * 16, share); };
-  uint8_t *now = s_kv, *next = s_kv + C::kTileBytes;
   if (first < end) load(first);
   X z;
   z.start(a, seq, min(row0, rows - 1), head);
-  store(now);
+  store(s_kv);
+  if (lane == 0) s_wide[wave] = z.wide;
   if (first < end) load(first + C::kUnits);
   __syncthreads();
-  if constexpr (!C::kOverlap) {
-    // While tile i is multiplied, tile i + 1 is on its way from memory; then it
-    // is decoded into the other buffer, which was last read before the barrier
-    // of the turn before.  (Past the end: what the registers hold, never used.)
-    for (int tile = first; tile < end; tile += C::kUnits) {
+  bool any_wide = false;
 #pragma unroll
-      for (int n = 0; n < C::kUnits; ++n) {
-        const int u = tile + n;
-        if (active && u < end)
-          z.template attend<true>(Staged<D>{now + n * Staged<D>::kBytes + lane * 16}, u * 32, mine.held(u));
+  for (int i = 0; i < C::kWaves; ++i) any_wide |= s_wide[i] != 0;
+  // (the same in every wave, since there are barriers in it)
+  auto attend = [&](auto far) {
+    constexpr bool FAR = decltype(far)::value;
+    uint8_t *now = s_kv, *next = s_kv + C::kTileBytes;
+    if constexpr (!C::kOverlap) {
+      // While tile i is multiplied, tile i + 1 is on its way from memory; then it
+      // is decoded into the other buffer, which was last read before the barrier
+      // of the turn before.  (Past the end: what the registers hold, never used.)
+      for (int tile = first; tile < end; tile += C::kUnits) {
+#pragma unroll
+        for (int n = 0; n < C::kUnits; ++n) {
+          const int u = tile + n;
+          if (active && u < end)
+            z.template attend<true, FAR>(Staged<D>{now + n * Staged<D>::kBytes + lane * 16}, u * 32, mine.held(u));
+        }
+        store(next);
+        load(tile + 2 * C::kUnits);
+        __syncthreads();
+        uint8_t* const done = now;
+        now = next;
+        next = done;
       }
-      store(next);
-      load(tile + 2 * C::kUnits);
-      __syncthreads();
-      uint8_t* const done = now;
-      now = next;
-      next = done;
-    }
-  } else {
-    // A tile is one unit.  While unit i is added up, the logits of unit i + 1 are
-    // made.  Of three buffers, a turn writes that of unit i + 1, last read (as
-    // values) two turns before: before the barrier of the turn before.
-    static_assert(!C::kOverlap || C::kUnits == 1, "one unit");
-    uint8_t* spare = s_kv + 2 * C::kTileBytes;
-    f32x4_t y[C::R][2];
-    if (active && first < end) {
-      f32x4_t s[C::R][2];
-      const bool held = mine.held(first);
-      z.logits(Staged<D>{now + lane * 16}, s);
-      if (!z.whole(first * 32, held)) z.mask(s, first * 32, held);
-      if (z.exponents(s, y)) z.raise(s, y);
-    }
-    for (int u = first; u < end; ++u) {
-      store(next);
-      load(u + 2);
-      __syncthreads();
-      if (active) {
-        const bool held = u + 1 < end && mine.held(u + 1);  // past the end: what lies there is masked
-        f16x8_t pr[C::R];
+    } else {
+      // A tile is one unit.  While unit i is added up, the logits of unit i + 1 are
+      // made.  Of three buffers, a turn writes that of unit i + 1, last read (as
+      // values) two turns before: before the barrier of the turn before.
+      static_assert(!C::kOverlap || C::kUnits == 1, "one unit");
+      uint8_t* spare = s_kv + 2 * C::kTileBytes;
+      f32x4_t y[C::R][2];
+      if (active && first < end) {
         f32x4_t s[C::R][2];
-        z.probabilities(y, pr);
-        z.logits(Staged<D>{next + lane * 16}, s);
-        z.add(Staged<D>{now + lane * 16}, pr);
-        if (!z.whole(u * 32 + 32, held)) z.mask(s, u * 32 + 32, held);
+        const bool held = mine.held(first);
+        z.template logits<FAR>(Staged<D>{now + lane * 16}, s);
+        if (!z.whole(first * 32, held)) z.mask(s, first * 32, held);
         if (z.exponents(s, y)) z.raise(s, y);
       }
-      uint8_t* const done = now;
-      now = next;
-      next = spare;
-      spare = done;
+      for (int u = first; u < end; ++u) {
+        store(next);
+        load(u + 2);
+        __syncthreads();
+        if (active) {
+          const bool held = u + 1 < end && mine.held(u + 1);  // past the end: what lies there is masked
+          f16x8_t pr[C::R];
+          f32x4_t s[C::R][2];
+          z.probabilities(y, pr);
+          z.template logits<FAR>(Staged<D>{next + lane * 16}, s);
+          z.add(Staged<D>{now + lane * 16}, pr);
+          if (!z.whole(u * 32 + 32, held)) z.mask(s, u * 32 + 32, held);
+          if (z.exponents(s, y)) z.raise(s, y);
+        }
+        uint8_t* const done = now;
+        now = next;
+        next = spare;
+        spare = done;
+      }
     }
-  }
+  };
+  if (__builtin_expect(any_wide, 0))
+    attend(std::true_type{});
+  else
+    attend(std::false_type{});
 
   z.finish();
   const int64_t slot = (int64_t)blockIdx.x * ROWS + wave * 16 * C::R;

@@ -31,6 +31,7 @@
 
 namespace nvfp4 {
 
+typedef __attribute__((ext_vector_type(2))) uint16_t u16x2_t;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;  // MFMA A/B operand
 

@@ -74,6 +74,50 @@ def test_queries_that_are_not_finite_over_a_split_context(d):
     check_attention(s, [1, 1], q, torch.where(at[..., None], want, out), torch.where(at, want_lse, lse), d ** -0.5)
 
 
+# ------------------------------------------------------ queries of many sizes
+
+
+@EVERY_PATH
+@pytest.mark.parametrize("spread", [20, 32, 33, 37, 40, 60, 150])
+def test_queries_of_very_different_sizes(d, rows, spread):
+    """Elements 2^-spread of the row's largest decide the softmax where the keys are zero at the larger ones: nothing
+    of a finite query may be lost to a number format shared by the row.  Rows of ordinary queries lie between."""
+    lens, new = [150, 700], [40, 33]
+    pages = _table_for(rows, lens, new, 3, 1, d, 32, 0)
+    print("kv attention spread queries", d, rows, spread, flush=True)
+    s = Sequences(35, lens, 1, d, 32, table_pages=pages)
+    for k in s.k:
+        k[:, :, 16:32] = 0.0
+    s.append()
+    q = queries(36, sum(new), 3, d)
+    large = q[:, :, 16:32].clone()
+    q[:, :, 16:32] = 0.0
+    wide = torch.arange(sum(new)) % 4 != 1
+    # the largest at 2^(spread / 2) and the rest at 2^(-spread / 2), which scale makes up for; other rows: at the rest's size
+    down = 2.0 ** -(spread // 2)
+    q = (q.float() * down).bfloat16()
+    q[:, :, 16:32] = torch.where(wide[:, None, None], large.float() * 2.0 ** (spread - spread // 2), large.float() * down).bfloat16()
+    scale = d ** -0.5 / down
+    out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, starts(new), scale=scale, return_lse=True)
+    check_attention(s, new, q, out, lse, scale)
+
+
+def test_one_small_query_element_beside_a_large_one():
+    """q = (2^24, 1.4453125 * 2^-12, 0, ..) and a key that is 0 in the first element and 2688 in the second: 0.948."""
+    d = 128
+    cache = nv.KVCache.empty(1, 32, 1, d)
+    k = torch.zeros(2, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[0, 0, 1] = 2688.0
+    nv.kv_append(cache, k, torch.ones_like(k), torch.arange(2, dtype=torch.int32, device="cuda"))
+    assert float(nv.kv_read(cache, torch.zeros(1, dtype=torch.int32, device="cuda"))[0][0, 0, 1]) == 2688.0
+    q = torch.zeros(1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 0], q[0, 0, 1] = 2.0 ** 24, 1.4453125 * 2.0 ** -12
+    i32 = dict(dtype=torch.int32, device="cuda")
+    _, lse = nv.kv_attention(q, cache, torch.zeros(1, 1, **i32), torch.tensor([2], **i32), scale=1.0, return_lse=True)
+    want = np.log(1.0 + np.exp(2688.0 * 1.4453125 * 2.0 ** -12))
+    assert abs(float(lse[0, 0]) - want) <= 2.0 ** -15  # as in kv_cases.bounds
+
+
 # ------------------------------------------------------------ factors
 
 
