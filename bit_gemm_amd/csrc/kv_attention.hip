@@ -366,6 +366,7 @@ struct Rows {
     const int rows = seq.count * a.group;
     // in 64 bits: neither it nor its product with a row's power of two may lose bits below fp32's range
     const double base = (double)a.scale * 1.44269504088896340736 * (double)a.k_scale[head];
+    const int large = (__double2hiint(base) >> 20 & 0x7FF) - 1023;  // floor(log2(|base|))
     const uint16_t* src[R];
     int e[R];
     bool far = false;
@@ -399,7 +400,8 @@ struct Rows {
       // 2^e, e = 14 - floor(log2(top)) as far as fp32 goes; an element's 8 bits must not pass below fp16's 2^-24 then
       const int exponent = top >> 7;
       e[r] = exponent == 255 ? kPoisoned : min(14 + 127 - exponent, 126);
-      far |= exponent != 255 && ((low + 1) >> 7) - 127 + e[r] - 7 < -24;
+      // (and the factor base 2^-e not past fp32's largest)
+      far |= exponent != 255 && (((low + 1) >> 7) - 127 + e[r] - 7 < -24 || large - e[r] > 126);
     }
     auto fill = [&](auto wide_) {
       constexpr bool WIDE = decltype(wide_)::value;
@@ -412,7 +414,7 @@ struct Rows {
         const float up = __uint_as_float((uint32_t)(127 + power) << 23);
         factor[r] = (float)(base * (double)__uint_as_float((uint32_t)(127 - power) << 23));
         const float sign = poisoned ? __builtin_nanf("") : factor[r] < 0.0f ? -up : up;
-        factor[r] = fmaxf(fabsf(factor[r]), 1e-37f);
+        factor[r] = fminf(fmaxf(fabsf(factor[r]), 1e-37f), 3.4e38f);  // (never 0 or infinite: nor is its product with 0 or -inf NaN)
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           float x[8 * N];

@@ -142,3 +142,47 @@ def test_value_scales_next_to_the_least(d, rows, power):
     # each side rounded to bf16 once, the quotients of fp32 before; subnormal results to steps of 2^-133
     assert ((out.double() - exact).abs() <= 2.0 ** -7 * (1 + 2.0 ** -8) * exact.abs() + 2.0 ** -133).all()
     assert (out != 0).any()
+
+
+def test_a_factor_past_fp32():
+    """scale * k_scale / the row's power of two passes fp32's largest number: tokens whose logit is 0 share the row,
+    those far below it are not seen."""
+    for d, tokens in ((64, 1), (128, 1), (128, 40), (256, 1)):
+        n = 100
+        k = torch.zeros(n, 1, d, dtype=torch.bfloat16)
+        k[:, 0, 5] = -6.0
+        k[[7, 33], 0, 5] = 0.0
+        v = torch.zeros(n, 1, d, dtype=torch.bfloat16)
+        v[7], v[33] = 6.0, 3.0
+        cache = nv.KVCache.empty(4, 32, 1, d)
+        nv.kv_append(cache, k.cuda(), v.cuda(), torch.arange(n, dtype=torch.int32, device="cuda"))
+        q = torch.zeros(tokens, 2, d, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 5] = 2.0 ** 100
+        table = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+        out, lse = nv.kv_attention(q, cache, table, torch.tensor([n], dtype=torch.int32, device="cuda"), starts([tokens]),
+                                   scale=1e20, return_lse=True)
+        assert (out == 4.5).all(), d
+        assert ((lse - np.log(2.0)).abs() <= 2.0 ** -20).all(), d
+
+
+def test_finite_logits_under_a_factor_past_fp32():
+    """As above, with finite logits: of elements 2^-30 of the row's largest, at which the keys are 0."""
+    for d, tokens in ((64, 1), (128, 1), (128, 40), (256, 1)):
+        k = torch.zeros(40, 1, d, dtype=torch.bfloat16)
+        k[:, 0, 17] = 3.0
+        k[9, 0, 17] = 6.0
+        v = torch.zeros(40, 1, d, dtype=torch.bfloat16)
+        v[9] = 5.0  # (the nearest codes: 4 and 6, times the block's scale 5 / 6 rounded to 0.8125)
+        cache = nv.KVCache.empty(2, 32, 1, d)
+        slots = torch.arange(40, dtype=torch.int32, device="cuda")
+        nv.kv_append(cache, k.cuda(), v.cuda(), slots)
+        held_k, held_v = nv.kv_read(cache, slots, torch.float32)
+        q = torch.zeros(tokens, 2, d, dtype=torch.bfloat16, device="cuda")
+        q[:, :, 5], q[:, :, 17] = 2.0 ** 100, 2.0 ** 70
+        table = torch.arange(2, dtype=torch.int32, device="cuda")[None]
+        out, lse = nv.kv_attention(q, cache, table, torch.tensor([40], dtype=torch.int32, device="cuda"), starts([tokens]),
+                                   scale=2.0 ** 45, return_lse=True, causal=False)
+        want = float(held_k[9, 0, 17]) * 2.0 ** 115
+        # the logit's factors and the return to natural logarithms are each rounded in fp32 (2^-24), five times at most
+        assert ((lse.double() - want).abs() <= 5 * 2.0 ** -24 * want).all(), d
+        assert torch.equal(out, held_v[9].bfloat16().expand_as(out)), d
