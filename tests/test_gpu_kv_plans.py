@@ -1,6 +1,7 @@
 """kv_attention in every form that a plan can give it, under every mask: windows
 on whole and on split contexts, split contexts that every token sees, both forms
-of the join, more sequences than a wave has lanes."""
+of the join, more sequences than a wave has lanes; and rows of tokens whose
+offsets pass 32 bits."""
 
 import numpy as np
 import pytest
@@ -8,7 +9,7 @@ import torch
 
 import bit_gemm_amd as nv
 import oracle.kv as okv
-from kv_cases import Sequences, bounds, check_attention, queries, starts
+from kv_cases import Sequences, bounds, check_attention, heads, queries, rope_table, starts
 from kv_plan_cases import CALLS, check_plan
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,31 @@ def test_single_tokens_named_by_their_rows(d, lens, hq, hkv, window):
     for first in (None, starts([1] * len(lens))):
         out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, first, window=window, return_lse=True)
         check_attention(s, [1] * len(lens), q, out, lse, d ** -0.5, True, window)
+
+
+def test_rows_of_tokens_past_32_bits():
+    """Tokens 2^30 elements and more apart: q, k, v and the rotated q as columns of one matrix of 4.3 GB, whose last
+    row's offset passes 2^31 elements and 2^32 bytes."""
+    n, hq, hkv, d = 3, 4, 2, 128
+    width = 2 * hq + 2 * hkv  # q, k, v, q_out
+    stride = (1 << 30) + 64
+    flat = torch.empty((n - 1) * stride + width * d, dtype=torch.bfloat16, device="cuda")
+    far = flat.as_strided((n, width, d), (stride, d, 1))
+    assert (n - 1) * stride > 2 ** 31
+    near = heads(np.random.default_rng(1), n, width, d).cuda()
+    far.copy_(near)
+    near, far = ([*x.split((hq, hkv, hkv, hq), 1)] for x in (near, far))
+    rope = torch.from_numpy(rope_table(8, d)).cuda()
+    slots = torch.tensor([5, 40, 70], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([96], dtype=torch.int32, device="cuda")
+    table = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    results = []
+    for q, k, v, q_out in (near, far):
+        cache = nv.KVCache.empty(3, 32, hkv, d, k_scale=0.01, v_scale=0.01)
+        cache.data.zero_()
+        nv.kv_append(cache, k, v, slots, q=q, q_out=q_out, positions=slots.remainder(8), rope=rope)
+        out, lse = nv.kv_attention(q_out, cache, table, lens, starts([n]), return_lse=True)
+        results.append((q_out.clone(), cache.data.clone(), out, lse))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert not torch.equal(results[0][0], near[0].contiguous())
