@@ -924,8 +924,8 @@ class KVCache:
     @staticmethod
     def empty(pages: int, page_size: int, heads: int, head_dim: int, device="cuda", k_scale=None,
               v_scale=None) -> "KVCache":
-        """An uninitialised cache.  k_scale, v_scale: a number, a float32 [heads] tensor, or None for 1 (magnitudes
-        from 2^-8 to 2688; below, blocks round to zero)."""
+        """An uninitialised cache.  k_scale, v_scale: a number, a float32 [heads] tensor, or None for 1: magnitudes
+        up to 2688; a block whose largest is 6 * 2^-10 or less becomes zero, as its own scale is then rounded to 0."""
         n = kv_page_bytes(heads, head_dim, page_size)
         if n == 0:
             raise ValueError(f"no cache of {heads} heads of {head_dim} in pages of {page_size} tokens")

@@ -15,7 +15,7 @@
 //       the largest element is brought to [2^60, 2^61): exact down to 2^-186.
 //   p = 2^(y - m), y = S^T * scale * S * log2(e) and m a bound 7 below a
 //       running maximum that is raised only when some y passes m by 15: p stays
-//       below 2^15 and is rounded to fp16 to within 2^-12 relative or 2^-32 of
+//       below 2^15 and is rounded to fp16 to within 2^-11 relative or 2^-32 of
 //       the row's largest.  The row's sum adds the p before their rounding.
 //   O^T += V^T P^T: a lane's results of S^T are its operand of P^T (kv_device.h).
 //
