@@ -1089,7 +1089,10 @@ def kv_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_l
     only its last `window` tokens.  Returns out, bf16 like q, or with
     return_lse (or lse) also the float32 [tokens, q_heads] logarithms of the
     softmax's sums.  Rows that see nothing are 0 and -inf; rows behind the
-    last sequence are left as they were in out and lse.  workspace: uint8 of
+    last sequence are left as they were in out and lse, and a row of q that is
+    not finite is NaN.  The width of page_table is taken for the length of every
+    context when the kernel is chosen: a table no wider than the longest context
+    is faster for short prompts (see include/nvfp4.h).  workspace: uint8 of
     kv_attention_workspace_size bytes, a new one by default; calls that may run
     at once need one each."""
     pages, heads, index = _kv_cache(cache)

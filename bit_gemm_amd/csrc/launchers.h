@@ -245,7 +245,8 @@ struct KvAttend {
 // query head; tiles 0: the blocks of k_kv_tiles), at most `blocks` of them for
 // each head, `waves` to a workgroup where tiles is not 0, and up to `parts`
 // more work items for each head from splitting long contexts (0: none is
-// split).  capacity: tokens of the longest context.
+// split).  capacity: tokens that the page table holds for a sequence, which the
+// plan takes for the length of every context (the lengths are on the device).
 struct KvPlan {
   int tiles, waves, parts;
   int64_t blocks;

@@ -619,6 +619,15 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  *            fp32 [tokens, q_heads] or NULL.
  * workspace  >= nvfp4_kv_attention_workspace_size bytes, 16-byte aligned (0
  *            bytes for short contexts: NULL allowed, one launch); one_each: q_starts is NULL.
+ * The kernel, the splitting and the workspace are chosen on the host from the
+ * sizes, with table_pages * page_size (or the window) as the length of every
+ * context: a table much wider than the contexts gives the same results (up to
+ * the order of the sums), but the choice for more work than there is.  A prompt
+ * of 1000 tokens of 32 heads on 8 of 128 takes 30 us under a table of its own
+ * length, 55 and 77 MB of workspace under one of 131072 tokens; 300 tokens 9.4
+ * and 23; one token on each of 16 contexts of 300 7.3 and 10; one token on 4096
+ * 11.4 and 11.6.  A caller that knows a bound on the lengths passes a table no
+ * wider than that.
  * Logits and the softmax's sums are fp32 (a logit below -2e38 counts as not
  * seen); the products are exact in their operands (of q down to 2^-186 of a
  * row's largest element) but for p, rounded to fp16 (11 bits).  Lengths are read
