@@ -666,10 +666,10 @@ struct RowOut {
 // A workgroup takes 16 R rows and a part of their context; its waves take the
 // part's units in turn, decode them in registers and add up at the end.  Bound
 // by HBM where the context is long: one token on 131072 of 8 heads (151 MB) is
-// read in 32.6 us, 4.6 TB/s (a copy: 4.76); with few units by latency (lens,
-// page numbers, the first unit, the sums: about 7 us).  With more rows the
+// read in 31.9 us, 4.7 TB/s (a copy: 4.76); with few units by latency (lens,
+// page numbers, queries, the first unit, the sums: about 6 us beside the launch).  With more rows the
 // decoding bounds it, 64 conversions and as many products a unit: 4096 tokens,
-// 32 heads in groups of 4, take 252 us with R = 1, 192 with 2.
+// 32 heads in groups of 4, take 260 us with R = 1, 203 with 2.
 template <int D, int R, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void k_kv_rows(KvAttend a, int parts, int least, float* __restrict__ partial,
                                                            float2* __restrict__ stats) {
@@ -837,7 +837,7 @@ struct Share {
 // Many rows: 16 R for each of 8 waves, which decode tiles of kUnits units
 // together into LDS operands, a share of a unit each, so that a unit is decoded
 // once for 256 (128) rows.  Two waves to a SIMD: 200 registers at R = 2, and
-// with R = 1 and four waves LDS is read twice as often (the same prompt 166 us).
+// with R = 1 and four waves LDS is read twice as often (166 us when this took 157).
 // 4096 tokens, 32 heads in groups of 4: 147 us, 0.94 PFLOP/s; 16384: 2.0 ms, 1.1
 // (the library's fp16 8192^3 product 1.15).  The matrix cores work a third of
 // the time, the vector units half; the rest is waiting, mostly for LDS.
@@ -850,7 +850,7 @@ struct Tiles {
   // Head_dim 256 has no registers to ask for a unit's values before its softmax.
   // There the logits of a unit are made while the one before is added up (which
   // reads a tile ahead and takes a third buffer): 4096 tokens of 16 heads in
-  // groups of 4 take 169 us, unit by unit 181.  Head_dim 128, 32 heads: 150 and,
+  // groups of 4 take 171 us, unit by unit 180.  Head_dim 128, 32 heads: 150 and,
   // unit by unit with the values asked for, 145 (147
   // since bounds far out are looked for).
   static constexpr bool kOverlap = D == 256;
@@ -1120,13 +1120,15 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   if (window > 0) units = std::min(units, (window + 31) / 32 + 2);
   // Blocks of 32 rows times the units that each may see.  Work enough to fill
   // the GPU with fewer, larger workgroups takes them.  1000 tokens of 32 heads
-  // in groups of 4, head_dim 128: 29 us with blocks of 16 rows, 35 with 32, 52
-  // in tiles; 2000: 75, 62, 73; 4096: 252, 192, 157.  8 tokens of each of 16
-  // contexts of 8192: 61, 46, 132.  Head_dim 64 has no tiles: 4000 tokens of 16
-  // heads 78, 59, 106 us, 16000 of 32 1017, 723, 809.  Head_dim 256 has no room
-  // for 32 rows: 1500 tokens of 16 heads in groups of 4 take 48 us with 16
-  // rows, 73 in tiles, 4096 tokens 242 and 177; 16 tokens of each of 8 contexts
-  // of 8192 80 and 102, 32 tokens 181 and 130.
+  // in groups of 4, head_dim 128: 30 us with blocks of 16 rows, 28 with 32, 38
+  // in tiles; 2000: 77, 65, 68; 2500: 111, 91, 82; 4096: 260, 203, 152 (the
+  // kernels cross a little before the lines drawn below).  8 tokens of each of
+  // 16 contexts of 8192: 53, 52, 151.  Head_dim 64 has no tiles: 4000 tokens of
+  // 16 heads 80 and 63 us, 16000 of 16 in groups of 2 1035 and 741, of 32 2071
+  // and 1484.  Head_dim 256 has no room for 32 rows: 1500 tokens of 16 heads in
+  // groups of 4 take 50 us with 16 rows, 62 in tiles, 2000 76 and 78, 4096 248
+  // and 173; of 32 heads in groups of 4, 16 tokens of each of 8 contexts of 8192
+  // 83 and 100, 32 tokens 133 and 125.
   const double work = (double)block_count(sequences, tokens, group, 32, one_each) * (double)heads * (double)units;
   const int64_t mean = (tokens * group + sequences - 1) / sequences;  // rows of a sequence
   if (mean >= 128 && ((head_dim == 256 && work >= 65536.0) || (head_dim == 128 && work >= 262144.0)))
@@ -1136,25 +1138,25 @@ KvPlan plan_kv_attention(int64_t sequences, int64_t tokens, int64_t q_heads, int
   const int rows = kv_block_rows(p, head_dim);
   p.blocks = block_count(sequences, tokens, group, rows, one_each);
   // The second launch takes 4 to 6 us, what a workgroup needs for 32 units.  One
-  // sequence of 1024 tokens of 8 heads: 9.2 us whole, 9.6 split; of 2048 13.0,
-  // 10.9; 8 of 2048 14.7, 14.2; 12 15.1, 16.6; 20 16.7, 20.3; 4 heads of 256, 16
-  // of 2048 22.1, 18.8, 24 25.0, 24.9.  Past 64 units as long as workgroups
-  // are few: 40 sequences of 1 to 4096 tokens of 8 heads 48, 31; 64 51, 42; 80
-  // 55, 53 (all of 4096: 76, 86); 100 61, 69.  A table of more than 8192 tokens
+  // sequence of 1024 tokens of 8 heads: 9.1 us whole, 10.9 split; of 2048 13.1,
+  // 11.0; 8 of 2048 14.7, 14.0; 12 14.8, 16.4; 20 16.2, 19.7; 4 heads of 256, 16
+  // of 2048 22.4, 18.4, 24 25.2, 25.0.  Past 64 units as long as workgroups
+  // are few: 40 sequences of 1 to 4096 tokens of 8 heads 47, 30; 64 49, 40; 80
+  // 54, 52 (all of 4096: 76, 81); 100 60, 66.  A table of more than 8192 tokens
   // may hold one context far longer than the rest, which a workgroup alone would
-  // take long for: split up to 1024 (100 of 1 to 8192 114 us whole, 123).
+  // take long for: split up to 1024 (100 of 1 to 8192 110 us whole, 116).
   const int64_t items = p.blocks * heads;
   const bool split =
       units > (items < (head_dim == 256 ? 96 : 64) ? 32 : 64) && items < (!p.tiles ? 256 : units > 256 ? 1024 : 640);
   // Long contexts that are not split, on a GPU that is not full: eight waves to
-  // a workgroup.  24 sequences with windows of 1024: 10.4 us with 4, 9.3; 32 of
-  // 2048 22.5, 20; but 8 of 300 tokens 5.5, 5.9.
+  // a workgroup.  24 sequences with windows of 1024: 10.5 us with 4, 9.2; 32 of
+  // 2048 21.7, 19.9; but 8 of 300 tokens 6.6, 6.9.
   p.waves = p.tiles == 1 && !split && items <= 512 && units > 16 ? 8 : 4;
   // As many work items as the GPU holds workgroups (three to a CU; of k_kv_tiles
   // one, but two rounds even out) if every block's last part counts half.  16
-  // ragged contexts: 24.8 us with 512 parts beside the blocks, 22.8; 8 of 9000
-  // to 15300, head_dim 64, 38.6, 32.2; 8 with 1 to 700 new tokens, head_dim 256
-  // (tiles), 146, 137.
+  // ragged contexts: 23.7 us with 512 parts beside the blocks, 21.9; 8 of 9000
+  // to 15300, head_dim 64, 36.5, 31.6; 8 with 1 to 700 new tokens, head_dim 256
+  // (tiles, 768 beside the blocks), 164, 140.
   const int64_t parts = std::max<int64_t>(1, (p.tiles ? 768 : 512) - items / 2);
   p.parts = split ? (int)((parts + heads - 1) / heads) : 0;
   p.ws_bytes = split ? (size_t)(p.blocks + p.parts) * heads * rows * (head_dim + 2) * sizeof(float) : 0;
