@@ -634,9 +634,10 @@ struct RowOut {
     to = a.out + at * D;
     lse = a.lse ? a.lse + at : nullptr;
     const float scale = a.v_scale[head];
-    const bool small = scale < 0x1p-40f;
+    const bool small = fabsf(scale) < 0x1p-40f;
     drop = small ? 0x1p-100f : 1.0f;
-    f = l == 0.0f ? 0.0f : (small ? scale * 0x1p100f : scale) / l;  // l is 0 where nothing is visible, and NaN where a visible token is
+    // l is 0 where nothing is visible, and NaN where a visible token is
+    f = l == 0.0f ? 0.0f : (small ? scale * 0x1p100f : scale) / l;
   }
   // Elements [d, d + E).
   template <int E>
