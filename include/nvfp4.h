@@ -632,7 +632,8 @@ NVFP4_API int nvfp4_kv_read(const uint8_t* cache, int64_t pages, int64_t page_si
  * seen); the products are exact in their operands (of q down to 2^-186 of a
  * row's largest element) but for p, rounded to fp16 (11 bits).  Lengths are read
  * on the device alone: a captured call follows them.  The order of the sums is
- * fixed for given sizes and lengths.
+ * fixed for given sizes and lengths; rows that are computed together round their
+ * logits alike, so a row's last bits may depend on the values of its neighbours.
  */
 NVFP4_API size_t nvfp4_kv_attention_workspace_size(int64_t sequences, int64_t tokens, int64_t q_heads, int64_t heads,
                                                    int64_t head_dim, int64_t page_size, int64_t table_pages,

@@ -102,6 +102,23 @@ def test_queries_of_very_different_sizes(d, rows, spread):
     check_attention(s, new, q, out, lse, scale)
 
 
+@EVERY_PATH
+def test_one_row_of_very_different_sizes_among_ordinary_ones(d, rows):
+    """One row in another wave (and most workgroups) than the rest: both kinds of operands in one call."""
+    lens, new = [400, 900], [300, 130]
+    pages = _table_for(rows, lens, new, 3, 1, d, 32, 0)
+    print("kv attention one spread row", d, rows, flush=True)
+    s = Sequences(39, lens, 1, d, 32, table_pages=pages)
+    for k in s.k:
+        k[:, :, 16:32] = 0.0
+    s.append()
+    q = queries(40, sum(new), 3, d)
+    for t, h in ((71, 1), (250, 0), (429, 2)):
+        q[t, h, 16:32] = (q[t, h, 16:32].float() * 2.0 ** 45).bfloat16()
+    out, lse = nv.kv_attention(q.cuda(), s.cache, s.table, s.kv_lens, starts(new), return_lse=True)
+    check_attention(s, new, q, out, lse, d ** -0.5)
+
+
 def test_one_small_query_element_beside_a_large_one():
     """q = (2^24, 1.4453125 * 2^-12, 0, ..) and a key that is 0 in the first element and 2688 in the second: 0.948."""
     d = 128
